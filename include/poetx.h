@@ -32,7 +32,8 @@
  * Errors
  *   Every call returns a poetx_status and never aborts. Arguments are checked on
  *   the host before any launch; nothing is launched on error. Device pointers
- *   must be 16-byte aligned. Permutation arrays must hold permutations; this is
+ *   must be 16-byte aligned, but for the calls "around the linears" below, which
+ *   take row strides and pointers aligned to their elements. Permutation arrays must hold permutations; this is
  *   the caller's guarantee and is not checked on the device.
  */
 #ifndef POETX_H
@@ -56,7 +57,9 @@ typedef enum {
   POETX_ERR_WORKSPACE = 7     /* workspace NULL or smaller than required      */
 } poetx_status;
 
-typedef enum { POETX_FP32 = 0, POETX_BF16 = 1 } poetx_dtype;
+/* POETX_INT8 is a type of rows with one fp32 scale each, value = scale * q; it
+ * stands where poetx_add_rms_norm and poetx_linear name it, and never in a plan. */
+typedef enum { POETX_FP32 = 0, POETX_BF16 = 1, POETX_INT8 = 2 } poetx_dtype;
 
 /* Storage of the pre-merged frozen weight Wt that forward, backward and merge read.
  *   POETX_WEIGHT_DENSE:     [m, n] in the plan dtype (poetx_permute_weight).
@@ -365,6 +368,100 @@ poetx_status poetx_gather_cols(const poetx_plan* plan, int64_t T, int32_t dim, c
                                const int32_t* idx, void* out, void* stream);
 poetx_status poetx_scatter_cols(const poetx_plan* plan, int64_t T, int32_t dim, const void* in,
                                 const int32_t* idx, void* out, void* stream);
+
+/* ------------------------------------------------------ around the linears
+ * What a block does next to its linears: the residual's addition and the norm in
+ * front of them, the product with a merged weight in their place when nothing is
+ * trained, and the clipping of all gradients behind them. These calls need no
+ * plan. Matrices are row-major with a row stride (ld, in elements, at least the
+ * columns; of no account for a single row) and any alignment of their elements;
+ * pointers and strides that are multiples of 16 bytes are the fast ones. fp32
+ * arrays marked [..] are contiguous. An output may not overlap an input or
+ * another output, except where named. */
+
+/* Residual addition and root-mean-square norm:
+ *   h = round(x + r) (h = x without r),  s = (mean_j h_j^2 + eps)^(-1/2) as fp32,
+ *   y_j = (h_j s) w_j, sums in 64 bits, the rest in fp32, one rounding.
+ *   X [T, dim] (dtype)      R [T, dim] (dtype) or NULL
+ *   w fp32 [dim]            H [T, dim] (dtype) or NULL: h; may be X or R itself
+ *   Y [T, dim]: y_dtype = dtype: y. y_dtype = POETX_INT8: rows by the rule of
+ *     poetx_quantize_weight, a = max_j |y_j|, q_j = rint(y_j (127 / a)) and
+ *     scale = a / 127. A row with a < 2^-119 is zero (q = 0, scale = 0); one that
+ *     is not finite has q = 0 and scale NaN, so every value it stands for is NaN.
+ *   scale fp32 [T] (POETX_INT8 only, else NULL)
+ *   rstd fp32 [T] or NULL: s, for the backward.
+ * T = 0 is a no-op. No row is touched behind the T-th. */
+typedef struct {
+  int64_t T;
+  int32_t dim;
+  int32_t dtype;            /* POETX_FP32 or POETX_BF16                       */
+  int32_t y_dtype;          /* dtype, or POETX_INT8                           */
+  int64_t ld_x, ld_r, ld_h, ld_y;
+  double eps;               /* finite, >= 0                                   */
+} poetx_norm_desc;
+poetx_status poetx_add_rms_norm(const poetx_norm_desc* desc, const void* X, const void* R, const float* w,
+                                void* H, void* Y, float* scale, float* rstd, void* stream);
+
+/* Backward of poetx_add_rms_norm (y_dtype = dtype) from G = dL/dY and G_H, the
+ * gradient that reaches h through the residual stream:
+ *   c = s^2 mean_j(g_j w_j h_j),  dx = dr = round(gh + s (g w - h c)),
+ *   g_w[j] = sum_t g_tj h_tj s_t (overwritten)
+ *   G [T, dim]    G_H [T, dim] or NULL    H [T, dim]: h (X where there was no r)
+ *   w fp32 [dim]  rstd fp32 [T]           G_X [T, dim]: dx; may be G or G_H itself
+ *   g_w fp32 [dim]                        ws poetx_rms_norm_backward_workspace bytes
+ * Deterministic: sums run in a fixed order. T = 0 writes zero g_w. */
+typedef struct {
+  int64_t T;
+  int32_t dim;
+  int32_t dtype;
+  int64_t ld_g, ld_gh, ld_h, ld_gx;
+} poetx_norm_backward_desc;
+size_t poetx_rms_norm_backward_workspace(int64_t T, int32_t dim);   /* 0 for bad sizes */
+poetx_status poetx_rms_norm_backward(const poetx_norm_backward_desc* desc, const void* G, const void* G_H,
+                                     const void* H, const float* w, const float* rstd, void* G_X,
+                                     float* g_w, void* ws, size_t ws_bytes, void* stream);
+
+/* Product with a weight that is not trained (W_out of poetx_merge_weight, or the
+ * INT8 rows of poetx_quantize_weight) and its epilogue:
+ *   Y = round(act(X W^T + bias) * mul + res), sums and epilogue in fp32.
+ *   X [T, n], W [m, n] (dtype)   Y [T, m] (y_dtype)   bias fp32 [m] or NULL
+ *   mul, res [T, m] (y_dtype) or NULL; Y may be mul or res itself
+ *   dtype = POETX_INT8: X and W are INT8 rows with scales sx fp32 [T] and
+ *     sw fp32 [m] (NULL otherwise): X W^T = (float(sum_j q_tj q_cj) sx_t) sw_c,
+ *     the sum exact in 32-bit integers; n <= 131071.
+ *   y_dtype: POETX_FP32 always; POETX_BF16 with dtype POETX_BF16 or POETX_INT8.
+ * The order of a sum depends on the sizes and strides alone. T = 0 is a no-op. */
+typedef enum {
+  POETX_ACT_NONE = 0,
+  POETX_ACT_RELU = 1,
+  POETX_ACT_SILU = 2,       /* z / (1 + exp(-z))                               */
+  POETX_ACT_GELU = 3,       /* z (1 + erf(z / sqrt 2)) / 2                     */
+  POETX_ACT_GELU_TANH = 4   /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+} poetx_act;
+typedef struct {
+  int64_t T;
+  int32_t m, n;
+  int32_t dtype, y_dtype;
+  int32_t act;              /* poetx_act                                       */
+  int64_t ld_x, ld_w, ld_y, ld_mul, ld_res;
+} poetx_linear_desc;
+poetx_status poetx_linear(const poetx_linear_desc* desc, const void* X, const void* W, const float* sx,
+                          const float* sw, const float* bias, const void* mul, const void* res, void* Y,
+                          void* stream);
+
+/* Global norm of count gradient tensors, and their clipping by it:
+ *   norm = sqrt(sum of all squares) (64-bit sums, norm_out rounded once),
+ *   c = min(1, max_norm / (norm + 1e-6)) as fp32,  out = round(c g).
+ * A NaN norm makes every output NaN; an infinite one makes c zero.
+ *   grads[i]: ns[i] >= 0 contiguous elements of dtypes[i] (POETX_FP32 or
+ *     POETX_BF16); outs[i] as many of the same type. outs[i] = grads[i] clips in
+ *     place; outs = NULL takes the norm only. No out may overlap another tensor.
+ *   norm_out fp32 [1] or NULL   ws poetx_clip_grads_workspace(count) bytes
+ * grads, ns, dtypes, outs are host arrays, read during the call. Deterministic. */
+size_t poetx_clip_grads_workspace(int32_t count);   /* 0 for count < 0 or above 2^20 */
+poetx_status poetx_clip_grads(int32_t count, const void* const* grads, const int64_t* ns,
+                              const int32_t* dtypes, void* const* outs, double max_norm, float* norm_out,
+                              void* ws, size_t ws_bytes, void* stream);
 
 /* Optional stage timing for benchmarks. Stage i is timed when bit i of `mask`
  * is set: every later call records a pair of HIP events on its own stream

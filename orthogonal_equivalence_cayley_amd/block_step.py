@@ -18,6 +18,7 @@ import numpy as np
 import torch
 
 from . import poetx as _px
+from .block_ops import clip_grads
 from .layer import PoetxLayer, build_many, param_grad_many
 
 # groups of layers with no data dependence between them inside a block
@@ -44,15 +45,20 @@ class BlockStep:
     theta_P, pi_R, pi_P, X and G_Y (host arrays); they are copied to the device
     once. backward=False runs build + forward only. The frozen weight is kept
     with its transpose by default ("dense_t"), so both of its products read it
-    K-contiguous."""
+    K-contiguous. clip_norm: the step ends by clipping the parameter gradients of
+    all layers, in place, to this global norm; self.grad_norm (fp32, one value)
+    holds the norm they had."""
 
     def __init__(self, layer_inputs, k: int, dtype: str = "bf16", *, backward: bool = True,
                  streams: int = 2, weight: str = "dense_t", cayley: str = "neumann",
                  fold: str = "none", index: str = "separate", series: str = "chain",
-                 xmem: bool = False):
+                 xmem: bool = False, clip_norm: Optional[float] = None):
         if streams not in (1, 2):
             raise ValueError("streams must be 1 or 2")
+        if clip_norm is not None and not backward:
+            raise ValueError("clip_norm needs the backward")
         self.k, self.dtype, self.backward, self.xmem = k, dtype, backward, xmem
+        self.clip_norm, self.grad_norm = clip_norm, None
         tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
         dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(tdt).cuda()
         self.names = [inp.spec.name for inp in layer_inputs]
@@ -117,6 +123,9 @@ class BlockStep:
             # parameterisation of all layers in one batched call
             self._run_groups([list(reversed(g)) for g in reversed(self.groups)], self._bwd, two)
             param_grad_many(self.layers, [b["g"] for b in self.bufs])
+            if self.clip_norm is not None:
+                g = [t for b in self.bufs for t in b["g"]]
+                self.grad_norm = clip_grads(g, self.clip_norm, out=g)
 
     # ------------------------------------------------------------------ results
     def outputs(self, li: int) -> dict:

@@ -1149,6 +1149,8 @@ poetx_status scratch_for_current_device(void** out) {
 
 }  // namespace
 
+void poetx::set_last_hip(hipError_t e) { g_last_hip = e; }
+
 extern "C" {
 
 const char* poetx_last_hip_error(void) {

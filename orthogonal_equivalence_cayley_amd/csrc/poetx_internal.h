@@ -233,4 +233,64 @@ struct TriBatch {
 hipError_t launch_unpack_batch(const TriBatch& tb, hipStream_t s);
 hipError_t launch_pack_batch(const TriBatch& tb, hipStream_t s);
 
+// ---------------------------------------------------------------- around the linears
+// The HIP error behind the calling thread's most recent POETX_ERR_HIP.
+void set_last_hip(hipError_t e);
+
+// Residual addition and root-mean-square norm (k_norm.hip); row strides in elements.
+struct NormArgs {
+  const void* X; const void* R; const float* w;
+  void* H; void* Y; float* scale; float* rstd;   // R, H, rstd may be null; scale with quant
+  long long T; int dim; int quant;               // quant: Y is INT8 rows
+  long long ldx, ldr, ldh, ldy;
+  double eps;
+};
+hipError_t launch_add_rms_norm(const NormArgs& a, int bf16, hipStream_t s);
+struct NormBackArgs {
+  const void* G; const void* GH; const void* H; const float* w; const float* rstd;   // GH may be null
+  void* GX; float* dw;
+  float* part;   // norm_backward_parts(T) x dim partial sums of dw
+  float* rowc;   // T values, for rows longer than kNormRegDim only
+  long long T; int dim;
+  long long ldg, ldgh, ldh, ldgx;
+};
+constexpr int kNormRegDim = 4096;   // rows up to this length stay in registers for every type
+int norm_backward_parts(long long T);
+hipError_t launch_rms_norm_backward(const NormBackArgs& a, int bf16, hipStream_t s);
+
+// Sum of squares and scaling of many tensors (k_clip.hip).
+struct ClipItem {
+  const void* g; void* out;
+  long long n;
+  int bf16;
+};
+struct ClipEntry {
+  const void* g; void* out;
+  long long n;
+  int chunk0;   // first chunk of the tensor in its launch
+  int bf16;
+};
+constexpr int kClipMax = 120;   // 32 bytes each: one launch's arguments stay below 4 KB
+struct ClipBatch {
+  int n;
+  ClipEntry e[kClipMax];
+};
+long long clip_parts(long long count);   // doubles of `part` for up to count tensors
+hipError_t launch_clip(const ClipItem* items, int count, double max_norm, double* part, float* norm_out,
+                       bool write, hipStream_t s);
+
+// Y = act(X W^T + bias) * mul + res (k_linear.hip); row strides in elements.
+enum LinearType { LINEAR_F32 = 0, LINEAR_BF16 = 1, LINEAR_I8 = 2 };
+struct LinearArgs {
+  const void* X; const void* W;
+  const float* sx; const float* sw;   // LINEAR_I8: scales of X's and of W's rows
+  const float* bias; const void* mul; const void* res;   // each may be null; mul and res in Y's type
+  void* Y;
+  long long T; int m, n;
+  long long ldx, ldw, ldy, ldm, ldr;
+  int act;       // poetx_act
+  int y_bf16;    // Y, mul and res are bf16 (else fp32)
+};
+hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s);
+
 }  // namespace poetx

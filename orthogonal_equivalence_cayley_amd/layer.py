@@ -41,6 +41,12 @@ def param_grad_many(layers, g_thetas=None):
     return out
 
 
+def _int8_views(buf: torch.Tensor, m: int, n: int):
+    """(q [m, n] int8, s [m] fp32) views of the buffer quantize_weight fills."""
+    off = (m * n + 255) // 256 * 256
+    return buf[:m * n].view(torch.int8).view(m, n), buf[off:off + 4 * m].view(torch.float32)
+
+
 class PoetxLayer:
     def __init__(self, m: int, n: int, bsz_R: Sequence[int], bsz_P: Sequence[int], k: int,
                  dtype: str = "bf16", device: str = "cuda", weight: str = "dense",
@@ -116,11 +122,7 @@ class PoetxLayer:
     def int8_weight(self):
         """(q [m, n] int8, s [m] fp32) views of an INT8 Wt (rows in permuted order)."""
         assert self.weight in ("int8", "int8_t")
-        mn = self.m * self.n
-        off = (mn + 255) // 256 * 256
-        q = self.Wt[:mn].view(torch.int8).view(self.m, self.n)
-        s = self.Wt[off:off + 4 * self.m].view(torch.float32)
-        return q, s
+        return _int8_views(self.Wt, self.m, self.n)
 
     def merge(self, W_out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """End of an inner loop: R W0 P in the original coordinates, from the
@@ -132,6 +134,24 @@ class PoetxLayer:
         self.plan.merge_weight(self.Wt, self.pi_R, self.pi_P, self.Q32[0], self.Q32[1], W_out,
                                ws, ws.numel())
         return W_out
+
+    def merged(self, bias: Optional[torch.Tensor] = None, weight: str = "dense") -> "MergedLinear":
+        """The layer for use without training, its blocks folded into the weight
+        (merge()): weight "dense" in the layer's dtype, or "int8", rows with a
+        scale each (bf16 layers, m and n multiples of 256)."""
+        from .block_ops import MergedLinear
+        if weight not in ("dense", "int8"):
+            raise ValueError("weight must be 'dense' or 'int8'")
+        W = self.merge()
+        if weight == "dense":
+            return MergedLinear(W, bias=bias)
+        plan = _px.Plan(self.m, self.n, self.plan.bsz_R, self.plan.bsz_P, self.k, _PX_DTYPE[self.dtype],
+                        _px.WEIGHT_INT8_ROWS)
+        buf = torch.empty(plan.weight_bytes(), dtype=torch.uint8, device=self.device)
+        same = [torch.arange(d, dtype=torch.int32, device=self.device) for d in (self.m, self.n)]
+        plan.quantize_weight(W, same[0], same[1], buf)
+        q, s = _int8_views(buf, self.m, self.n)
+        return MergedLinear(q, bias=bias, w_scale=s)
 
     def set_theta(self, theta_R: torch.Tensor, theta_P: torch.Tensor) -> None:
         self.theta = [theta_R.to(device=self.device, dtype=torch.float32).contiguous(),

@@ -25,6 +25,7 @@ POETX_ERR_WORKSPACE = 7
 
 POETX_FP32 = 0
 POETX_BF16 = 1
+POETX_INT8 = 2     # rows with a scale each: norm output, merged-weight product
 SIDE_R = 0
 SIDE_P = 1
 WS_BUILD = 0
@@ -50,6 +51,8 @@ INDEX_FUSED = 1
 SERIES_CHAIN = 0
 SERIES_PS = 1
 
+ACTS = ("none", "relu", "silu", "gelu", "gelu_tanh")   # poetx_act, by value
+
 EXPORTED = (
     "poetx_plan_create", "poetx_plan_destroy", "poetx_param_count", "poetx_block_elems",
     "poetx_workspace_size", "poetx_status_string", "poetx_last_hip_error", "poetx_permute_weight",
@@ -58,6 +61,8 @@ EXPORTED = (
     "poetx_backward_dq", "poetx_param_grad_batch", "poetx_gather_cols",
     "poetx_scatter_cols", "poetx_timing_enable", "poetx_timing_read", "poetx_timing_reset",
     "poetx_forward_noalloc", "poetx_forward_noalloc_max_bytes",
+    "poetx_add_rms_norm", "poetx_rms_norm_backward", "poetx_rms_norm_backward_workspace",
+    "poetx_linear", "poetx_clip_grads", "poetx_clip_grads_workspace",
 )
 
 STAGES = ("build", "gather", "block_fwd", "w0_fwd", "scatter", "dq", "block_bwd", "w0_bwd",
@@ -81,6 +86,32 @@ class Desc(ctypes.Structure):
         ("k", ctypes.c_int32), ("dtype", ctypes.c_int32), ("weight", ctypes.c_int32),
         ("cayley", ctypes.c_int32), ("fold", ctypes.c_int32), ("index", ctypes.c_int32),
         ("series", ctypes.c_int32),
+    ]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("ld_x", ctypes.c_int64), ("ld_r", ctypes.c_int64), ("ld_h", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64), ("eps", ctypes.c_double),
+    ]
+
+
+class NormBackwardDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("ld_g", ctypes.c_int64), ("ld_gh", ctypes.c_int64), ("ld_h", ctypes.c_int64),
+        ("ld_gx", ctypes.c_int64),
+    ]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("m", ctypes.c_int32), ("n", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+        ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+        ("ld_mul", ctypes.c_int64), ("ld_res", ctypes.c_int64),
     ]
 
 
@@ -122,6 +153,12 @@ def _load() -> ctypes.CDLL:
         "poetx_param_grad_batch": (st, [i32, vp, vp, vp, vp, vp, vp, vp, vp]),
         "poetx_gather_cols": (st, [vp, i64, i32, vp, vp, vp, vp]),
         "poetx_scatter_cols": (st, [vp, i64, i32, vp, vp, vp, vp]),
+        "poetx_add_rms_norm": (st, [ctypes.POINTER(NormDesc)] + [vp] * 8),
+        "poetx_rms_norm_backward": (st, [ctypes.POINTER(NormBackwardDesc)] + [vp] * 8 + [sz, vp]),
+        "poetx_rms_norm_backward_workspace": (sz, [i64, i32]),
+        "poetx_linear": (st, [ctypes.POINTER(LinearDesc)] + [vp] * 9),
+        "poetx_clip_grads": (st, [i32, vp, vp, vp, vp, ctypes.c_double, vp, vp, sz, vp]),
+        "poetx_clip_grads_workspace": (sz, [i32]),
         "poetx_timing_enable": (st, [ctypes.c_uint32]),
         "poetx_timing_read": (st, [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]),
         "poetx_timing_reset": (None, []),

@@ -97,7 +97,8 @@ def quant_ref(h, s, w):
 
 # one row and many, around every variant's longest row, and rows no register variant holds
 NORM_SIZES = [(1, 1), (3, 7), (5, 63), (2, 64), (4, 65), (1, 2048), (7, 512), (6, 513), (3, 1000), (9, 1024),
-              (4, 1365), (130, 2049), (5, 4096), (3, 4097), (2, 8200), (3, 16385), (2, 20001)]
+              (4, 1365), (130, 2049), (5, 4096), (3, 4097), (2, 8200), (3, 16385), (2, 20001),
+              (1030, 65), (1100, 1000), (1024, 512)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -202,7 +203,7 @@ def test_norm_backward(T, dim, dt):
     s = (1 / (h.double().square().mean(1) + 1e-6).sqrt()).float()
     # the dot product's additions in a row: at most 64 in a lane (dim / 256 in the long rows), then across lanes
     nsum = max(64, dim // 256 + 1) + 16
-    nrow = T // 4 + 8          # rows a partial sum of g_w can have
+    nrow = T // 4 + 8          # rows a partial sum of g_w can have (fewer)
     for x in (gh, None):
         dx, mag, dc, gw, gwm = back_ref(gy, x, h, w, s)
         G_X, g_w = oec.add_rms_norm_backward(gy.cuda(), h.cuda(), w.cuda(), s.cuda(),

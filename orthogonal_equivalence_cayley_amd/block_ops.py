@@ -23,38 +23,40 @@ from . import poetx as _px
 
 _PX_DTYPE = {torch.float32: _px.POETX_FP32, torch.bfloat16: _px.POETX_BF16, torch.int8: _px.POETX_INT8}
 _REAL = (torch.bfloat16, torch.float32)
+_REAL_SET = frozenset(_REAL)
 _ACT = {name: i for i, name in enumerate(_px.ACTS)}
 _LIB = _px.LIB
+_raw_stream = torch._C._cuda_getCurrentRawStream   # of one GPU, without a Stream object around it
 
 
-def _matrix(name: str, t: torch.Tensor, shape=None, dtype=None, device=None) -> int:
-    """Checks a [rows, columns] argument; returns its row stride."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape or '[rows, columns]'}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} is on {t.device}, expected {device or 'a GPU'}")
+def _matrix(name: str, t: torch.Tensor, dev: int, shape=None, dtype=None) -> int:
+    """Checks a [rows, columns] argument on GPU dev; returns its row stride."""
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
+        raise ValueError(f"{name}: shape {tuple(size)}, expected {shape or '[rows, columns]'}")
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {f'cuda:{dev}' if dev >= 0 else 'a GPU'}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    rows, cols = t.shape
-    sr, sc = t.stride()
-    if cols > 1 and sc != 1:
+    row, col = t.stride()
+    if col != 1 and size[1] > 1:
         raise ValueError(f"{name}: columns are not contiguous")
-    return sr if rows > 1 else cols
+    return row if size[0] > 1 else size[1]
 
 
-def _vector(name: str, t: torch.Tensor, n: int, device) -> None:
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != torch.float32 or t.device != device or \
-            not t.is_contiguous():
-        raise ValueError(f"{name} must be {n} contiguous fp32 values on {device}")
+def _vector(name: str, t: torch.Tensor, n: int, dev: int) -> int:
+    if t.shape != (n,) or t.dtype != torch.float32 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous fp32 values on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _call(fn, where: str, device: torch.device, *args) -> None:
-    """fn(*args, stream) on the current stream of the tensors' device."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+def _call(fn, where: str, dev: int, *args) -> None:
+    """fn(*args, stream) on the current stream of the tensors' GPU."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev))
     else:
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        st = fn(*args, _raw_stream(dev))
     if st != _px.POETX_OK:
         raise _px.PoetxError(st, where)
 
@@ -78,26 +80,27 @@ def add_rms_norm(X: torch.Tensor, weight: torch.Tensor, residual: Optional[torch
     X, residual [T, dim] bf16 or fp32; weight fp32 [dim]. H: where h goes, X or
     residual itself for an update in place (default: a new tensor). quantize: y
     as INT8 rows, y = scale * Y. save: keep rstd for add_rms_norm_backward."""
-    ld_x = _matrix("X", X)
-    T, dim = X.shape
-    dt, dev = X.dtype, X.device
+    dev, dt = X.get_device(), X.dtype
+    ld_x = _matrix("X", X, dev)
+    shape = X.shape
+    T, dim = shape
     if dt not in _REAL:
         raise ValueError(f"X: {dt}, expected bfloat16 or float32")
-    _vector("weight", weight, dim, dev)
+    w = _vector("weight", weight, dim, dev)
     ld_r = ld_h = dim
     if residual is not None:
-        ld_r = _matrix("residual", residual, (T, dim), dt, dev)
-        if H is None:
-            H = torch.empty(T, dim, dtype=dt, device=dev)
+        ld_r = _matrix("residual", residual, dev, shape, dt)
     if H is not None:
-        ld_h = _matrix("H", H, (T, dim), dt, dev)
-    Y = torch.empty(T, dim, dtype=torch.int8 if quantize else dt, device=dev)
-    scale = torch.empty(T, dtype=torch.float32, device=dev) if quantize else None
-    rstd = torch.empty(T, dtype=torch.float32, device=dev) if save else None
-    d = _px.NormDesc(T, dim, _PX_DTYPE[dt], _px.POETX_INT8 if quantize else _PX_DTYPE[dt],
-                     ld_x, ld_r, ld_h, dim, eps)
-    _call(_LIB.poetx_add_rms_norm, "poetx_add_rms_norm", dev, d, X.data_ptr(), _ptr(residual),
-          weight.data_ptr(), _ptr(H), Y.data_ptr(), _ptr(scale), _ptr(rstd))
+        ld_h = _matrix("H", H, dev, shape, dt)
+    elif residual is not None:
+        H = torch.empty_like(X, memory_format=torch.contiguous_format)
+    code = _PX_DTYPE[dt]
+    Y = torch.empty_like(X, dtype=torch.int8 if quantize else dt, memory_format=torch.contiguous_format)
+    scale = torch.empty(T, dtype=torch.float32, device=X.device) if quantize else None
+    rstd = torch.empty(T, dtype=torch.float32, device=X.device) if save else None
+    d = _px.NormDesc(T, dim, code, _px.POETX_INT8 if quantize else code, ld_x, ld_r, ld_h, dim, eps)
+    _call(_LIB.poetx_add_rms_norm, "poetx_add_rms_norm", dev, d, X.data_ptr(), _ptr(residual), w, _ptr(H),
+          Y.data_ptr(), _ptr(scale), _ptr(rstd))
     return NormOut(Y, X if H is None else H, rstd, scale)
 
 
@@ -108,26 +111,28 @@ def add_rms_norm_backward(G_Y: torch.Tensor, H: torch.Tensor, weight: torch.Tens
     through the residual stream. H and rstd are those of add_rms_norm; G_X is the
     gradient of X and of the residual alike, and may be G_Y or G_H itself.
     g_weight is fp32 [dim], overwritten."""
-    ld_g = _matrix("G_Y", G_Y)
-    T, dim = G_Y.shape
-    dt, dev = G_Y.dtype, G_Y.device
+    dev, dt = G_Y.get_device(), G_Y.dtype
+    ld_g = _matrix("G_Y", G_Y, dev)
+    shape = G_Y.shape
+    T, dim = shape
     if dt not in _REAL:
         raise ValueError(f"G_Y: {dt}, expected bfloat16 or float32")
-    ld_h = _matrix("H", H, (T, dim), dt, dev)
-    _vector("weight", weight, dim, dev)
-    _vector("rstd", rstd, T, dev)
-    ld_gh = dim if G_H is None else _matrix("G_H", G_H, (T, dim), dt, dev)
+    ld_h = _matrix("H", H, dev, shape, dt)
+    w, s = _vector("weight", weight, dim, dev), _vector("rstd", rstd, T, dev)
+    ld_gh = dim if G_H is None else _matrix("G_H", G_H, dev, shape, dt)
     if G_X is None:
-        G_X = torch.empty(T, dim, dtype=dt, device=dev)
-    ld_gx = _matrix("G_X", G_X, (T, dim), dt, dev)
+        G_X = torch.empty_like(G_Y, memory_format=torch.contiguous_format)
+        ld_gx = dim
+    else:
+        ld_gx = _matrix("G_X", G_X, dev, shape, dt)
     if g_weight is None:
-        g_weight = torch.empty(dim, dtype=torch.float32, device=dev)
-    _vector("g_weight", g_weight, dim, dev)
-    ws = torch.empty(_LIB.poetx_rms_norm_backward_workspace(T, dim), dtype=torch.uint8, device=dev)
+        g_weight = torch.empty(dim, dtype=torch.float32, device=G_Y.device)
+    gw = _vector("g_weight", g_weight, dim, dev)
+    n = _LIB.poetx_rms_norm_backward_workspace(T, dim)
+    ws = torch.empty(n, dtype=torch.uint8, device=G_Y.device)
     d = _px.NormBackwardDesc(T, dim, _PX_DTYPE[dt], ld_g, ld_gh, ld_h, ld_gx)
     _call(_LIB.poetx_rms_norm_backward, "poetx_rms_norm_backward", dev, d, G_Y.data_ptr(), _ptr(G_H),
-          H.data_ptr(), weight.data_ptr(), rstd.data_ptr(), G_X.data_ptr(), g_weight.data_ptr(),
-          ws.data_ptr(), ws.numel())
+          H.data_ptr(), w, s, G_X.data_ptr(), gw, ws.data_ptr(), n)
     return G_X, g_weight
 
 
@@ -142,38 +147,40 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     act: one of poetx.ACTS. The result is bf16 for INT8 operands and X's dtype
     otherwise, or out_dtype (fp32 always possible, bf16 unless X is fp32). out: a
     [T, m] tensor for it, mul or residual itself for an update in place."""
-    ld_x, ld_w = _matrix("X", X), _matrix("W", W)
+    dev, dt = X.get_device(), X.dtype
+    ld_x, ld_w = _matrix("X", X, dev), _matrix("W", W, dev, None, dt)
     T, n = X.shape
-    m = W.shape[0]
-    dt, dev = X.dtype, X.device
+    m, k = W.shape
     if dt not in _PX_DTYPE:
         raise ValueError(f"X: {dt}, expected bfloat16, float32 or int8")
-    if W.shape[1] != n or W.dtype != dt or W.device != dev:
-        raise ValueError(f"W: {W.dtype} {tuple(W.shape)} on {W.device} for X: {dt} {tuple(X.shape)} on {dev}")
+    if k != n:
+        raise ValueError(f"W: {k} columns for {n} of X")
     if act not in _ACT:
         raise ValueError(f"act must be one of {_px.ACTS}")
+    sx = sw = b = None
     if dt == torch.int8:
         if x_scale is None or w_scale is None:
             raise ValueError("INT8 operands need x_scale and w_scale")
-        _vector("x_scale", x_scale, T, dev)
-        _vector("w_scale", w_scale, m, dev)
+        sx, sw = _vector("x_scale", x_scale, T, dev), _vector("w_scale", w_scale, m, dev)
     elif x_scale is not None or w_scale is not None:
         raise ValueError("x_scale and w_scale are for INT8 operands")
     if bias is not None:
-        _vector("bias", bias, m, dev)
+        b = _vector("bias", bias, m, dev)
+    shape = (T, m)
     if out is None:
-        out = torch.empty(T, m, dtype=out_dtype or (torch.bfloat16 if dt == torch.int8 else dt), device=dev)
+        out = torch.empty(shape, dtype=out_dtype or (torch.bfloat16 if dt == torch.int8 else dt),
+                          device=X.device)
         ld_y = m
     else:
-        ld_y = _matrix("out", out, (T, m), out_dtype, dev)
+        ld_y = _matrix("out", out, dev, shape, out_dtype)
     yt = out.dtype
     if yt not in _REAL or (dt == torch.float32 and yt != dt):
         raise ValueError(f"the result cannot be {yt} for {dt} operands")
-    ld_m = m if mul is None else _matrix("mul", mul, (T, m), yt, dev)
-    ld_r = m if residual is None else _matrix("residual", residual, (T, m), yt, dev)
+    ld_m = m if mul is None else _matrix("mul", mul, dev, shape, yt)
+    ld_r = m if residual is None else _matrix("residual", residual, dev, shape, yt)
     d = _px.LinearDesc(T, m, n, _PX_DTYPE[dt], _PX_DTYPE[yt], _ACT[act], ld_x, ld_w, ld_y, ld_m, ld_r)
-    _call(_LIB.poetx_linear, "poetx_linear", dev, d, X.data_ptr(), W.data_ptr(), _ptr(x_scale),
-          _ptr(w_scale), _ptr(bias), _ptr(mul), _ptr(residual), out.data_ptr())
+    _call(_LIB.poetx_linear, "poetx_linear", dev, d, X.data_ptr(), W.data_ptr(), sx, sw, b, _ptr(mul),
+          _ptr(residual), out.data_ptr())
     return out
 
 
@@ -205,33 +212,34 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
     grads: contiguous bf16 or fp32 tensors of one GPU. out: tensors of the same
     sizes and dtypes, grads itself for an update in place; None: the norm only."""
     grads = list(grads)
-    if not grads:
+    n = len(grads)
+    if not n:
         raise ValueError("no gradients")
-    dev = grads[0].device
-    if not grads[0].is_cuda:
-        raise ValueError(f"gradients are on {dev}, expected a GPU")
-    types = array("i")
-    for g in grads:
-        if g.dtype not in _REAL or g.device != dev or not g.is_contiguous():
-            raise ValueError("gradients must be contiguous bf16 or fp32 tensors of one GPU")
-        types.append(_PX_DTYPE[g.dtype])
+    first = grads[0]
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"gradients are on {first.device}, expected a GPU")
+    types = [g.dtype for g in grads]
+    ns = [g.numel() for g in grads]
+    if not _REAL_SET.issuperset(types) or not all([g.get_device() == dev for g in grads]) or \
+            not all([g.is_contiguous() for g in grads]):
+        raise ValueError("gradients must be contiguous bf16 or fp32 tensors of one GPU")
     ptrs = array("Q", [g.data_ptr() for g in grads])
-    ns = array("q", [g.numel() for g in grads])
+    sizes, codes = array("q", ns), array("i", [_PX_DTYPE[t] for t in types])
     outs = None
     if out is not None:
         out = list(out)
-        if len(out) != len(grads):
-            raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
-        for g, o in zip(grads, out):
-            if o is not g and (o.dtype != g.dtype or o.device != dev or o.numel() != g.numel() or
-                               not o.is_contiguous()):
-                raise ValueError("an output differs from its gradient in size, dtype or device, or is "
-                                 "not contiguous")
+        if len(out) != n:
+            raise ValueError(f"{len(out)} outputs for {n} gradients")
+        if [o.dtype for o in out] != types or [o.numel() for o in out] != ns or \
+                not all([o.get_device() == dev for o in out]) or not all([o.is_contiguous() for o in out]):
+            raise ValueError("an output differs from its gradient in size, dtype or device, or is not "
+                             "contiguous")
         outs = array("Q", [o.data_ptr() for o in out])
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    n = len(grads)
-    ws = torch.empty(_LIB.poetx_clip_grads_workspace(n), dtype=torch.uint8, device=dev)
-    addr = lambda a: None if a is None else a.buffer_info()[0]  # noqa: E731
-    _call(_LIB.poetx_clip_grads, "poetx_clip_grads", dev, n, addr(ptrs), addr(ns), addr(types), addr(outs),
-          max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel())
+    norm = torch.empty((), dtype=torch.float32, device=first.device)
+    wsb = _LIB.poetx_clip_grads_workspace(n)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=first.device)
+    _call(_LIB.poetx_clip_grads, "poetx_clip_grads", dev, n, ptrs.buffer_info()[0], sizes.buffer_info()[0],
+          codes.buffer_info()[0], None if outs is None else outs.buffer_info()[0], max_norm, norm.data_ptr(),
+          ws.data_ptr(), wsb)
     return norm

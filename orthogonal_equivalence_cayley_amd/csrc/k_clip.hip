@@ -4,13 +4,15 @@
 //   out = rnd(c g)
 //
 // Bound by memory. The norm has to be known before the first product, so all
-// gradients are read twice and written once: the second read comes from the
-// caches where they hold the set (256 MB behind the eight L2s). Two launches for
-// up to kClipMax tensors: partial sums of squares, one per workgroup, in 64
-// bits (no overflow for any fp32 gradient, and no order that shows in the fp32
-// result's rounding but in the rarest cases), then the products, where every
-// workgroup adds up the few partial sums itself, in the same order, instead of
-// waiting for a launch between.
+// gradients are read twice and written once. Two launches for up to kClipMax
+// tensors: partial sums of squares, one per workgroup, in 64 bits (no overflow for
+// any fp32 gradient, and an order that does not show in the fp32 norm but in the
+// rarest cases), then the products, where every workgroup adds up the few
+// partial sums itself, in the same order, instead of waiting for a launch between.
+// Workgroups take chunks of 8192 elements, all loads of a chunk out at once.
+// Measured: 204 tensors of 1.4 GB in all 730 us (sums 5.9 TB/s, products 5.4
+// TB/s); 16 of 20 MB 7.5 + 9.7 us. 2048 workgroups to a launch instead of 1024:
+// 752 us.
 #include <algorithm>
 
 #include "poetx_internal.h"
@@ -21,12 +23,19 @@ namespace {
 constexpr int kThr = 256;
 constexpr int kChunk = 8192;        // elements of one step of a workgroup
 constexpr int kGrid = 1024;         // workgroups of one launch
+constexpr long long kCached = 256LL << 20;   // bytes of the cache in front of the memory
 constexpr int kFold = 4096;         // partial sums a workgroup adds up itself
 
 __device__ __forceinline__ float bf(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ uint32_t rnd(float v) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
+
+// 16 bytes at any element alignment
+struct __attribute__((packed, aligned(2))) Vec16 {
+  uint32_t w[4];
+};
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4), aligned(2)));
 
 __device__ __forceinline__ double block_sum(double v) {
   __shared__ double red[kThr / 64];
@@ -51,48 +60,50 @@ __device__ __forceinline__ int entry_of(const ClipBatch& b, int q) {
   return lo;
 }
 
+__device__ __forceinline__ void add_squares(const Vec16& v, bool bf16, double& s) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (bf16) {
+      const double lo = bf(v.w[k] & 0xffffu), hi = bf(v.w[k] >> 16);
+      s += lo * lo;
+      s += hi * hi;
+    } else {
+      const double x = __uint_as_float(v.w[k]);
+      s += x * x;
+    }
+  }
+}
+
+// VECS vectors of each thread in one go where the chunk is whole
+template <bool BF16>
+__device__ __forceinline__ void sum_chunk(const void* p, long long i0, int n, double& s) {
+  constexpr int N = BF16 ? 8 : 4, VECS = kChunk / (kThr * N);
+  const char* g = static_cast<const char*>(p) + i0 * (16 / N);
+  if (n == kChunk) {
+    Vec16 v[VECS];
+#pragma unroll
+    for (int k = 0; k < VECS; ++k) v[k] = *reinterpret_cast<const Vec16*>(g + (k * kThr + threadIdx.x) * 16);
+#pragma unroll
+    for (int k = 0; k < VECS; ++k) add_squares(v[k], BF16, s);
+    return;
+  }
+  const int whole = n / N;
+  for (int k = threadIdx.x; k < whole; k += kThr) add_squares(*reinterpret_cast<const Vec16*>(g + k * 16), BF16, s);
+  const int k = whole * N + threadIdx.x;
+  if (k < n) {
+    const double x = BF16 ? bf(reinterpret_cast<const uint16_t*>(g)[k]) : reinterpret_cast<const float*>(g)[k];
+    s += x * x;
+  }
+}
+
 __global__ __launch_bounds__(kThr) void sum_squares_kernel(ClipBatch b, int chunks, double* part) {
   double s = 0.0;
   for (int q = blockIdx.x; q < chunks; q += gridDim.x) {
     const ClipEntry& e = b.e[entry_of(b, q)];
     const long long i0 = (long long)(q - e.chunk0) * kChunk;
     const int n = (int)min((long long)kChunk, e.n - i0);
-    if (e.bf16) {
-      const uint16_t* g = static_cast<const uint16_t*>(e.g) + i0;
-      for (int i = threadIdx.x * 8; i < n; i += kThr * 8) {
-        if (i + 8 <= n) {
-          uint4 v;
-          __builtin_memcpy(&v, g + i, 16);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const double lo = bf(w[k] & 0xffffu), hi = bf(w[k] >> 16);
-            s += lo * lo;
-            s += hi * hi;
-          }
-        } else {
-          for (int k = i; k < n; ++k) {
-            const double x = bf(g[k]);
-            s += x * x;
-          }
-        }
-      }
-    } else {
-      const float* g = static_cast<const float*>(e.g) + i0;
-#pragma unroll 4
-      for (int i = threadIdx.x * 4; i < n; i += kThr * 4) {
-        if (i + 4 <= n) {
-          float4 v;
-          __builtin_memcpy(&v, g + i, 16);
-          s += (double)v.x * v.x;
-          s += (double)v.y * v.y;
-          s += (double)v.z * v.z;
-          s += (double)v.w * v.w;
-        } else {
-          for (int k = i; k < n; ++k) s += (double)g[k] * g[k];
-        }
-      }
-    }
+    if (e.bf16) sum_chunk<true>(e.g, i0, n, s);
+    else sum_chunk<false>(e.g, i0, n, s);
   }
   s = block_sum(s);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -106,66 +117,88 @@ __global__ __launch_bounds__(kThr) void fold_kernel(double* part, int n) {
   if (threadIdx.x == 0) part[0] = s;
 }
 
+__device__ __forceinline__ Vec16 scaled(Vec16 v, bool bf16, float c) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    v.w[k] = bf16 ? rnd(c * bf(v.w[k] & 0xffffu)) | rnd(c * bf(v.w[k] >> 16)) << 16
+                  : __float_as_uint(c * __uint_as_float(v.w[k]));
+  return v;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void clip_chunk(const void* p, void* q, long long i0, int n, float c,
+                                           bool stream) {
+  constexpr int N = BF16 ? 8 : 4, VECS = kChunk / (kThr * N);
+  const char* g = static_cast<const char*>(p) + i0 * (16 / N);
+  char* o = static_cast<char*>(q) + i0 * (16 / N);
+  if (n == kChunk) {
+    Vec16 v[VECS];
+#pragma unroll
+    for (int k = 0; k < VECS; ++k) v[k] = *reinterpret_cast<const Vec16*>(g + (k * kThr + threadIdx.x) * 16);
+#pragma unroll
+    for (int k = 0; k < VECS; ++k) {
+      const Vec16 r = scaled(v[k], BF16, c);
+      char* to = o + (k * kThr + threadIdx.x) * 16;
+      if (stream) __builtin_nontemporal_store(u32x4{r.w[0], r.w[1], r.w[2], r.w[3]}, reinterpret_cast<u32x4*>(to));
+      else *reinterpret_cast<Vec16*>(to) = r;
+    }
+    return;
+  }
+  const int whole = n / N;
+  for (int k = threadIdx.x; k < whole; k += kThr)
+    *reinterpret_cast<Vec16*>(o + k * 16) = scaled(*reinterpret_cast<const Vec16*>(g + k * 16), BF16, c);
+  const int k = whole * N + threadIdx.x;
+  if (k < n) {
+    if (BF16) reinterpret_cast<uint16_t*>(o)[k] = (uint16_t)rnd(c * bf(reinterpret_cast<const uint16_t*>(g)[k]));
+    else reinterpret_cast<float*>(o)[k] = c * reinterpret_cast<const float*>(g)[k];
+  }
+}
+
+// Chunks from the last to the first: what the sums read last is what the caches
+// still hold.
 __global__ __launch_bounds__(kThr) void clip_kernel(ClipBatch b, int chunks, const double* part, int nparts,
-                                                    double max_norm, float* norm_out) {
+                                                    double max_norm, float* norm_out, bool stream) {
   double s = 0.0;
   for (int i = threadIdx.x; i < nparts; i += kThr) s += part[i];
   const double norm = sqrt(block_sum(s));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   const double ratio = max_norm / (norm + 1e-6);
   const float c = ratio >= 1.0 ? 1.0f : (float)ratio;   // NaN stays NaN
-  for (int q = blockIdx.x; q < chunks; q += gridDim.x) {
+  for (int q = chunks - 1 - (int)blockIdx.x; q >= 0; q -= gridDim.x) {
     const ClipEntry& e = b.e[entry_of(b, q)];
     if (c == 1.0f && e.g == e.out) continue;   // in place and within the limit: nothing changes
     const long long i0 = (long long)(q - e.chunk0) * kChunk;
     const int n = (int)min((long long)kChunk, e.n - i0);
-    if (e.bf16) {
-      const uint16_t* g = static_cast<const uint16_t*>(e.g) + i0;
-      uint16_t* o = static_cast<uint16_t*>(e.out) + i0;
-      for (int i = threadIdx.x * 8; i < n; i += kThr * 8) {
-        if (i + 8 <= n) {
-          uint32_t w[4];
-          __builtin_memcpy(w, g + i, 16);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = rnd(c * bf(w[k] & 0xffffu)) | rnd(c * bf(w[k] >> 16)) << 16;
-          __builtin_memcpy(o + i, w, 16);
-        } else {
-          for (int k = i; k < n; ++k) o[k] = (uint16_t)rnd(c * bf(g[k]));
-        }
-      }
-    } else {
-      const float* g = static_cast<const float*>(e.g) + i0;
-      float* o = static_cast<float*>(e.out) + i0;
-#pragma unroll 4
-      for (int i = threadIdx.x * 4; i < n; i += kThr * 4) {
-        if (i + 4 <= n) {
-          float v[4];
-          __builtin_memcpy(v, g + i, 16);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] *= c;
-          __builtin_memcpy(o + i, v, 16);
-        } else {
-          for (int k = i; k < n; ++k) o[k] = c * g[k];
-        }
-      }
-    }
+    if (e.bf16) clip_chunk<true>(e.g, e.out, i0, n, c, stream);
+    else clip_chunk<false>(e.g, e.out, i0, n, c, stream);
   }
 }
 
-// fills b from items [i0, ..) and returns how many it took; `chunks`: their chunks
+// Fills b with the items from i0 on that fit one launch, backward from the one
+// before i0 with BACK (still in their order inside b); returns how many it took.
+// `chunks`: their chunks.
+template <bool BACK>
 int fill(const ClipItem* items, int count, int i0, ClipBatch& b, long long& chunks) {
   b.n = 0;
   chunks = 0;
-  int i = i0;
-  for (; i < count && b.n < kClipMax; ++i) {
+  int took = 0, first = i0;
+  // the range first, then the entries in order
+  long long total = 0;
+  for (int n = 0; BACK ? i0 - took > 0 : i0 + took < count; ++took) {
+    const ClipItem& it = items[BACK ? i0 - took - 1 : i0 + took];
+    if (it.n <= 0) continue;
+    total += (it.n + kChunk - 1) / kChunk;
+    if (n == kClipMax || total > 0x7fffffffLL) break;
+    ++n;
+  }
+  if (BACK) first = i0 - took;
+  for (int i = first; i < first + took; ++i) {
     const ClipItem& it = items[i];
     if (it.n <= 0) continue;
-    const long long c = (it.n + kChunk - 1) / kChunk;
-    if (chunks + c > 0x7fffffffLL) break;
     b.e[b.n++] = ClipEntry{it.g, it.out, it.n, (int)chunks, it.bf16};
-    chunks += c;
+    chunks += (it.n + kChunk - 1) / kChunk;
   }
-  return i - i0;
+  return took;
 }
 
 }  // namespace
@@ -178,7 +211,7 @@ hipError_t launch_clip(const ClipItem* items, int count, double max_norm, double
   long long chunks = 0;
   int nparts = 0;
   for (int i = 0; i < count;) {
-    i += fill(items, count, i, b, chunks);
+    i += fill<false>(items, count, i, b, chunks);
     if (!b.n) continue;
     const int grid = (int)std::min<long long>(chunks, kGrid);
     hipLaunchKernelGGL(sum_squares_kernel, dim3(grid), dim3(kThr), 0, s, b, (int)chunks, part + nparts);
@@ -192,14 +225,20 @@ hipError_t launch_clip(const ClipItem* items, int count, double max_norm, double
     if (e != hipSuccess) return e;
     nparts = 1;
   }
+  // Results that the caches cannot hold for their reader go past them: 1.4 GB
+  // in 730 instead of 770 us (the sums of the next step find fewer lines to write
+  // back). A set that fits stays: it is read next, and 20 MB take 17 us either way.
+  long long bytes = 0;
+  for (int i = 0; i < count; ++i) bytes += items[i].n * (items[i].bf16 ? 2 : 4);
+  const bool stream = bytes > kCached;
   bool first = true;
-  for (int i = 0; i < count || first;) {
-    i += fill(items, count, i, b, chunks);
+  for (int i = count; i > 0 || first;) {
+    i -= fill<true>(items, count, i, b, chunks);
     if (!b.n && !first) continue;
     if (!write) chunks = 0;   // the norm only
     const int grid = (int)std::max<long long>(1, std::min<long long>(chunks, kGrid));
     hipLaunchKernelGGL(clip_kernel, dim3(grid), dim3(kThr), 0, s, b, (int)chunks, part, nparts, max_norm,
-                       first ? norm_out : nullptr);
+                       first ? norm_out : nullptr, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     first = false;

@@ -61,7 +61,7 @@ bool real_type(int dtype) { return dtype == POETX_FP32 || dtype == POETX_BF16; }
 
 constexpr int64_t kMaxRows = 0x7fffffff;
 constexpr int32_t kMaxTensors = 1 << 20;
-constexpr int64_t kMaxElems = int64_t(1) << 40;   // of one gradient tensor
+constexpr int64_t kMaxElems = int64_t(1) << 37;   // of one gradient tensor: a launch counts chunks in 31 bits
 
 }  // namespace
 

@@ -115,7 +115,7 @@ constexpr int kTileThr = 256;
 constexpr int kKB = 128;   // bytes of n per stage
 
 // BM tokens x BN rows of W, four waves of BM/2 x BN/2. 16-byte chunk c of tile
-// row r sits at slot 8 r + (c ^ (r & 7)): the 16 rows a quarter of a wave reads
+// row r sits at slot 8 r + (c ^ ((r / 2) & 7)): the 16 rows a quarter of a wave reads
 // at one chunk fall in distinct banks. The next stage's global loads are in
 // flight while the current one is multiplied.
 template <typename Ty, int BM, int BN, bool YBF16>
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kTileThr) void linear_tile_kernel(LinearArgs a) {
 #pragma unroll
     for (int i = 0; i < LW; ++i) wr[i] = load16<Ty::kSize>(ws[i] + k, kb - k);
   };
-  auto slot = [](int r, int c) { return r * 8 + (c ^ (r & 7)); };
+  auto slot = [](int r, int c) { return r * 8 + (c ^ ((r / 2) & 7)); };
   typename Ty::Acc acc[TM][TN] = {};
   fetch(0);
   for (long long k0 = 0; k0 < kb; k0 += kKB) {
@@ -228,6 +228,7 @@ hipError_t launch_typed(const LinearArgs& a, hipStream_t s) {
 
 hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s) {
   if (a.T <= 0 || a.m <= 0 || a.n <= 0) return hipErrorInvalidValue;
+  if (a.T > 256 && linear_pipe_supported(a, type)) return launch_linear_pipe(a, type, s);
   switch (type) {
     case LINEAR_F32: return a.y_bf16 ? hipErrorInvalidValue : launch_typed<TypeF32, false>(a, s);
     case LINEAR_BF16: return a.y_bf16 ? launch_typed<TypeBf16, true>(a, s) : launch_typed<TypeBf16, false>(a, s);

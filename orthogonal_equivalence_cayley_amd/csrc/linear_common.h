@@ -2,6 +2,8 @@
 // element types with their matrix instructions, and the epilogue.
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/poetx.h"
 #include "poetx_internal.h"
 
@@ -84,11 +86,6 @@ __device__ __forceinline__ i32x4 load16(const char* p, long long left) {
   return v;
 }
 
-__device__ __forceinline__ float load_y(const void* p, long long i, int bf16) {
-  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16)
-              : static_cast<const float*>(p)[i];
-}
-
 // The activations in 32 bits. A result that is rounded to bf16 takes the
 // hardware's exponential and reciprocal (a few units of 2^-24 off), an fp32 one
 // the library's functions.
@@ -97,12 +94,29 @@ __device__ __forceinline__ float logistic(float z) {
   if constexpr (BF16) return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
   else return 1.0f / (1.0f + expf(-z));
 }
+// erfc(|x| / sqrt 2) / 2 within 0.75e-7 (Abramowitz and Stegun 7.1.26), for
+// results that are rounded to bf16
+__device__ __forceinline__ float half_erfc(float x) {
+  const float y = fabsf(x) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, y, 1.0f));
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  return 0.5f * p * t * __expf(-y * y);
+}
 template <bool BF16>
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
     case POETX_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
     case POETX_ACT_SILU: return z * logistic<BF16>(z);
-    case POETX_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case POETX_ACT_GELU:
+      if constexpr (BF16) {
+        const float e = z * half_erfc(z);
+        return z > 0.0f ? z - e : e;
+      } else {
+        return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+      }
     case POETX_ACT_GELU_TANH: {
       const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
       // (1 + tanh u) / 2 is the logistic function of 2 u
@@ -112,82 +126,87 @@ __device__ __forceinline__ float activate(float z, int act) {
   }
 }
 
-template <typename S>
-__device__ __forceinline__ float scaled(const LinearArgs& a, S acc, long long t, int c) {
-  return (float)acc;
+template <typename E, int N>
+struct __attribute__((packed, aligned(sizeof(E)))) Pack {
+  E v[N];
+};
+// N values at p as fp32; the first `cols` with EDGE
+template <bool EDGE, int N>
+__device__ __forceinline__ void load_cols(const float* p, int cols, float (&o)[N]) {
+  if constexpr (EDGE) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = i < cols ? p[i] : 0.0f;
+  } else {
+    const Pack<float, N> v = *reinterpret_cast<const Pack<float, N>*>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = v.v[i];
+  }
 }
-template <>
-__device__ __forceinline__ float scaled<int>(const LinearArgs& a, int acc, long long t, int c) {
-  return (float)acc * a.sx[t] * a.sw[c];
+template <bool EDGE, int N>
+__device__ __forceinline__ void load_cols(const uint16_t* p, int cols, float (&o)[N]) {
+  if constexpr (EDGE) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = i < cols ? __uint_as_float((uint32_t)p[i] << 16) : 0.0f;
+  } else {
+    const Pack<uint16_t, N> v = *reinterpret_cast<const Pack<uint16_t, N>*>(p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = __uint_as_float((uint32_t)v.v[i] << 16);
+  }
 }
 
-// N consecutive columns c .. of row t; `cols` of them exist
-template <bool BF16, typename S, int N>
-__device__ __forceinline__ void finish(const LinearArgs& a, const S (&acc)[N], long long t, int c) {
-  const int cols = min(N, a.m - c);
-  float v[N];
+// N consecutive columns c .. of row t, all of them inside the result (or the first
+// `cols` with EDGE). ACT: the activation where the kernel is made for one.
+constexpr int kAnyAct = -1;
+template <bool BF16, int ACT, bool EDGE, typename S, int N>
+__device__ __forceinline__ void finish_cols(const LinearArgs& a, const S (&acc)[N], long long t, int c,
+                                            int cols) {
+  float v[N], o[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (i >= cols) continue;
-    float z = scaled(a, acc[i], t, c + i);
-    if (a.bias) z += a.bias[c + i];
-    v[i] = activate<BF16>(z, a.act);
+  for (int i = 0; i < N; ++i) v[i] = (float)acc[i];
+  if constexpr (std::is_same<S, int>::value) {
+    const float sx = a.sx[t];
+    load_cols<EDGE>(a.sw + c, cols, o);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] * sx * o[i];
   }
-  auto operand = [&](const void* p, long long ld, float (&o)[N]) {
-    if constexpr (BF16) {
-      uint16_t h[N];
-      const uint16_t* q = static_cast<const uint16_t*>(p) + t * ld + c;
-      if (cols == N) {
-        __builtin_memcpy(h, q, sizeof(h));
-      } else {
+  if (a.bias) {
+    load_cols<EDGE>(a.bias + c, cols, o);
 #pragma unroll
-        for (int i = 0; i < N; ++i) h[i] = i < cols ? q[i] : 0;
-      }
+    for (int i = 0; i < N; ++i) v[i] += o[i];
+  }
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = __uint_as_float((uint32_t)h[i] << 16);
-    } else {
-      const float* q = static_cast<const float*>(p) + t * ld + c;
-      if (cols == N) {
-        __builtin_memcpy(o, q, sizeof(o));
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = i < cols ? q[i] : 0.0f;
-      }
-    }
-  };
-  float o[N];
+  for (int i = 0; i < N; ++i) v[i] = activate<BF16>(v[i], ACT == kAnyAct ? a.act : ACT);
+  typedef typename std::conditional<BF16, uint16_t, float>::type E;
   if (a.mul) {
-    operand(a.mul, a.ldm, o);
+    load_cols<EDGE>(static_cast<const E*>(a.mul) + t * a.ldm + c, cols, o);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] *= o[i];
   }
   if (a.res) {
-    operand(a.res, a.ldr, o);
+    load_cols<EDGE>(static_cast<const E*>(a.res) + t * a.ldr + c, cols, o);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += o[i];
   }
-  if constexpr (BF16) {
-    uint16_t h[N];
+  Pack<E, N> r;
 #pragma unroll
-    for (int i = 0; i < N; ++i) h[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[i]));
-    uint16_t* y = static_cast<uint16_t*>(a.Y) + t * a.ldy + c;
-    if (cols == N) {
-      __builtin_memcpy(y, h, sizeof(h));
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < cols) y[i] = h[i];
-    }
-  } else {
-    float* y = static_cast<float*>(a.Y) + t * a.ldy + c;
-    if (cols == N) {
-      __builtin_memcpy(y, v, sizeof(v));
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < cols) y[i] = v[i];
-    }
+  for (int i = 0; i < N; ++i) {
+    if constexpr (BF16) r.v[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[i]));
+    else r.v[i] = v[i];
   }
+  E* y = static_cast<E*>(a.Y) + t * a.ldy + c;
+  if constexpr (EDGE) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < cols) y[i] = r.v[i];
+  } else {
+    *reinterpret_cast<Pack<E, N>*>(y) = r;
+  }
+}
+// the same where the columns may end inside the N
+template <bool BF16, int ACT = kAnyAct, typename S, int N>
+__device__ __forceinline__ void finish(const LinearArgs& a, const S (&acc)[N], long long t, int c) {
+  if (c + N <= a.m) finish_cols<BF16, ACT, false>(a, acc, t, c, N);
+  else finish_cols<BF16, ACT, true>(a, acc, t, c, a.m - c);
 }
 
 }  // namespace lin

@@ -292,5 +292,8 @@ struct LinearArgs {
   int y_bf16;    // Y, mul and res are bf16 (else fp32)
 };
 hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s);
+// 256 x 256 tiles with one load pipeline (k_linear_pipe.hip): bf16 and INT8
+bool linear_pipe_supported(const LinearArgs& a, int type);
+hipError_t launch_linear_pipe(const LinearArgs& a, int type, hipStream_t s);
 
 }  // namespace poetx

@@ -105,20 +105,22 @@ void linear_pipe_kernel(LinearArgs p) {
   // by its workgroups with a stride of their count; a tile index maps to an origin
   // in groups of kGroupRows tile-rows
   const int tn = (p.m + kTile - 1) / kTile, tm = (int)((p.T + kTile - 1) / kTile);
-  const long long ntile = (long long)tn * tm;
+  const int ntile = tn * tm;
   const int x = blockIdx.x % 8, sx = blockIdx.x / 8;
   const int nx = (int)gridDim.x / 8 + (x < (int)gridDim.x % 8 ? 1 : 0);
-  const long long t_first = ntile * x / 8 + sx, t_end = ntile * (x + 1) / 8;
-  const int t_count = t_first < t_end ? (int)((t_end - t_first + nx - 1) / nx) : 0;
+  const int t_first = (int)((long long)ntile * x / 8) + sx, t_end = (int)((long long)ntile * (x + 1) / 8);
+  const int t_count = t_first < t_end ? (t_end - t_first + nx - 1) / nx : 0;
   if (t_count == 0) return;
+  // 32-bit throughout, and told to be uniform: a 64-bit division leaves its result
+  // in vector registers, and every load would loop over its lanes' descriptors
   auto origin = [&](int ti, int& m0, int& n0) {
-    const long long lin = t_first + (long long)ti * nx;
-    const int grp = (int)(lin / (kGroupRows * (long long)tn));
+    const int lin = t_first + ti * nx;
+    const int grp = lin / (kGroupRows * tn);
     const int first = grp * kGroupRows;
     const int gsz = min(kGroupRows, tm - first);
-    const int in = (int)(lin - grp * (kGroupRows * (long long)tn));
-    m0 = (first + in % gsz) * kTile;
-    n0 = (in / gsz) * kTile;
+    const int in = lin - grp * (kGroupRows * tn);
+    m0 = __builtin_amdgcn_readfirstlane((first + in % gsz) * kTile);
+    n0 = __builtin_amdgcn_readfirstlane((in / gsz) * kTile);
   };
 
   const int lda = (int)(p.ldx * Ty::kSize), ldb = (int)(p.ldw * Ty::kSize);   // bytes, 256 of them below 2^31
@@ -215,8 +217,6 @@ void linear_pipe_kernel(LinearArgs p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (AHEAD && opnd && i < 3) fetch(opnd, ldo, m0, n0, i + 1, pre[(i + 1) & 1]);
-      Cols second[4];
-      if (AHEAD && p.mul && p.res) fetch(static_cast<const E*>(p.res), p.ldr, m0, n0, i, second);
       float sx = 1.0f;
       if constexpr (SCALED) sx = p.sx[(long long)m0 + wm0 + i * 32 + cm];
 #pragma unroll
@@ -247,7 +247,7 @@ void linear_pipe_kernel(LinearArgs p) {
           for (int e = 0; e < 8; ++e) v[e] *= o[e];
         }
         if (p.res) {
-          if constexpr (AHEAD) widen(p.mul ? second[q] : pre[i & 1][q], o);
+          if (AHEAD && !p.mul) widen(pre[i & 1][q], o);
           else widen(fetch_one(static_cast<const E*>(p.res), p.ldr, m0, n0, i, q), o);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] += o[e];
@@ -409,6 +409,7 @@ hipError_t launch(const LinearArgs& a, hipStream_t s) {
 bool linear_pipe_supported(const LinearArgs& a, int type) {
   if (type == LINEAR_F32) return false;
   const int es = type == LINEAR_BF16 ? 2 : 1;
+  if ((a.T / kTile + 1) * (a.m / kTile + 1) >= (1LL << 28)) return false;   // tile numbers in 32 bits
   if (a.T < kTile || a.m < kTile || a.m % 8 || (long long)a.n * es % kKB || a.ldx * es % 16 || a.ldw * es % 16) return false;
   if (((uintptr_t)a.X | (uintptr_t)a.W) & 15) return false;
   return a.ldx * es * kTile < (1LL << 31) && a.ldw * es * kTile < (1LL << 31);

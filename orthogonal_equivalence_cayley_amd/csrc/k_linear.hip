@@ -4,12 +4,13 @@
 // (z = float(sum q q) sx sw, the sum exact in 32 bits). Sums in fp32 (INT8: in
 // integers), the epilogue in fp32, one rounding at the end.
 //
-// Three kernels by the number of tokens:
-//  * up to 4, linear_rows: every wave takes rows of W whole and multiplies on
-//    the vector units: bound by the weight's bytes.
-//  * up to 64, linear_few: 16 rows of W to a workgroup, its 8 waves split n and
-//    feed the matrix units straight from memory; their sums meet in LDS.
-//  * more, linear_tile: tiles staged through LDS, any sizes and alignment.
+// Four kernels:
+//  * one token (up to four where rows are unaligned), linear_rows: every wave takes
+//    rows of W whole and multiplies on the vector units: bound by the weight's bytes.
+//  * linear_pipe (k_linear_pipe.hip) and linear_ring (k_linear_ring.hip): tiles
+//    filled by direct-to-LDS loads, for rows of whole 128-byte pieces.
+//  * linear_tile: tiles filled through registers, any sizes and alignment.
+// The tile is the one of least cost for the grid it makes (`cheapest`).
 #include <algorithm>
 
 #include "linear_common.h"
@@ -61,118 +62,111 @@ __global__ __launch_bounds__(kRowThr) void linear_rows_kernel(LinearArgs a) {
   }
 }
 
-// ------------------------------------------------------------------ few tokens
-constexpr int kFewWaves = 8;
-constexpr int kFewThr = kFewWaves * 64;
-
-// Wave w takes the 256-byte pieces w, w + 8, .. of n: four slabs of 64 bytes
-// whose loads go out together. NT token tiles of 16.
-template <typename Ty, int NT, bool YBF16>
-__global__ __launch_bounds__(kFewThr) void linear_few_kernel(LinearArgs a) {
-  __shared__ typename Ty::Acc red[kFewWaves][NT][64];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int r0 = blockIdx.x * 16;
-  const int row = lane & 15, ko = (lane >> 4) * 16;
-  const long long kb = (long long)a.n * Ty::kSize;
-  const char* w = static_cast<const char*>(a.W) + (long long)min(r0 + row, a.m - 1) * a.ldw * Ty::kSize;
-  const char* x[NT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-    x[j] = static_cast<const char*>(a.X) + min((long long)(j * 16 + row), a.T - 1) * a.ldx * Ty::kSize;
-  typename Ty::Acc acc[NT] = {};
-  for (long long q = (long long)wave * 256; q < kb; q += kFewWaves * 256) {
-    i32x4 wv[4], xv[NT][4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const long long k = q + s * 64 + ko;
-      wv[s] = load16<Ty::kSize>(w + k, kb - k);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) xv[j][s] = load16<Ty::kSize>(x[j] + k, kb - k);
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) Ty::mma(wv[s], xv[j][s], acc[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < NT; ++j) red[wave][j][lane] = acc[j];
-  __syncthreads();
-  for (int j = wave; j < NT; j += kFewWaves) {
-    typename Ty::Acc v = red[0][j][lane];
-#pragma unroll
-    for (int i = 1; i < kFewWaves; ++i) v += red[i][j][lane];
-    const long long t = j * 16 + (lane & 15);
-    const int c = r0 + 4 * (lane >> 4);
-    if (t < a.T && c < a.m) {
-      const typename Ty::Sum o[4] = {v[0], v[1], v[2], v[3]};
-      finish<YBF16>(a, o, t, c);
-    }
-  }
-}
-
 // ------------------------------------------------------------------ tiles
-constexpr int kTileThr = 256;
-constexpr int kKB = 128;   // bytes of n per stage
-
-// BM tokens x BN rows of W, four waves of BM/2 x BN/2. 16-byte chunk c of tile
-// row r sits at slot 8 r + (c ^ ((r / 2) & 7)): the 16 rows a quarter of a wave reads
-// at one chunk fall in distinct banks. The next stage's global loads are in
-// flight while the current one is multiplied.
-template <typename Ty, int BM, int BN, bool YBF16>
-__global__ __launch_bounds__(kTileThr) void linear_tile_kernel(LinearArgs a) {
-  constexpr int LX = BM * 8 / kTileThr, LW = BN * 8 / kTileThr;
-  constexpr int TM = BM / 32, TN = BN / 32;   // 16 x 16 tiles of a wave
-  __shared__ __align__(16) i32x4 lds[(BM + BN) * 8];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// BM tokens x BN rows of W per workgroup, four waves of BM/2 x BN/2 each, any
+// sizes and alignment. KB bytes of n per stage, two LDS buffers and one barrier a
+// stage: while a stage is multiplied the next one's global loads are in flight in
+// registers. KS groups of four waves take every KS-th stage and add up their sums
+// in LDS, for grids that leave CUs idle. 16-byte chunk c of tile row r sits at
+// slot r KB/16 + (c ^ sw(r)), so that the 16 rows a quarter of a wave reads at one
+// chunk fall in distinct banks.
+template <int BM, int BN, int KB, int KS>
+constexpr int tile_lds() {
+  return KS * 2 * (BM + BN) * KB;
+}
+template <typename Ty, int BM, int BN, int KB, int KS, bool YBF16>
+__global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void linear_tile_kernel(LinearArgs a) {
+  constexpr int CPR = KB / 16;
+  constexpr int RPL = 256 / CPR;               // rows one load of the group covers
+  constexpr int LX = BM / RPL, LW = BN / RPL;
+  constexpr int TM = BM / 32, TN = BN / 32;    // 16 x 16 tiles of a wave
+  static_assert(BM % RPL == 0 && BN % RPL == 0 && TM > 0 && TN > 0, "whole loads and tiles");
+  extern __shared__ __align__(16) i32x4 lds[];
+  const int tid = threadIdx.x & 255, lane = tid & 63, wave = tid >> 6;
+  const int grp = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  i32x4* const mine = lds + grp * 2 * (BM + BN) * CPR;
   const long long t0 = (long long)blockIdx.y * BM;
   const int c0 = blockIdx.x * BN;
   const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
   const long long kb = (long long)a.n * Ty::kSize;
+  const int lr = tid / CPR, lc = tid % CPR;
   const char* xs[LX];
   const char* ws[LW];
 #pragma unroll
-  for (int i = 0; i < LX; ++i) {
-    const int r = (i * kTileThr + tid) / 8;
-    xs[i] = static_cast<const char*>(a.X) + min(t0 + r, a.T - 1) * a.ldx * Ty::kSize;
-  }
+  for (int i = 0; i < LX; ++i)
+    xs[i] = static_cast<const char*>(a.X) + min(t0 + i * RPL + lr, a.T - 1) * a.ldx * Ty::kSize + lc * 16;
 #pragma unroll
-  for (int i = 0; i < LW; ++i) {
-    const int r = (i * kTileThr + tid) / 8;
-    ws[i] = static_cast<const char*>(a.W) + (long long)min(c0 + r, a.m - 1) * a.ldw * Ty::kSize;
-  }
-  const int kc = (tid & 7) * 16;
+  for (int i = 0; i < LW; ++i)
+    ws[i] = static_cast<const char*>(a.W) + (long long)min(c0 + i * RPL + lr, a.m - 1) * a.ldw * Ty::kSize + lc * 16;
   i32x4 xr[LX], wr[LW];
   auto fetch = [&](long long k0) {
-    const long long k = k0 + kc;
+    const long long left = kb - k0 - lc * 16;
+    if (k0 + KB <= kb) {   // every chunk of the stage is whole
 #pragma unroll
-    for (int i = 0; i < LX; ++i) xr[i] = load16<Ty::kSize>(xs[i] + k, kb - k);
+      for (int i = 0; i < LX; ++i) __builtin_memcpy(&xr[i], xs[i] + k0, 16);
 #pragma unroll
-    for (int i = 0; i < LW; ++i) wr[i] = load16<Ty::kSize>(ws[i] + k, kb - k);
+      for (int i = 0; i < LW; ++i) __builtin_memcpy(&wr[i], ws[i] + k0, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < LX; ++i) xr[i] = load16<Ty::kSize>(xs[i] + k0, left);
+#pragma unroll
+      for (int i = 0; i < LW; ++i) wr[i] = load16<Ty::kSize>(ws[i] + k0, left);
+    }
   };
-  auto slot = [](int r, int c) { return r * 8 + (c ^ ((r / 2) & 7)); };
+  auto slot = [](int r, int c) { return r * CPR + (c ^ (CPR == 8 ? (r / 2) & 7 : r & (CPR - 1))); };
+  auto keep = [&](int buf) {
+    i32x4* const to = mine + buf * (BM + BN) * CPR;
+#pragma unroll
+    for (int i = 0; i < LX; ++i) to[slot(i * RPL + lr, lc)] = xr[i];
+#pragma unroll
+    for (int i = 0; i < LW; ++i) to[BM * CPR + slot(i * RPL + lr, lc)] = wr[i];
+  };
   typename Ty::Acc acc[TM][TN] = {};
-  fetch(0);
-  for (long long k0 = 0; k0 < kb; k0 += kKB) {
-    __syncthreads();   // the stage before is read
-#pragma unroll
-    for (int i = 0; i < LX; ++i) lds[slot((i * kTileThr + tid) / 8, tid & 7)] = xr[i];
-#pragma unroll
-    for (int i = 0; i < LW; ++i) lds[BM * 8 + slot((i * kTileThr + tid) / 8, tid & 7)] = wr[i];
+  // the same number of stages for every group: those behind the end hold zeros
+  const int stages = (int)((kb + (long long)KB * KS - 1) / ((long long)KB * KS));
+  const long long first = (long long)grp * KB, step = (long long)KB * KS;
+  fetch(first);
+  keep(0);
+  if (stages > 1) fetch(first + step);
+  for (int s = 0; s < stages; ++s) {
     __syncthreads();
-    if (k0 + kKB < kb) fetch(k0 + kKB);
+    const i32x4* const from = mine + (s & 1) * (BM + BN) * CPR;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int q = 0; q < KB / 64; ++q) {
       i32x4 xf[TM], wf[TN];
-      const int c = s * 4 + (lane >> 4);
+      const int c = q * 4 + (lane >> 4);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) xf[i] = lds[slot(wm + i * 16 + (lane & 15), c)];
+      for (int i = 0; i < TM; ++i) xf[i] = from[slot(wm + i * 16 + (lane & 15), c)];
 #pragma unroll
-      for (int j = 0; j < TN; ++j) wf[j] = lds[BM * 8 + slot(wn + j * 16 + (lane & 15), c)];
+      for (int j = 0; j < TN; ++j) wf[j] = from[BM * CPR + slot(wn + j * 16 + (lane & 15), c)];
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) Ty::mma(wf[j], xf[i], acc[i][j]);
     }
+    if (s + 1 < stages) keep((s + 1) & 1);
+    if (s + 2 < stages) fetch(first + (s + 2) * step);
+  }
+  if constexpr (KS > 1) {
+    typedef typename Ty::Acc Acc;
+    static_assert((KS - 1) * BM * BN * 4 <= tile_lds<BM, BN, KB, KS>(), "sums fit where the stages were");
+    __syncthreads();   // the last stage is read
+    Acc* const sums = reinterpret_cast<Acc*>(lds);
+    if (grp > 0) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sums[(((grp - 1) * TM + i) * TN + j) * 256 + tid] = acc[i][j];
+    }
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int g = 0; g < KS - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] += sums[((g * TM + i) * TN + j) * 256 + tid];
   }
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -187,54 +181,131 @@ __global__ __launch_bounds__(kTileThr) void linear_tile_kernel(LinearArgs a) {
     }
 }
 
+template <typename Ty, int BM, int BN, int KB, int KS, bool YBF16>
+void tiles(const LinearArgs& a, hipStream_t s) {
+  // grid.y carries the token tiles: at most 65535 per launch
+  const long long step = 65535LL * BM;
+  for (long long t = 0; t < a.T; t += step) {
+    LinearArgs b = a;
+    b.T = std::min(step, a.T - t);
+    auto off = [](const void* p, long long bytes) {
+      return p ? static_cast<const void*>(static_cast<const char*>(p) + bytes) : nullptr;
+    };
+    const int ys = YBF16 ? 2 : 4;
+    b.X = off(a.X, t * a.ldx * Ty::kSize);
+    b.sx = static_cast<const float*>(off(a.sx, t * 4));
+    b.mul = off(a.mul, t * a.ldm * ys);
+    b.res = off(a.res, t * a.ldr * ys);
+    b.Y = const_cast<void*>(off(a.Y, t * a.ldy * ys));
+    hipLaunchKernelGGL((linear_tile_kernel<Ty, BM, BN, KB, KS, YBF16>),
+                       dim3((unsigned)((a.m + BN - 1) / BN), (unsigned)((b.T + BM - 1) / BM)), dim3(256 * KS),
+                       (tile_lds<BM, BN, KB, KS>()), s, b);
+  }
+}
+
 template <typename Ty, bool YBF16>
-hipError_t launch_typed(const LinearArgs& a, hipStream_t s) {
-  if (a.T <= 4) {
-    const int per = kRowThr / 64 * kRowsPerWave;
-    const dim3 grid((unsigned)((a.m + per - 1) / per));
-    if (a.T == 1) hipLaunchKernelGGL((linear_rows_kernel<Ty, 1, YBF16>), grid, dim3(kRowThr), 0, s, a);
-    else if (a.T == 2) hipLaunchKernelGGL((linear_rows_kernel<Ty, 2, YBF16>), grid, dim3(kRowThr), 0, s, a);
-    else hipLaunchKernelGGL((linear_rows_kernel<Ty, 4, YBF16>), grid, dim3(kRowThr), 0, s, a);
-  } else if (a.T <= 64) {
-    const dim3 grid((unsigned)((a.m + 15) / 16));
-    if (a.T <= 16) hipLaunchKernelGGL((linear_few_kernel<Ty, 1, YBF16>), grid, dim3(kFewThr), 0, s, a);
-    else if (a.T <= 32) hipLaunchKernelGGL((linear_few_kernel<Ty, 2, YBF16>), grid, dim3(kFewThr), 0, s, a);
-    else hipLaunchKernelGGL((linear_few_kernel<Ty, 4, YBF16>), grid, dim3(kFewThr), 0, s, a);
-  } else {
-    // grid.y carries the token tiles: at most 65535 per launch
-    constexpr int BM = 128, BN = 128;
-    const long long step = 65535LL * BM;
-    for (long long t = 0; t < a.T; t += step) {
-      LinearArgs b = a;
-      b.T = std::min(step, a.T - t);
-      auto off = [](const void* p, long long bytes) {
-        return p ? static_cast<const void*>(static_cast<const char*>(p) + bytes) : nullptr;
-      };
-      const int ys = YBF16 ? 2 : 4;
-      b.X = off(a.X, t * a.ldx * Ty::kSize);
-      b.sx = static_cast<const float*>(off(a.sx, t * 4));
-      b.mul = off(a.mul, t * a.ldm * ys);
-      b.res = off(a.res, t * a.ldr * ys);
-      b.Y = const_cast<void*>(off(a.Y, t * a.ldy * ys));
-      hipLaunchKernelGGL((linear_tile_kernel<Ty, BM, BN, YBF16>),
-                         dim3((unsigned)((a.m + BN - 1) / BN), (unsigned)((b.T + BM - 1) / BM)), dim3(kTileThr),
-                         0, s, b);
-    }
+hipError_t launch_tiles(const LinearArgs& a, int tile, hipStream_t s) {
+  switch (tile) {
+    case LINEAR_TILE_128: tiles<Ty, 128, 128, 128, 1, YBF16>(a, s); break;
+    case LINEAR_TILE_128x64: tiles<Ty, 128, 64, 128, 1, YBF16>(a, s); break;
+    case LINEAR_TILE_64: tiles<Ty, 64, 64, 256, 1, YBF16>(a, s); break;
+    case LINEAR_TILE_32x64: tiles<Ty, 32, 64, 256, 1, YBF16>(a, s); break;
+    case LINEAR_TILE_32_SPLIT: tiles<Ty, 32, 32, 256, 2, YBF16>(a, s); break;
+    default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
+}
+hipError_t launch_tiles(const LinearArgs& a, int type, int tile, hipStream_t s) {
+  switch (type) {
+    case LINEAR_F32: return launch_tiles<TypeF32, false>(a, tile, s);
+    case LINEAR_BF16:
+      return a.y_bf16 ? launch_tiles<TypeBf16, true>(a, tile, s) : launch_tiles<TypeBf16, false>(a, tile, s);
+  }
+  return a.y_bf16 ? launch_tiles<TypeI8, true>(a, tile, s) : launch_tiles<TypeI8, false>(a, tile, s);
+}
+
+template <typename Ty, int TT, bool YBF16>
+hipError_t rows(const LinearArgs& a, hipStream_t s) {
+  const int per = kRowThr / 64 * kRowsPerWave;
+  hipLaunchKernelGGL((linear_rows_kernel<Ty, TT, YBF16>), dim3((unsigned)((a.m + per - 1) / per)), dim3(kRowThr), 0, s,
+                     a);
+  return hipGetLastError();
+}
+template <typename Ty, bool YBF16>
+hipError_t rows(const LinearArgs& a, hipStream_t s) {
+  if (a.T == 1) return rows<Ty, 1, YBF16>(a, s);
+  if (a.T == 2) return rows<Ty, 2, YBF16>(a, s);
+  return rows<Ty, 4, YBF16>(a, s);
+}
+hipError_t launch_rows(const LinearArgs& a, int type, hipStream_t s) {
+  switch (type) {
+    case LINEAR_F32: return rows<TypeF32, false>(a, s);
+    case LINEAR_BF16: return a.y_bf16 ? rows<TypeBf16, true>(a, s) : rows<TypeBf16, false>(a, s);
+  }
+  return a.y_bf16 ? rows<TypeI8, true>(a, s) : rows<TypeI8, false>(a, s);
+}
+
+// What a tile costs, in us for 4 KB of every operand row (all of them scale with
+// the row): `first` for a grid of up to 256 tiles, one to a CU, and `round` for
+// every 256 tiles of a grid where the CUs are full; measured at 2048 x 2048
+// weights and 80 to 16384 tokens. bf16 and INT8 cost the same a byte; fp32 is bound
+// by its matrix rate, so its cost goes by the tile's area. E.g. bf16 1024 tokens:
+// 128 x 128 26.5 us, 128 x 64 15.7, 64 x 64 16.8, 32 x 32 27.9; 16384 tokens: 256 x
+// 256 108 us, 128 x 128 141, 128 x 64 173.
+struct Cost {
+  int tile, bm, bn;
+  float first, round;
+};
+constexpr Cost kRing[] = {
+    {LINEAR_TILE_256, 256, 256, 36, 50},      {LINEAR_TILE_128, 128, 128, 24, 17},
+    {LINEAR_TILE_128x64, 128, 64, 11, 9.5f},  {LINEAR_TILE_64, 64, 64, 6.5f, 5.8f},
+    {LINEAR_TILE_32x64, 32, 64, 4.6f, 4.3f},  {LINEAR_TILE_32, 32, 32, 3.7f, 2.8f},
+    {LINEAR_TILE_32_SPLIT, 32, 32, 3.2f, 3.2f}};
+constexpr Cost kRingF32[] = {
+    {LINEAR_TILE_128, 128, 128, 64, 60},   {LINEAR_TILE_128x64, 128, 64, 33, 30}, {LINEAR_TILE_64, 64, 64, 18, 16.5f},
+    {LINEAR_TILE_32x64, 32, 64, 10, 9},    {LINEAR_TILE_32, 32, 32, 6.5f, 5},     {LINEAR_TILE_32_SPLIT, 32, 32, 5, 7.3f}};
+constexpr Cost kTiles[] = {
+    {LINEAR_TILE_128, 128, 128, 25, 20},     {LINEAR_TILE_128x64, 128, 64, 16.5f, 13}, {LINEAR_TILE_64, 64, 64, 9, 8},
+    {LINEAR_TILE_32x64, 32, 64, 5.6f, 5},    {LINEAR_TILE_32_SPLIT, 32, 32, 3.2f, 3.3f}};
+constexpr Cost kTilesF32[] = {
+    {LINEAR_TILE_128, 128, 128, 75, 65},     {LINEAR_TILE_128x64, 128, 64, 42, 35}, {LINEAR_TILE_64, 64, 64, 23.7f, 18.5f},
+    {LINEAR_TILE_32x64, 32, 64, 15.6f, 10.5f}, {LINEAR_TILE_32_SPLIT, 32, 32, 8, 6.6f}};
+
+template <size_t N, typename F>
+int cheapest(const Cost (&costs)[N], const LinearArgs& a, F allowed) {
+  int best = -1;
+  double least = 0.0;
+  for (const Cost& c : costs) {
+    if (!allowed(c.tile)) continue;
+    const long long n = ((a.T + c.bm - 1) / c.bm) * ((a.m + c.bn - 1) / c.bn);
+    const double cost = std::max((double)c.first, (double)c.round * (double)((n + 255) / 256));
+    if (best < 0 || cost < least) {
+      best = c.tile;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s) {
   if (a.T <= 0 || a.m <= 0 || a.n <= 0) return hipErrorInvalidValue;
-  if (a.T > 256 && linear_pipe_supported(a, type)) return launch_linear_pipe(a, type, s);
-  switch (type) {
-    case LINEAR_F32: return a.y_bf16 ? hipErrorInvalidValue : launch_typed<TypeF32, false>(a, s);
-    case LINEAR_BF16: return a.y_bf16 ? launch_typed<TypeBf16, true>(a, s) : launch_typed<TypeBf16, false>(a, s);
-    case LINEAR_I8: return a.y_bf16 ? launch_typed<TypeI8, true>(a, s) : launch_typed<TypeI8, false>(a, s);
-  }
-  return hipErrorInvalidValue;
+  if (a.y_bf16 && type == LINEAR_F32) return hipErrorInvalidValue;
+  const bool ring = linear_ring_supported(a, type);
+  // One token goes by rows (2048 to 5632 bf16 6.4 us, 7.0 in tiles); with 2 to 4 the
+  // tiles are as fast or faster (2 tokens, 4096 to 11008 INT8 11.4 against 9.7 us).
+  if (a.T == 1 || (a.T <= 4 && !ring)) return launch_rows(a, type, s);
+  if (!ring)
+    return launch_tiles(a, type, type == LINEAR_F32 ? cheapest(kTilesF32, a, [](int) { return true; })
+                                                    : cheapest(kTiles, a, [](int) { return true; }), s);
+  const bool pipe = linear_pipe_supported(a, type);
+  const long long stages = (long long)a.n * (type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1) / 128;
+  const auto allowed = [&](int tile) {
+    return tile == LINEAR_TILE_256 ? pipe : tile == LINEAR_TILE_32_SPLIT ? stages % 2 == 0 : true;
+  };
+  const int tile = type == LINEAR_F32 ? cheapest(kRingF32, a, allowed) : cheapest(kRing, a, allowed);
+  return tile == LINEAR_TILE_256 ? launch_linear_pipe(a, type, s) : launch_linear_ring(a, type, tile, s);
 }
 
 }  // namespace poetx

@@ -1,0 +1,222 @@
+// The merged-weight product (k_linear.hip) where 256 x 256 tiles would leave CUs
+// idle: smaller tiles, one to a workgroup of four waves, with a ring of NS LDS
+// stages of 128 bytes of every operand row filled by direct-to-LDS loads. One
+// barrier a stage, in its middle: the products of a stage's first half run beside
+// the LDS reads of its second, those of the second half beside the loads of the
+// stage that takes its place and the reads of the next one's first half. (Reads,
+// loads and products one after the other: 31 against 22 us a 1024 x 2048 x 2048
+// bf16 product in 128 x 128 tiles; more stages in flight changed nothing.) With
+// KS = 2 a second group of four waves takes the other half of n, for grids that
+// leave CUs idle (16 x 2048 x 5632 7.5 -> 7.0 us, 16 x 5632 x 2048 14.1 -> 11.5 us).
+//
+// Rows past the last token or weight row are clamped to it (not stored).
+// Requirements (linear_ring_supported): 128-byte multiples of n, 16-byte rows.
+#include <algorithm>
+#include <type_traits>
+
+#include "linear_common.h"
+
+namespace poetx {
+namespace {
+
+using namespace lin;
+
+constexpr int kThr = 256;
+constexpr int kKB = 128;          // bytes of a row per stage
+constexpr int kGroupRows = 4;     // tile-rows per group of the XCD-aware order
+
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void lds_sync() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// 16 bytes per lane from base + off + k (below `bytes`) to lane * 16 behind `to`
+__device__ __forceinline__ void load_lds(const char* base, int bytes, unsigned char* to, uint32_t off, int k) {
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, bytes, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)to, 16, off, k, 0, 0);
+}
+
+template <typename Ty, int BM, int BN, int NS, int KS, bool YBF16>
+__global__ __launch_bounds__(kThr * KS)
+__attribute__((amdgpu_waves_per_eu(std::max(2, KS), std::max(2, KS))))
+void linear_ring_kernel(LinearArgs p) {
+  constexpr int LX = BM / 32, LW = BN / 32;    // loads of a lane per stage: 32 rows each
+  constexpr int TM = BM / 32, TN = BN / 32;    // 16 x 16 tiles of a wave (2 x 2 waves)
+  constexpr int STAGE = (BM + BN) * kKB;
+  static_assert(NS * (LX + LW) <= 63, "loads in flight");
+  extern __shared__ __align__(16) unsigned char lds[];
+  const int tid = threadIdx.x & 255, lane = tid & 63;
+  const int grp_k = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  unsigned char* const ring = lds + grp_k * NS * STAGE;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
+
+  // XCD x = blockIdx.x % 8 takes the tiles [ntile x / 8, ntile (x + 1) / 8), in
+  // groups of kGroupRows tile-rows
+  const int tn = (p.m + BN - 1) / BN, tm = (int)((p.T + BM - 1) / BM), ntile = tn * tm;
+  const int x = blockIdx.x % 8;
+  const int lin = (int)((long long)ntile * x / 8) + (int)blockIdx.x / 8;
+  if (lin >= (int)((long long)ntile * (x + 1) / 8)) return;
+  const int grp = lin / (kGroupRows * tn), first = grp * kGroupRows;
+  const int gsz = min(kGroupRows, tm - first), in = lin - grp * (kGroupRows * tn);
+  const int m0 = __builtin_amdgcn_readfirstlane((first + in % gsz) * BM);
+  const int n0 = __builtin_amdgcn_readfirstlane((in / gsz) * BN);
+
+  const int lda = (int)(p.ldx * Ty::kSize), ldb = (int)(p.ldw * Ty::kSize);
+  const int lr = tid / 8;
+  const uint32_t lc = (uint32_t)((tid & 7) ^ ((lr / 2) & 7)) * 16;
+  const int rx = (int)min((long long)BM, p.T - m0), rw = min(BN, p.m - n0);   // rows that exist
+  uint32_t vx[LX], vw[LW];
+#pragma unroll
+  for (int i = 0; i < LX; ++i) vx[i] = (uint32_t)(min(i * 32 + lr, rx - 1) * lda) + lc;
+#pragma unroll
+  for (int i = 0; i < LW; ++i) vw[i] = (uint32_t)(min(i * 32 + lr, rw - 1) * ldb) + lc;
+  const char* const bx = static_cast<const char*>(p.X) + (long long)m0 * lda;
+  const char* const bw = static_cast<const char*>(p.W) + (long long)n0 * ldb;
+  const int nk = (int)((long long)p.n * Ty::kSize / kKB) / KS;   // stages of a group, a piece of n in a row
+  const int k0 = grp_k * nk * kKB;
+
+  // stage s (past the end: the last one again, into a buffer nobody reads)
+  auto issue = [&](int s, int buf) __attribute__((always_inline)) {
+    const int k = k0 + min(s, nk - 1) * kKB;
+    unsigned char* st = ring + buf * STAGE + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < LX; ++i) load_lds(bx, rx * lda, st + i * 4096, vx[i], k);
+#pragma unroll
+    for (int i = 0; i < LW; ++i) load_lds(bw, rw * ldb, st + BM * kKB + i * 4096, vw[i], k);
+  };
+  // chunk c of row r at slot 8 r + (c ^ ((r / 2) & 7))
+  auto frag = [&](const unsigned char* st, int r, int c) __attribute__((always_inline)) {
+    return *reinterpret_cast<const i32x4*>(st + r * kKB + ((c ^ ((r / 2) & 7)) * 16));
+  };
+
+  typename Ty::Acc acc[TM][TN] = {};
+  i32x4 xf[2][TM], wf[2][TN];
+  // fragments of the first (q = 0) or second 64-byte slab of a stage
+  auto read = [&](int buf, int q) __attribute__((always_inline)) {
+    const unsigned char* st = ring + buf * STAGE;
+    const int c = q * 4 + (lane >> 4);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) xf[q][i] = frag(st, wm + i * 16 + (lane & 15), c);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) wf[q][j] = frag(st + BM * kKB, wn + j * 16 + (lane & 15), c);
+  };
+  auto multiply = [&](int q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) Ty::mma(wf[q][j], xf[q][i], acc[i][j]);
+  };
+  // The reads (and loads) of a half stage go out between its products
+  constexpr int PM = std::max(1, TM * TN * (Ty::kSize == 4 ? 4 : 1) / (TM + TN));   // products a read
+  constexpr int PL = (LX + LW + TM + TN - 1) / (TM + TN);                           // loads a read
+  auto spread = [](auto loads) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < TM + TN; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x008, PM, 0);
+      if (decltype(loads)::value) __builtin_amdgcn_sched_group_barrier(0x020, PL, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < NS; ++s) issue(s, s);
+  vm_wait<(NS - 1) * (LX + LW)>();   // this wave's part of stage 0 landed
+  lds_sync();                        // and everyone's
+  read(0, 0);
+  int buf = 0;
+  for (int s = 0; s < nk; ++s) {
+    const int next = buf + 1 == NS ? 0 : buf + 1;
+    read(buf, 1);
+    multiply(0);
+    spread(std::false_type{});
+    __builtin_amdgcn_sched_barrier(0);
+    vm_wait<(NS - 2) * (LX + LW)>();
+    lds_sync();   // stage s + 1 landed, and nobody reads stage s any more
+    issue(s + NS, buf);
+    read(next, 0);
+    multiply(1);
+    spread(std::true_type{});
+    __builtin_amdgcn_sched_barrier(0);
+    buf = next;
+  }
+  // the last loads went into buffers nobody reads: let them land before the
+  // workgroup's LDS is released
+  vm_wait<0>();
+  if constexpr (KS > 1) {
+    typedef typename Ty::Acc Acc;
+    static_assert((KS - 1) * BM * BN * 4 <= KS * NS * STAGE, "sums fit where the stages were");
+    __syncthreads();   // every group's loads landed
+    Acc* const sums = reinterpret_cast<Acc*>(lds);
+    if (grp_k > 0) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sums[(((grp_k - 1) * TM + i) * TN + j) * kThr + tid] = acc[i][j];
+    }
+    __syncthreads();
+    if (grp_k > 0) return;
+#pragma unroll
+    for (int g = 0; g < KS - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] += sums[((g * TM + i) * TN + j) * kThr + tid];
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const long long t = (long long)m0 + wm + i * 16 + (lane & 15);
+      const int c = n0 + wn + j * 16 + 4 * (lane >> 4);
+      if (t < p.T && c < p.m) {
+        const typename Ty::Sum o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        finish<YBF16>(p, o, t, c);
+      }
+    }
+}
+
+template <typename Ty, int BM, int BN, int NS, int KS, bool YBF16>
+hipError_t tiles(const LinearArgs& a, hipStream_t s) {
+  const long long ntile = ((a.T + BM - 1) / BM) * ((a.m + BN - 1) / BN);
+  hipLaunchKernelGGL((linear_ring_kernel<Ty, BM, BN, NS, KS, YBF16>), dim3((unsigned)((ntile + 7) / 8 * 8)),
+                     dim3(kThr * KS), KS * NS * (BM + BN) * kKB, s, a);
+  return hipGetLastError();
+}
+
+template <typename Ty, bool YBF16>
+hipError_t launch(const LinearArgs& a, int tile, hipStream_t s) {
+  switch (tile) {
+    case LINEAR_TILE_128: return tiles<Ty, 128, 128, 2, 1, YBF16>(a, s);
+    case LINEAR_TILE_128x64: return tiles<Ty, 128, 64, 3, 1, YBF16>(a, s);
+    case LINEAR_TILE_64: return tiles<Ty, 64, 64, 4, 1, YBF16>(a, s);
+    case LINEAR_TILE_32x64: return tiles<Ty, 32, 64, 4, 1, YBF16>(a, s);
+    case LINEAR_TILE_32: return tiles<Ty, 32, 32, 4, 1, YBF16>(a, s);
+    case LINEAR_TILE_32_SPLIT: return tiles<Ty, 32, 32, 4, 2, YBF16>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+bool linear_ring_supported(const LinearArgs& a, int type) {
+  const int es = type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1;
+  if ((long long)a.n * es % kKB || a.ldx * es % 16 || a.ldw * es % 16) return false;
+  if (((uintptr_t)a.X | (uintptr_t)a.W) & 15) return false;
+  // 256 rows within 32-bit offsets, tile numbers in 32 bits
+  return a.ldx * es * 256 < (1LL << 31) && a.ldw * es * 256 < (1LL << 31) &&
+         (a.T / 32 + 1) * (a.m / 32 + 1) < (1LL << 28);
+}
+
+hipError_t launch_linear_ring(const LinearArgs& a, int type, int tile, hipStream_t s) {
+  switch (type) {
+    case LINEAR_F32: return launch<TypeF32, false>(a, tile, s);
+    case LINEAR_BF16: return a.y_bf16 ? launch<TypeBf16, true>(a, tile, s) : launch<TypeBf16, false>(a, tile, s);
+  }
+  return a.y_bf16 ? launch<TypeI8, true>(a, tile, s) : launch<TypeI8, false>(a, tile, s);
+}
+
+}  // namespace poetx

@@ -295,5 +295,12 @@ hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s);
 // 256 x 256 tiles with one load pipeline (k_linear_pipe.hip): bf16 and INT8
 bool linear_pipe_supported(const LinearArgs& a, int type);
 hipError_t launch_linear_pipe(const LinearArgs& a, int type, hipStream_t s);
+// smaller tiles with a ring of LDS stages (k_linear_ring.hip): every type
+bool linear_ring_supported(const LinearArgs& a, int type);
+enum LinearTile {
+  LINEAR_TILE_256, LINEAR_TILE_128, LINEAR_TILE_128x64, LINEAR_TILE_64, LINEAR_TILE_32x64, LINEAR_TILE_32,
+  LINEAR_TILE_32_SPLIT   // 32 x 32, two groups of waves share n
+};
+hipError_t launch_linear_ring(const LinearArgs& a, int type, int tile, hipStream_t s);
 
 }  // namespace poetx

@@ -346,6 +346,28 @@ def test_linear(T, n, m, dt):
         close(f"{act} {parts}", run_linear(c, act), v, tol)
 
 
+# grids that take each tile, with whole rows of 128 bytes and with ragged ones; ends inside tiles
+@pytest.mark.parametrize("dt", ["bf16", "f32", "int8"])
+@pytest.mark.parametrize("T, m", [(30, 2047), (130, 4096), (500, 2040), (1030, 2040), (4090, 2056), (16380, 1032),
+                                  (16390, 1032)])
+@pytest.mark.parametrize("n", [70, 256])
+def test_linear_tiles(T, n, m, dt):
+    """Every part of the epilogue, written over the residual; the rows behind stay as they were."""
+    import torch
+    log(f"linear tiles T={T} n={n} m={m} {dt}")
+    c = linear_case(T + n + m, T, n, m, dt, "bmr")
+    v, tol = linear_ref(c, "silu", HALF["f32" if dt == "f32" else "bf16"])
+    buf = torch.full((T + 300, m + 8), 3.0, dtype=c["res"].dtype, device="cuda")
+    res = buf[:T, :m]
+    res.copy_(c["res"])
+    y = run_linear(c, "silu", residual=res, out=res)
+    close("over the residual", y, v, tol)
+    assert bool((buf[T:] == 3).all()) and bool((buf[:, m:] == 3).all())
+    first = y.clone()
+    res.copy_(c["res"])
+    assert torch.equal(run_linear(c, "silu", residual=res, out=res), first)   # the same bits again
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dt", ["bf16", "f32", "int8"])
 @pytest.mark.parametrize("T, n, m", [(1, 80, 70), (20, 96, 70), (150, 72, 131), (600, 256, 260)])
@@ -359,14 +381,16 @@ def test_linear_epilogues(T, n, m, dt, act):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "int8"])
-@pytest.mark.parametrize("T", [1, 20, 200, 700])
-def test_linear_fp32_result(T, dt):
+@pytest.mark.parametrize("T, n, m", [(1, 200, 72), (20, 256, 72), (200, 200, 72), (700, 256, 520), (16390, 128, 1032)])
+def test_linear_fp32_result(T, n, m, dt):
     import torch
-    c = linear_case(T, T, 200, 72, dt, "b")
-    v, tol = linear_ref(c, "none", HALF["f32"])
-    y = run_linear(c, "none", out_dtype=torch.float32)
-    assert y.dtype == torch.float32
-    close("fp32", y, v, tol)
+    for act, parts in (("none", "b"), ("relu", "bmr")):
+        c = linear_case(T, T, n, m, dt, parts)
+        c["mul"], c["res"] = (None if t is None else t.float() for t in (c["mul"], c["res"]))
+        v, tol = linear_ref(c, act, HALF["f32"])
+        y = run_linear(c, act, out_dtype=torch.float32)
+        assert y.dtype == torch.float32
+        close("fp32", y, v, tol)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32", "int8"])

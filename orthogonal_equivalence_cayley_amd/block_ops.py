@@ -13,7 +13,7 @@ columns and any row stride.
 """
 from __future__ import annotations
 
-import ctypes
+import operator
 from array import array
 from typing import NamedTuple, Optional, Sequence
 
@@ -26,6 +26,7 @@ _REAL = (torch.bfloat16, torch.float32)
 _REAL_SET = frozenset(_REAL)
 _ACT = {name: i for i, name in enumerate(_px.ACTS)}
 _LIB = _px.LIB
+_dtype_of = operator.attrgetter("dtype")
 _raw_stream = torch._C._cuda_getCurrentRawStream   # of one GPU, without a Stream object around it
 
 
@@ -204,6 +205,14 @@ class MergedLinear:
         return linear(X, self.W, self.bias, act, mul, residual, x_scale, self.w_scale, out, out_dtype)
 
 
+def _facts(tensors, dev: int):
+    """dtypes, element counts, addresses, and whether all are contiguous and on GPU dev."""
+    T = torch.Tensor
+    ok = all(map(T.is_contiguous, tensors)) and set(map(T.get_device, tensors)) == {dev}
+    return (list(map(_dtype_of, tensors)), array("q", map(T.numel, tensors)),
+            array("Q", map(T.data_ptr, tensors)), ok)
+
+
 def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
                out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
     """The global 2-norm over all gradient tensors (fp32, one value, on the GPU)
@@ -219,27 +228,27 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float,
     dev = first.get_device()
     if dev < 0:
         raise ValueError(f"gradients are on {first.device}, expected a GPU")
-    types = [g.dtype for g in grads]
-    ns = [g.numel() for g in grads]
-    if not _REAL_SET.issuperset(types) or not all([g.get_device() == dev for g in grads]) or \
-            not all([g.is_contiguous() for g in grads]):
+    # a step's gradients are hundreds of tensors: each question is one pass in C over all of them
+    types, ns, ptrs, ok = _facts(grads, dev)
+    if not ok or not _REAL_SET.issuperset(types):
         raise ValueError("gradients must be contiguous bf16 or fp32 tensors of one GPU")
-    ptrs = array("Q", [g.data_ptr() for g in grads])
-    sizes, codes = array("q", ns), array("i", [_PX_DTYPE[t] for t in types])
+    codes = array("i", map(_PX_DTYPE.__getitem__, types))
     outs = None
     if out is not None:
         out = list(out)
         if len(out) != n:
             raise ValueError(f"{len(out)} outputs for {n} gradients")
-        if [o.dtype for o in out] != types or [o.numel() for o in out] != ns or \
-                not all([o.get_device() == dev for o in out]) or not all([o.is_contiguous() for o in out]):
+        if all(map(operator.is_, out, grads)):
+            o_types, o_ns, outs = types, ns, ptrs
+        else:
+            o_types, o_ns, outs, ok = _facts(out, dev)
+        if not ok or o_types != types or o_ns != ns:
             raise ValueError("an output differs from its gradient in size, dtype or device, or is not "
                              "contiguous")
-        outs = array("Q", [o.data_ptr() for o in out])
     norm = torch.empty((), dtype=torch.float32, device=first.device)
     wsb = _LIB.poetx_clip_grads_workspace(n)
     ws = torch.empty(wsb, dtype=torch.uint8, device=first.device)
-    _call(_LIB.poetx_clip_grads, "poetx_clip_grads", dev, n, ptrs.buffer_info()[0], sizes.buffer_info()[0],
+    _call(_LIB.poetx_clip_grads, "poetx_clip_grads", dev, n, ptrs.buffer_info()[0], ns.buffer_info()[0],
           codes.buffer_info()[0], None if outs is None else outs.buffer_info()[0], max_norm, norm.data_ptr(),
           ws.data_ptr(), wsb)
     return norm

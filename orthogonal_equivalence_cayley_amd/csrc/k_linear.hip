@@ -40,13 +40,31 @@ __global__ __launch_bounds__(kRowThr) void linear_rows_kernel(LinearArgs a) {
   for (int t = 0; t < TT; ++t)
     x[t] = static_cast<const char*>(a.X) + (long long)min((long long)t, a.T - 1) * a.ldx * Ty::kSize;
   typename Ty::Sum acc[TT][R] = {};
-#pragma unroll 4
-  for (long long k = lane * 16; k < kb; k += 1024) {
+  // pieces of 1 KB, four at a time with all their loads out first
+  constexpr int U = 4;
+  long long k = lane * 16;
+  for (; k - lane * 16 + 1024 * U <= kb; k += 1024 * U) {
+    i32x4 wv[U][R], xv[U][TT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) __builtin_memcpy(&wv[u][r], w[r] + k + u * 1024, 16);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) __builtin_memcpy(&xv[u][t], x[t] + k + u * 1024, 16);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int r = 0; r < R; ++r) Ty::dot(wv[u][r], xv[u][t], acc[t][r]);
+  }
+  for (; k - lane * 16 < kb; k += 1024) {
     i32x4 wv[R], xv[TT];
 #pragma unroll
-    for (int r = 0; r < R; ++r) wv[r] = load16<Ty::kSize>(w[r] + k, kb - k);
+    for (int r = 0; r < R; ++r) wv[r] = load16<Ty::kSize>(w[r], k, kb);
 #pragma unroll
-    for (int t = 0; t < TT; ++t) xv[t] = load16<Ty::kSize>(x[t] + k, kb - k);
+    for (int t = 0; t < TT; ++t) xv[t] = load16<Ty::kSize>(x[t], k, kb);
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -63,13 +81,19 @@ __global__ __launch_bounds__(kRowThr) void linear_rows_kernel(LinearArgs a) {
 }
 
 // ------------------------------------------------------------------ tiles
+// Barrier that waits for this wave's LDS traffic only: global loads stay in flight.
+__device__ __forceinline__ void lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // BM tokens x BN rows of W per workgroup, four waves of BM/2 x BN/2 each, any
 // sizes and alignment. KB bytes of n per stage, two LDS buffers and one barrier a
-// stage: while a stage is multiplied the next one's global loads are in flight in
-// registers. KS groups of four waves take every KS-th stage and add up their sums
-// in LDS, for grids that leave CUs idle. 16-byte chunk c of tile row r sits at
-// slot r KB/16 + (c ^ sw(r)), so that the 16 rows a quarter of a wave reads at one
-// chunk fall in distinct banks.
+// stage; the global loads of the next two stages are under way in registers, and
+// the LDS reads of the next 64-byte slab beside the products of one. KS groups of
+// four waves take every KS-th stage and add up their sums in LDS, for grids that
+// leave CUs idle. 16-byte chunk c of tile row r sits at slot r KB/16 + (c ^ sw(r)),
+// so that the 16 rows a quarter of a wave reads at one chunk fall in distinct
+// banks. Measured: 1000 x 999 x 1000 bf16 12.5 us, 16384 x 1001 x 2001 137 us
+// (480 TFLOP/s), 1531 x 1005 x 707 fp32 39 us (56 TFLOP/s; the matrix units alone
+// would take 23 for the three tiles the fullest CU gets).
 template <int BM, int BN, int KB, int KS>
 constexpr int tile_lds() {
   return KS * 2 * (BM + BN) * KB;
@@ -86,8 +110,9 @@ void linear_tile_kernel(LinearArgs a) {
   const int tid = threadIdx.x & 255, lane = tid & 63, wave = tid >> 6;
   const int grp = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   i32x4* const mine = lds + grp * 2 * (BM + BN) * CPR;
-  const long long t0 = (long long)blockIdx.y * BM;
-  const int c0 = blockIdx.x * BN;
+  int m0, c0;
+  if (!tile_origin(a.T, a.m, BM, BN, m0, c0)) return;
+  const long long t0 = m0;
   const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
   const long long kb = (long long)a.n * Ty::kSize;
   const int lr = tid / CPR, lc = tid % CPR;
@@ -95,58 +120,75 @@ void linear_tile_kernel(LinearArgs a) {
   const char* ws[LW];
 #pragma unroll
   for (int i = 0; i < LX; ++i)
-    xs[i] = static_cast<const char*>(a.X) + min(t0 + i * RPL + lr, a.T - 1) * a.ldx * Ty::kSize + lc * 16;
+    xs[i] = static_cast<const char*>(a.X) + min(t0 + i * RPL + lr, a.T - 1) * a.ldx * Ty::kSize;
 #pragma unroll
   for (int i = 0; i < LW; ++i)
-    ws[i] = static_cast<const char*>(a.W) + (long long)min(c0 + i * RPL + lr, a.m - 1) * a.ldw * Ty::kSize + lc * 16;
-  i32x4 xr[LX], wr[LW];
-  auto fetch = [&](long long k0) {
-    const long long left = kb - k0 - lc * 16;
+    ws[i] = static_cast<const char*>(a.W) + (long long)min(c0 + i * RPL + lr, a.m - 1) * a.ldw * Ty::kSize;
+  i32x4 xr[2][LX], wr[2][LW];   // two stages under way
+  auto fetch = [&](long long k0, int set) __attribute__((always_inline)) {
+    const long long k = k0 + lc * 16;
     if (k0 + KB <= kb) {   // every chunk of the stage is whole
 #pragma unroll
-      for (int i = 0; i < LX; ++i) __builtin_memcpy(&xr[i], xs[i] + k0, 16);
+      for (int i = 0; i < LX; ++i) __builtin_memcpy(&xr[set][i], xs[i] + k, 16);
 #pragma unroll
-      for (int i = 0; i < LW; ++i) __builtin_memcpy(&wr[i], ws[i] + k0, 16);
+      for (int i = 0; i < LW; ++i) __builtin_memcpy(&wr[set][i], ws[i] + k, 16);
     } else {
 #pragma unroll
-      for (int i = 0; i < LX; ++i) xr[i] = load16<Ty::kSize>(xs[i] + k0, left);
+      for (int i = 0; i < LX; ++i) xr[set][i] = load16<Ty::kSize>(xs[i], k, kb);
 #pragma unroll
-      for (int i = 0; i < LW; ++i) wr[i] = load16<Ty::kSize>(ws[i] + k0, left);
+      for (int i = 0; i < LW; ++i) wr[set][i] = load16<Ty::kSize>(ws[i], k, kb);
     }
   };
   auto slot = [](int r, int c) { return r * CPR + (c ^ (CPR == 8 ? (r / 2) & 7 : r & (CPR - 1))); };
-  auto keep = [&](int buf) {
+  auto keep = [&](int buf, int set) __attribute__((always_inline)) {
     i32x4* const to = mine + buf * (BM + BN) * CPR;
 #pragma unroll
-    for (int i = 0; i < LX; ++i) to[slot(i * RPL + lr, lc)] = xr[i];
+    for (int i = 0; i < LX; ++i) to[slot(i * RPL + lr, lc)] = xr[set][i];
 #pragma unroll
-    for (int i = 0; i < LW; ++i) to[BM * CPR + slot(i * RPL + lr, lc)] = wr[i];
+    for (int i = 0; i < LW; ++i) to[BM * CPR + slot(i * RPL + lr, lc)] = wr[set][i];
   };
   typename Ty::Acc acc[TM][TN] = {};
   // the same number of stages for every group: those behind the end hold zeros
   const int stages = (int)((kb + (long long)KB * KS - 1) / ((long long)KB * KS));
   const long long first = (long long)grp * KB, step = (long long)KB * KS;
-  fetch(first);
-  keep(0);
-  if (stages > 1) fetch(first + step);
-  for (int s = 0; s < stages; ++s) {
-    __syncthreads();
-    const i32x4* const from = mine + (s & 1) * (BM + BN) * CPR;
+  constexpr int Q = KB / 64;   // slabs of a stage
+  static_assert(Q % 2 == 0, "fragment sets alternate across stages");
+  i32x4 xf[2][TM], wf[2][TN];
+  auto read = [&](int buf, int q) __attribute__((always_inline)) {
+    const i32x4* const from = mine + buf * (BM + BN) * CPR;
+    const int c = q * 4 + (lane >> 4);
 #pragma unroll
-    for (int q = 0; q < KB / 64; ++q) {
-      i32x4 xf[TM], wf[TN];
-      const int c = q * 4 + (lane >> 4);
+    for (int i = 0; i < TM; ++i) xf[q & 1][i] = from[slot(wm + i * 16 + (lane & 15), c)];
 #pragma unroll
-      for (int i = 0; i < TM; ++i) xf[i] = from[slot(wm + i * 16 + (lane & 15), c)];
+    for (int j = 0; j < TN; ++j) wf[q & 1][j] = from[BM * CPR + slot(wn + j * 16 + (lane & 15), c)];
+  };
+  fetch(first, 0);
+  keep(0, 0);
+  if (stages > 1) fetch(first + step, 1);
+  if (stages > 2) fetch(first + 2 * step, 0);
+  lds_sync();
+  read(0, 0);
+  auto stage = [&](int s, int buf) __attribute__((always_inline)) {
+    // nobody reads the other buffer since the barrier of the stage before
+    if (s + 1 < stages) keep(buf ^ 1, buf ^ 1);
+    if (s + 3 < stages) fetch(first + (s + 3) * step, buf ^ 1);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) wf[j] = from[BM * CPR + slot(wn + j * 16 + (lane & 15), c)];
+    for (int q = 0; q < Q; ++q) {
+      if (q + 1 < Q) {
+        read(buf, q + 1);
+      } else {
+        lds_sync();
+        if (s + 1 < stages) read(buf ^ 1, 0);
+      }
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) Ty::mma(wf[j], xf[i], acc[i][j]);
+        for (int j = 0; j < TN; ++j) Ty::mma(wf[q & 1][j], xf[q & 1][i], acc[i][j]);
     }
-    if (s + 1 < stages) keep((s + 1) & 1);
-    if (s + 2 < stages) fetch(first + (s + 2) * step);
+  };
+  for (int s = 0; s < stages; s += 2) {
+    stage(s, 0);
+    if (s + 1 < stages) stage(s + 1, 1);
   }
   if constexpr (KS > 1) {
     typedef typename Ty::Acc Acc;
@@ -183,8 +225,8 @@ void linear_tile_kernel(LinearArgs a) {
 
 template <typename Ty, int BM, int BN, int KB, int KS, bool YBF16>
 void tiles(const LinearArgs& a, hipStream_t s) {
-  // grid.y carries the token tiles: at most 65535 per launch
-  const long long step = 65535LL * BM;
+  // tokens of one launch, so that tile numbers stay in 32 bits (T itself does)
+  const long long step = std::max(1LL, kMaxTiles / ((a.m + BN - 1) / BN)) * BM;
   for (long long t = 0; t < a.T; t += step) {
     LinearArgs b = a;
     b.T = std::min(step, a.T - t);
@@ -198,7 +240,7 @@ void tiles(const LinearArgs& a, hipStream_t s) {
     b.res = off(a.res, t * a.ldr * ys);
     b.Y = const_cast<void*>(off(a.Y, t * a.ldy * ys));
     hipLaunchKernelGGL((linear_tile_kernel<Ty, BM, BN, KB, KS, YBF16>),
-                       dim3((unsigned)((a.m + BN - 1) / BN), (unsigned)((b.T + BM - 1) / BM)), dim3(256 * KS),
+                       dim3((unsigned)tile_grid(b.T, b.m, BM, BN)), dim3(256 * KS),
                        (tile_lds<BM, BN, KB, KS>()), s, b);
   }
 }
@@ -209,7 +251,7 @@ hipError_t launch_tiles(const LinearArgs& a, int tile, hipStream_t s) {
     case LINEAR_TILE_128: tiles<Ty, 128, 128, 128, 1, YBF16>(a, s); break;
     case LINEAR_TILE_128x64: tiles<Ty, 128, 64, 128, 1, YBF16>(a, s); break;
     case LINEAR_TILE_64: tiles<Ty, 64, 64, 256, 1, YBF16>(a, s); break;
-    case LINEAR_TILE_32x64: tiles<Ty, 32, 64, 256, 1, YBF16>(a, s); break;
+    case LINEAR_TILE_32x64: tiles<Ty, 32, 64, 128, 1, YBF16>(a, s); break;
     case LINEAR_TILE_32_SPLIT: tiles<Ty, 32, 32, 256, 2, YBF16>(a, s); break;
     default: return hipErrorInvalidValue;
   }
@@ -265,7 +307,7 @@ constexpr Cost kRingF32[] = {
     {LINEAR_TILE_128, 128, 128, 64, 60},   {LINEAR_TILE_128x64, 128, 64, 33, 30}, {LINEAR_TILE_64, 64, 64, 18, 16.5f},
     {LINEAR_TILE_32x64, 32, 64, 10, 9},    {LINEAR_TILE_32, 32, 32, 6.5f, 5},     {LINEAR_TILE_32_SPLIT, 32, 32, 5, 7.3f}};
 constexpr Cost kTiles[] = {
-    {LINEAR_TILE_128, 128, 128, 25, 20},     {LINEAR_TILE_128x64, 128, 64, 16.5f, 13}, {LINEAR_TILE_64, 64, 64, 9, 8},
+    {LINEAR_TILE_128, 128, 128, 25, 20},     {LINEAR_TILE_128x64, 128, 64, 16.5f, 13}, {LINEAR_TILE_64, 64, 64, 10.5f, 8},
     {LINEAR_TILE_32x64, 32, 64, 5.6f, 5},    {LINEAR_TILE_32_SPLIT, 32, 32, 3.2f, 3.3f}};
 constexpr Cost kTilesF32[] = {
     {LINEAR_TILE_128, 128, 128, 75, 65},     {LINEAR_TILE_128x64, 128, 64, 42, 35}, {LINEAR_TILE_64, 64, 64, 23.7f, 18.5f},

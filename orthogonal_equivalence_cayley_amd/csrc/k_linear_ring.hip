@@ -23,7 +23,6 @@ using namespace lin;
 
 constexpr int kThr = 256;
 constexpr int kKB = 128;          // bytes of a row per stage
-constexpr int kGroupRows = 4;     // tile-rows per group of the XCD-aware order
 
 template <int N>
 __device__ __forceinline__ void vm_wait() {
@@ -55,17 +54,8 @@ void linear_ring_kernel(LinearArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
 
-  // XCD x = blockIdx.x % 8 takes the tiles [ntile x / 8, ntile (x + 1) / 8), in
-  // groups of kGroupRows tile-rows
-  const int tn = (p.m + BN - 1) / BN, tm = (int)((p.T + BM - 1) / BM), ntile = tn * tm;
-  const int x = blockIdx.x % 8;
-  const int lin = (int)((long long)ntile * x / 8) + (int)blockIdx.x / 8;
-  if (lin >= (int)((long long)ntile * (x + 1) / 8)) return;
-  const int grp = lin / (kGroupRows * tn), first = grp * kGroupRows;
-  const int gsz = min(kGroupRows, tm - first), in = lin - grp * (kGroupRows * tn);
-  const int m0 = __builtin_amdgcn_readfirstlane((first + in % gsz) * BM);
-  const int n0 = __builtin_amdgcn_readfirstlane((in / gsz) * BN);
-
+  int m0, n0;
+  if (!tile_origin(p.T, p.m, BM, BN, m0, n0)) return;
   const int lda = (int)(p.ldx * Ty::kSize), ldb = (int)(p.ldw * Ty::kSize);
   const int lr = tid / 8;
   const uint32_t lc = (uint32_t)((tid & 7) ^ ((lr / 2) & 7)) * 16;
@@ -181,8 +171,7 @@ void linear_ring_kernel(LinearArgs p) {
 
 template <typename Ty, int BM, int BN, int NS, int KS, bool YBF16>
 hipError_t tiles(const LinearArgs& a, hipStream_t s) {
-  const long long ntile = ((a.T + BM - 1) / BM) * ((a.m + BN - 1) / BN);
-  hipLaunchKernelGGL((linear_ring_kernel<Ty, BM, BN, NS, KS, YBF16>), dim3((unsigned)((ntile + 7) / 8 * 8)),
+  hipLaunchKernelGGL((linear_ring_kernel<Ty, BM, BN, NS, KS, YBF16>), dim3((unsigned)tile_grid(a.T, a.m, BM, BN)),
                      dim3(kThr * KS), KS * NS * (BM + BN) * kKB, s, a);
   return hipGetLastError();
 }
@@ -208,7 +197,7 @@ bool linear_ring_supported(const LinearArgs& a, int type) {
   if (((uintptr_t)a.X | (uintptr_t)a.W) & 15) return false;
   // 256 rows within 32-bit offsets, tile numbers in 32 bits
   return a.ldx * es * 256 < (1LL << 31) && a.ldw * es * 256 < (1LL << 31) &&
-         (a.T / 32 + 1) * (a.m / 32 + 1) < (1LL << 28);
+         (a.T / 32 + 1) * (a.m / 32 + 1) < kMaxTiles;
 }
 
 hipError_t launch_linear_ring(const LinearArgs& a, int type, int tile, hipStream_t s) {

@@ -62,29 +62,58 @@ struct TypeF32 {
   }
 };
 
-// 16 bytes at p, of which `left` (a multiple of the element size) belong to the
-// row; what is behind them counts as zero and is not read. Global loads take
-// any alignment on this target.
+// 16 bytes of a row of kb bytes from byte k on; what is behind its end counts as
+// zero and is not read. Global loads take any alignment on this target. A chunk
+// the end cuts is the row's last 16 bytes, moved into place, so that it costs one
+// load like the others; a row of less than 16 bytes goes element by element.
 template <int ES>
-__device__ __forceinline__ i32x4 load16(const char* p, long long left) {
+__device__ __forceinline__ i32x4 load16(const char* row, long long k, long long kb) {
   i32x4 v = {0, 0, 0, 0};
-  if (left >= 16) {
-    __builtin_memcpy(&v, p, 16);
-  } else if (left > 0) {
+  if (kb < 16) {
     uint32_t w[4] = {0, 0, 0, 0};
+    for (int b = 0; b < 16 / ES; ++b) {
+      if (k + b * ES < kb) {
+        uint32_t e = 0;
+        __builtin_memcpy(&e, row + k + b * ES, ES);
 #pragma unroll
-    for (int i = 0; i < 16 / ES; ++i) {
-      if (i * ES < left) {
-        uint32_t b = 0;
-        __builtin_memcpy(&b, p + i * ES, ES);
-        w[i * ES / 4] |= b << (8 * (i * ES % 4));
+        for (int i = 0; i < 4; ++i) w[i] |= b * ES / 4 == i ? e << (8 * (b * ES % 4)) : 0u;
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (int)w[i];
+    return v;
   }
+  uint64_t q[2];
+  __builtin_memcpy(q, row + (k + 16 <= kb ? k : kb - 16), 16);
+  // the chunk starts `cut` bytes into what was loaded
+  const int cut = (int)(k + 16 <= kb ? 0 : k - (kb - 16) < 16 ? k - (kb - 16) : 16);
+  const int sh = (cut & 7) * 8;
+  const uint64_t next = cut < 8 ? q[1] : 0, low = cut < 8 ? q[0] : q[1];
+  q[0] = sh ? low >> sh | next << (64 - sh) : low;
+  q[1] = next >> sh;
+  if (cut >= 16) q[0] = q[1] = 0;
+  __builtin_memcpy(&v, q, 16);
   return v;
 }
+
+// The tile of this workgroup: XCD x = blockIdx.x % 8 takes the tiles [ntile x / 8,
+// ntile (x + 1) / 8) in groups of 4 tile-rows, so that those resident together share
+// operand rows in its L2. False for workgroups behind the range. Grid: tile_grid.
+__device__ __forceinline__ bool tile_origin(long long T, int m, int bm, int bn, int& m0, int& n0) {
+  const int tn = (m + bn - 1) / bn, tm = (int)((T + bm - 1) / bm), ntile = tn * tm;
+  const int x = blockIdx.x % 8;
+  const int lin = (int)((long long)ntile * x / 8) + (int)blockIdx.x / 8;
+  if (lin >= (int)((long long)ntile * (x + 1) / 8)) return false;
+  const int grp = lin / (4 * tn), first = grp * 4;
+  const int gsz = min(4, tm - first), in = lin - grp * (4 * tn);
+  m0 = __builtin_amdgcn_readfirstlane((first + in % gsz) * bm);
+  n0 = __builtin_amdgcn_readfirstlane((in / gsz) * bn);
+  return true;
+}
+inline long long tile_grid(long long T, int m, int bm, int bn) {
+  return (((T + bm - 1) / bm) * ((m + bn - 1) / bn) + 7) / 8 * 8;
+}
+constexpr long long kMaxTiles = 1LL << 28;   // of one launch: tile numbers in 32 bits
 
 // The activations in 32 bits. A result that is rounded to bf16 takes the
 // hardware's exponential and reciprocal (a few units of 2^-24 off), an fp32 one
@@ -160,32 +189,26 @@ constexpr int kAnyAct = -1;
 template <bool BF16, int ACT, bool EDGE, typename S, int N>
 __device__ __forceinline__ void finish_cols(const LinearArgs& a, const S (&acc)[N], long long t, int c,
                                             int cols) {
-  float v[N], o[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = (float)acc[i];
-  if constexpr (std::is_same<S, int>::value) {
-    const float sx = a.sx[t];
-    load_cols<EDGE>(a.sw + c, cols, o);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = v[i] * sx * o[i];
-  }
-  if (a.bias) {
-    load_cols<EDGE>(a.bias + c, cols, o);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += o[i];
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = activate<BF16>(v[i], ACT == kAnyAct ? a.act : ACT);
   typedef typename std::conditional<BF16, uint16_t, float>::type E;
-  if (a.mul) {
-    load_cols<EDGE>(static_cast<const E*>(a.mul) + t * a.ldm + c, cols, o);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= o[i];
+  constexpr bool SCALED = std::is_same<S, int>::value;
+  // every load out before the first is used: one wait for memory, not four
+  float v[N], w[N], b[N], m[N], r0[N];
+  float sx = 1.0f;
+  if constexpr (SCALED) {
+    sx = a.sx[t];
+    load_cols<EDGE>(a.sw + c, cols, w);
   }
-  if (a.res) {
-    load_cols<EDGE>(static_cast<const E*>(a.res) + t * a.ldr + c, cols, o);
+  if (a.bias) load_cols<EDGE>(a.bias + c, cols, b);
+  if (a.mul) load_cols<EDGE>(static_cast<const E*>(a.mul) + t * a.ldm + c, cols, m);
+  if (a.res) load_cols<EDGE>(static_cast<const E*>(a.res) + t * a.ldr + c, cols, r0);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += o[i];
+  for (int i = 0; i < N; ++i) {
+    v[i] = (float)acc[i];
+    if constexpr (SCALED) v[i] = v[i] * sx * w[i];
+    if (a.bias) v[i] += b[i];
+    v[i] = activate<BF16>(v[i], ACT == kAnyAct ? a.act : ACT);
+    if (a.mul) v[i] *= m[i];
+    if (a.res) v[i] += r0[i];
   }
   Pack<E, N> r;
 #pragma unroll

@@ -390,7 +390,8 @@ poetx_status poetx_scatter_cols(const poetx_plan* plan, int64_t T, int32_t dim, 
  *     is not finite has q = 0 and scale NaN, so every value it stands for is NaN.
  *   scale fp32 [T] (POETX_INT8 only, else NULL)
  *   rstd fp32 [T] or NULL: s, for the backward.
- * T = 0 is a no-op. No row is touched behind the T-th. */
+ * T = 0 is a no-op. No row is touched behind the T-th. dim <= 2^24 (POETX_ERR_SHAPE),
+ * also in the backward. */
 typedef struct {
   int64_t T;
   int32_t dim;
@@ -430,7 +431,8 @@ poetx_status poetx_rms_norm_backward(const poetx_norm_backward_desc* desc, const
  *     sw fp32 [m] (NULL otherwise): X W^T = (float(sum_j q_tj q_cj) sx_t) sw_c,
  *     the sum exact in 32-bit integers; n <= 131071.
  *   y_dtype: POETX_FP32 always; POETX_BF16 with dtype POETX_BF16 or POETX_INT8.
- * The order of a sum depends on the sizes and strides alone. T = 0 is a no-op. */
+ * The order of a sum depends on sizes, strides and alignment alone. T = 0 is a
+ * no-op. m <= 2^24 (POETX_ERR_SHAPE). */
 typedef enum {
   POETX_ACT_NONE = 0,
   POETX_ACT_RELU = 1,

@@ -225,24 +225,8 @@ void linear_tile_kernel(LinearArgs a) {
 
 template <typename Ty, int BM, int BN, int KB, int KS, bool YBF16>
 void tiles(const LinearArgs& a, hipStream_t s) {
-  // tokens of one launch, so that tile numbers stay in 32 bits (T itself does)
-  const long long step = std::max(1LL, kMaxTiles / ((a.m + BN - 1) / BN)) * BM;
-  for (long long t = 0; t < a.T; t += step) {
-    LinearArgs b = a;
-    b.T = std::min(step, a.T - t);
-    auto off = [](const void* p, long long bytes) {
-      return p ? static_cast<const void*>(static_cast<const char*>(p) + bytes) : nullptr;
-    };
-    const int ys = YBF16 ? 2 : 4;
-    b.X = off(a.X, t * a.ldx * Ty::kSize);
-    b.sx = static_cast<const float*>(off(a.sx, t * 4));
-    b.mul = off(a.mul, t * a.ldm * ys);
-    b.res = off(a.res, t * a.ldr * ys);
-    b.Y = const_cast<void*>(off(a.Y, t * a.ldy * ys));
-    hipLaunchKernelGGL((linear_tile_kernel<Ty, BM, BN, KB, KS, YBF16>),
-                       dim3((unsigned)tile_grid(b.T, b.m, BM, BN)), dim3(256 * KS),
-                       (tile_lds<BM, BN, KB, KS>()), s, b);
-  }
+  hipLaunchKernelGGL((linear_tile_kernel<Ty, BM, BN, KB, KS, YBF16>), dim3((unsigned)tile_grid(a.T, a.m, BM, BN)),
+                     dim3(256 * KS), (tile_lds<BM, BN, KB, KS>()), s, a);
 }
 
 template <typename Ty, bool YBF16>
@@ -329,11 +313,7 @@ int cheapest(const Cost (&costs)[N], const LinearArgs& a, F allowed) {
   return best;
 }
 
-}  // namespace
-
-hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s) {
-  if (a.T <= 0 || a.m <= 0 || a.n <= 0) return hipErrorInvalidValue;
-  if (a.y_bf16 && type == LINEAR_F32) return hipErrorInvalidValue;
+hipError_t launch_piece(const LinearArgs& a, int type, hipStream_t s) {
   const bool ring = linear_ring_supported(a, type);
   // One token goes by rows (2048 to 5632 bf16 6.4 us, 7.0 in tiles); with 2 to 4 the
   // tiles are as fast or faster (2 tokens, 4096 to 11008 INT8 11.4 against 9.7 us).
@@ -348,6 +328,32 @@ hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s) {
   };
   const int tile = type == LINEAR_F32 ? cheapest(kRingF32, a, allowed) : cheapest(kRing, a, allowed);
   return tile == LINEAR_TILE_256 ? launch_linear_pipe(a, type, s) : launch_linear_ring(a, type, tile, s);
+}
+
+}  // namespace
+
+hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s) {
+  if (a.T <= 0 || a.m <= 0 || a.n <= 0 || a.m > kLinearMaxRows) return hipErrorInvalidValue;
+  if (a.y_bf16 && type == LINEAR_F32) return hipErrorInvalidValue;
+  // A launch counts threads in 32 bits: at most 2^22 of the smallest tiles. One
+  // launch for any size but results of 2^32 elements and more.
+  const long long step = std::max(256LL, (1LL << 32) / a.m / 256 * 256);
+  const int es = type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1, ys = a.y_bf16 ? 2 : 4;
+  const auto off = [](const void* p, long long bytes) {
+    return p ? static_cast<const void*>(static_cast<const char*>(p) + bytes) : nullptr;
+  };
+  for (long long t = 0; t < a.T; t += step) {
+    LinearArgs b = a;
+    b.T = std::min(step, a.T - t);
+    b.X = off(a.X, t * a.ldx * es);
+    b.sx = static_cast<const float*>(off(a.sx, t * 4));
+    b.mul = off(a.mul, t * a.ldm * ys);
+    b.res = off(a.res, t * a.ldr * ys);
+    b.Y = const_cast<void*>(off(a.Y, t * a.ldy * ys));
+    const hipError_t e = launch_piece(b, type, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace poetx

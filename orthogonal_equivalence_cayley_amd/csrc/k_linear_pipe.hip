@@ -409,7 +409,6 @@ hipError_t launch(const LinearArgs& a, hipStream_t s) {
 bool linear_pipe_supported(const LinearArgs& a, int type) {
   if (type == LINEAR_F32) return false;
   const int es = type == LINEAR_BF16 ? 2 : 1;
-  if ((a.T / kTile + 1) * (a.m / kTile + 1) >= (1LL << 28)) return false;   // tile numbers in 32 bits
   if (a.T < kTile || a.m < kTile || a.m % 8 || (long long)a.n * es % kKB || a.ldx * es % 16 || a.ldw * es % 16) return false;
   if (((uintptr_t)a.X | (uintptr_t)a.W) & 15) return false;
   return a.ldx * es * kTile < (1LL << 31) && a.ldw * es * kTile < (1LL << 31);

@@ -195,9 +195,8 @@ bool linear_ring_supported(const LinearArgs& a, int type) {
   const int es = type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1;
   if ((long long)a.n * es % kKB || a.ldx * es % 16 || a.ldw * es % 16) return false;
   if (((uintptr_t)a.X | (uintptr_t)a.W) & 15) return false;
-  // 256 rows within 32-bit offsets, tile numbers in 32 bits
-  return a.ldx * es * 256 < (1LL << 31) && a.ldw * es * 256 < (1LL << 31) &&
-         (a.T / 32 + 1) * (a.m / 32 + 1) < kMaxTiles;
+  // 256 rows within 32-bit offsets
+  return a.ldx * es * 256 < (1LL << 31) && a.ldw * es * 256 < (1LL << 31);
 }
 
 hipError_t launch_linear_ring(const LinearArgs& a, int type, int tile, hipStream_t s) {

@@ -367,14 +367,15 @@ __global__ __launch_bounds__(kThr) void rms_norm_backward_kernel(NormBackArgs a)
 template <typename E>
 __global__ __launch_bounds__(kThr) void rms_norm_dot_kernel(NormBackArgs a) {
   __shared__ float red[4];
-  const long long t = blockIdx.x;
-  const E* g = static_cast<const E*>(a.G) + t * a.ldg;
-  const E* h = static_cast<const E*>(a.H) + t * a.ldh;
-  float dot = 0.0f;
-  for (int c = threadIdx.x; c < a.dim; c += kThr) dot += (to_f(g[c]) * a.w[c]) * to_f(h[c]);
-  dot = row_reduce<4>(dot, red, Add{});
-  const float s = a.rstd[t];
-  if (threadIdx.x == 0) a.rowc[t] = dot / (float)a.dim * s * s;
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const E* g = static_cast<const E*>(a.G) + t * a.ldg;
+    const E* h = static_cast<const E*>(a.H) + t * a.ldh;
+    float dot = 0.0f;
+    for (int c = threadIdx.x; c < a.dim; c += kThr) dot += (to_f(g[c]) * a.w[c]) * to_f(h[c]);
+    dot = row_reduce<4>(dot, red, Add{});
+    const float s = a.rstd[t];
+    if (threadIdx.x == 0) a.rowc[t] = dot / (float)a.dim * s * s;
+  }
 }
 template <typename E>
 __global__ __launch_bounds__(kThr) void rms_norm_cols_kernel(NormBackArgs a, int nparts) {
@@ -464,7 +465,7 @@ void bwd_any(const NormBackArgs& a, int parts, hipStream_t s) {
   // us, 16384 x 2048 64 against 50 us
   if (a.T >= kManyRows && with_nv<2>(a.dim, 64 * N, [&](auto nv) { bwd<E, nv.value, 1>(a, parts, s); })) return;
   if (with_nv<4>(a.dim, 256 * N, [&](auto nv) { bwd<E, nv.value, 4>(a, parts, s); })) return;
-  hipLaunchKernelGGL((rms_norm_dot_kernel<E>), dim3((unsigned)a.T), dim3(kThr), 0, s, a);
+  hipLaunchKernelGGL((rms_norm_dot_kernel<E>), dim3((unsigned)std::min<long long>(a.T, 8192)), dim3(kThr), 0, s, a);
   hipLaunchKernelGGL((rms_norm_cols_kernel<E>), dim3((unsigned)((a.dim + kThr - 1) / kThr), (unsigned)parts),
                      dim3(kThr), 0, s, a, parts);
 }
@@ -475,16 +476,42 @@ void bwd_any(const NormBackArgs& a, int parts, hipStream_t s) {
 // (too few loads in flight) and 50 with 1024 (twice the partial sums).
 int norm_backward_parts(long long T) { return (int)std::min<long long>((T + 1) / 2, 512); }
 
+namespace {
+
+// A launch counts threads in 32 bits: rows of one, for a workgroup of 256 a row
+constexpr long long kRowsPerLaunch = 1LL << 23;
+
+template <typename E>
+const E* at(const E* p, long long n) { return p ? p + n : nullptr; }
+template <typename E>
+E* at(E* p, long long n) { return p ? p + n : nullptr; }
+const void* at(const void* p, long long bytes) { return at(static_cast<const char*>(p), bytes); }
+void* at(void* p, long long bytes) { return at(static_cast<char*>(p), bytes); }
+
+}  // namespace
+
 hipError_t launch_add_rms_norm(const NormArgs& a, int bf16, hipStream_t s) {
-  if (a.T <= 0) return hipSuccess;
-  if (a.T > 0x7fffffffLL || a.dim <= 0) return hipErrorInvalidValue;
-  if (bf16) fwd_any<uint16_t>(a, s);
-  else fwd_any<float>(a, s);
-  return hipGetLastError();
+  if (a.dim <= 0 || a.dim > kNormMaxDim) return hipErrorInvalidValue;
+  const int es = bf16 ? 2 : 4;
+  for (long long t = 0; t < a.T; t += kRowsPerLaunch) {
+    NormArgs b = a;
+    b.T = std::min(kRowsPerLaunch, a.T - t);
+    b.X = at(a.X, t * a.ldx * es);
+    b.R = at(a.R, t * a.ldr * es);
+    b.H = at(a.H, t * a.ldh * es);
+    b.Y = at(a.Y, t * a.ldy * (a.quant ? 1 : es));
+    b.scale = at(a.scale, t);
+    b.rstd = at(a.rstd, t);
+    if (bf16) fwd_any<uint16_t>(b, s);
+    else fwd_any<float>(b, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_rms_norm_backward(const NormBackArgs& a, int bf16, hipStream_t s) {
-  if (a.T <= 0 || a.T > 0x7fffffffLL || a.dim <= 0) return hipErrorInvalidValue;
+  if (a.T <= 0 || a.dim <= 0 || a.dim > kNormMaxDim) return hipErrorInvalidValue;
   const int parts = norm_backward_parts(a.T);
   NormBackArgs b = a;
   if (parts == 1) b.part = a.dw;   // the only partial sum is the sum

@@ -113,7 +113,6 @@ __device__ __forceinline__ bool tile_origin(long long T, int m, int bm, int bn, 
 inline long long tile_grid(long long T, int m, int bm, int bn) {
   return (((T + bm - 1) / bm) * ((m + bn - 1) / bn) + 7) / 8 * 8;
 }
-constexpr long long kMaxTiles = 1LL << 28;   // of one launch: tile numbers in 32 bits
 
 // The activations in 32 bits. A result that is rounded to bf16 takes the
 // hardware's exponential and reciprocal (a few units of 2^-24 off), an fp32 one

@@ -254,6 +254,7 @@ struct NormBackArgs {
   long long T; int dim;
   long long ldg, ldgh, ldh, ldgx;
 };
+constexpr int kNormMaxDim = 1 << 24;
 constexpr int kNormRegDim = 4096;   // rows up to this length stay in registers for every type
 int norm_backward_parts(long long T);
 hipError_t launch_rms_norm_backward(const NormBackArgs& a, int bf16, hipStream_t s);
@@ -291,6 +292,7 @@ struct LinearArgs {
   int act;       // poetx_act
   int y_bf16;    // Y, mul and res are bf16 (else fp32)
 };
+constexpr int kLinearMaxRows = 1 << 24;   // rows of W: column tiles of a launch stay countable
 hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s);
 // 256 x 256 tiles with one load pipeline (k_linear_pipe.hip): bf16 and INT8
 bool linear_pipe_supported(const LinearArgs& a, int type);

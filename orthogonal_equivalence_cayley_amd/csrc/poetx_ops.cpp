@@ -70,7 +70,7 @@ extern "C" {
 poetx_status poetx_add_rms_norm(const poetx_norm_desc* d, const void* X, const void* R, const float* w,
                                 void* H, void* Y, float* scale, float* rstd, void* stream) {
   if (!d || d->T < 0) return POETX_ERR_INVALID_ARG;
-  if (d->dim < 1 || d->T > kMaxRows) return POETX_ERR_SHAPE;
+  if (d->dim < 1 || d->dim > poetx::kNormMaxDim || d->T > kMaxRows) return POETX_ERR_SHAPE;
   if (!real_type(d->dtype) || (d->y_dtype != d->dtype && d->y_dtype != POETX_INT8)) return POETX_ERR_DTYPE;
   if (!(d->eps >= 0.0) || !std::isfinite(d->eps)) return POETX_ERR_INVALID_ARG;
   if (d->T == 0) return POETX_OK;
@@ -96,7 +96,7 @@ poetx_status poetx_add_rms_norm(const poetx_norm_desc* d, const void* X, const v
 }
 
 size_t poetx_rms_norm_backward_workspace(int64_t T, int32_t dim) {
-  if (T < 0 || T > kMaxRows || dim < 1) return 0;
+  if (T < 0 || T > kMaxRows || dim < 1 || dim > poetx::kNormMaxDim) return 0;
   // partial sums of g_w, then one value per row for rows that no wave holds
   const size_t rows = dim > poetx::kNormRegDim ? (size_t)T * 4 : 0;
   return ((size_t)poetx::norm_backward_parts(T) * dim * 4 + rows + 255) / 256 * 256 + 256;
@@ -106,7 +106,7 @@ poetx_status poetx_rms_norm_backward(const poetx_norm_backward_desc* d, const vo
                                      const void* H, const float* w, const float* rstd, void* G_X,
                                      float* g_w, void* ws, size_t ws_bytes, void* stream) {
   if (!d || d->T < 0) return POETX_ERR_INVALID_ARG;
-  if (d->dim < 1 || d->T > kMaxRows) return POETX_ERR_SHAPE;
+  if (d->dim < 1 || d->dim > poetx::kNormMaxDim || d->T > kMaxRows) return POETX_ERR_SHAPE;
   if (!real_type(d->dtype)) return POETX_ERR_DTYPE;
   if (!g_w) return POETX_ERR_INVALID_ARG;
   if (!aligned(g_w, 4)) return POETX_ERR_ALIGNMENT;
@@ -142,7 +142,7 @@ poetx_status poetx_linear(const poetx_linear_desc* d, const void* X, const void*
                           const float* sw, const float* bias, const void* mul, const void* res, void* Y,
                           void* stream) {
   if (!d || d->T < 0) return POETX_ERR_INVALID_ARG;
-  if (d->m < 1 || d->n < 1 || d->T > kMaxRows) return POETX_ERR_SHAPE;
+  if (d->m < 1 || d->m > poetx::kLinearMaxRows || d->n < 1 || d->T > kMaxRows) return POETX_ERR_SHAPE;
   const bool q = d->dtype == POETX_INT8;
   if (!q && !real_type(d->dtype)) return POETX_ERR_DTYPE;
   if (d->y_dtype != POETX_FP32 && !(d->y_dtype == POETX_BF16 && d->dtype != POETX_FP32)) return POETX_ERR_DTYPE;

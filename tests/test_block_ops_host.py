@@ -27,6 +27,7 @@ INV, SHAPE, DTYPE, ALIGN, UNSUP, WS = (px.POETX_ERR_INVALID_ARG, px.POETX_ERR_SH
     (dict(T=0), px.POETX_OK),
     (dict(T=0, X=None, Y=None, w=None), px.POETX_OK),
     (dict(null=True), INV), (dict(T=-1), INV), (dict(T=2 ** 31), SHAPE), (dict(dim=0), SHAPE),
+    (dict(dim=2 ** 24 + 1), SHAPE),
     (dict(dtype=px.POETX_INT8), DTYPE), (dict(dtype=7), DTYPE), (dict(y_dtype=px.POETX_FP32), DTYPE),
     (dict(eps=-1.0), INV), (dict(eps=float("nan")), INV), (dict(eps=float("inf")), INV),
     (dict(X=None), INV), (dict(w=None), INV), (dict(Y=None), INV),
@@ -69,7 +70,7 @@ def test_norm_backward_refusals(kw, status):
 
 def test_norm_backward_workspace():
     f = L.poetx_rms_norm_backward_workspace
-    assert f(-1, 8) == 0 and f(2 ** 31, 8) == 0 and f(4, 0) == 0
+    assert f(-1, 8) == 0 and f(2 ** 31, 8) == 0 and f(4, 0) == 0 and f(4, 2 ** 24 + 1) == 0
     assert f(0, 8) > 0
     assert f(1000, 64) >= 4 * 64 * (1000 // 4)
     # rows longer than any register variant keep one more value each
@@ -88,6 +89,7 @@ Q = dict(dtype=px.POETX_INT8, sx=G, sw=H)
 @pytest.mark.parametrize("kw, status", [
     (dict(T=0), px.POETX_OK), (dict(T=0, X=None, Y=None), px.POETX_OK),
     (dict(null=True), INV), (dict(T=-1), INV), (dict(T=2 ** 31), SHAPE), (dict(m=0), SHAPE), (dict(n=0), SHAPE),
+    (dict(m=2 ** 24 + 1), SHAPE),
     (dict(dtype=3), DTYPE), (dict(y_dtype=px.POETX_INT8), DTYPE), (dict(dtype=px.POETX_FP32), DTYPE),
     (dict(act=-1), INV), (dict(act=5), INV),
     (dict(Q, n=131072, ld=(131072, 131072, 32, 32, 32)), UNSUP),

@@ -8,7 +8,7 @@
 //  * one token (up to four where rows are unaligned), linear_rows: every wave takes
 //    rows of W whole and multiplies on the vector units: bound by the weight's bytes.
 //  * linear_pipe (k_linear_pipe.hip) and linear_ring (k_linear_ring.hip): tiles
-//    filled by direct-to-LDS loads, for rows of whole 128-byte pieces.
+//    filled by direct-to-LDS loads, for rows of whole 128- and 16-byte pieces.
 //  * linear_tile: tiles filled through registers, any sizes and alignment.
 // The tile is the one of least cost for the grid it makes (`cheapest`).
 #include <algorithm>
@@ -322,7 +322,7 @@ hipError_t launch_piece(const LinearArgs& a, int type, hipStream_t s) {
     return launch_tiles(a, type, type == LINEAR_F32 ? cheapest(kTilesF32, a, [](int) { return true; })
                                                     : cheapest(kTiles, a, [](int) { return true; }), s);
   const bool pipe = linear_pipe_supported(a, type);
-  const long long stages = (long long)a.n * (type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1) / 128;
+  const long long stages = ((long long)a.n * (type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1) + 127) / 128;
   const auto allowed = [&](int tile) {
     return tile == LINEAR_TILE_256 ? pipe : tile == LINEAR_TILE_32_SPLIT ? stages % 2 == 0 : true;
   };

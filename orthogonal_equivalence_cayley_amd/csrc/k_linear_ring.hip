@@ -10,7 +10,7 @@
 // leave CUs idle (16 x 2048 x 5632 7.5 -> 7.0 us, 16 x 5632 x 2048 14.1 -> 11.5 us).
 //
 // Rows past the last token or weight row are clamped to it (not stored).
-// Requirements (linear_ring_supported): 128-byte multiples of n, 16-byte rows.
+// Requirements (linear_ring_supported): n and row strides of whole 16 bytes.
 #include <algorithm>
 #include <type_traits>
 
@@ -39,7 +39,9 @@ __device__ __forceinline__ void load_lds(const char* base, int bytes, unsigned c
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)to, 16, off, k, 0, 0);
 }
 
-template <typename Ty, int BM, int BN, int NS, int KS, bool YBF16>
+// TAIL: n is no multiple of 128 bytes (its own kernel: the extra work costs the
+// others 10 %)
+template <typename Ty, int BM, int BN, int NS, int KS, bool TAIL, bool YBF16>
 __global__ __launch_bounds__(kThr * KS)
 __attribute__((amdgpu_waves_per_eu(std::max(2, KS), std::max(2, KS))))
 void linear_ring_kernel(LinearArgs p) {
@@ -67,17 +69,32 @@ void linear_ring_kernel(LinearArgs p) {
   for (int i = 0; i < LW; ++i) vw[i] = (uint32_t)(min(i * 32 + lr, rw - 1) * ldb) + lc;
   const char* const bx = static_cast<const char*>(p.X) + (long long)m0 * lda;
   const char* const bw = static_cast<const char*>(p.W) + (long long)n0 * ldb;
-  const int nk = (int)((long long)p.n * Ty::kSize / kKB) / KS;   // stages of a group, a piece of n in a row
+  const long long kb = (long long)p.n * Ty::kSize;
+  const int stages = (int)((kb + kKB - 1) / kKB);
+  const int nk = stages / KS;   // stages of a group, a piece of n in a row
   const int k0 = grp_k * nk * kKB;
+  // A last stage that n cuts: the lanes whose chunks lie behind the row's end load
+  // the stage's first chunk in their place, and write zeros over it once it landed
+  const int tail = (int)(kb - (long long)(stages - 1) * kKB);
+  const int cut = tail < kKB && grp_k == KS - 1 ? nk - 1 : nk;   // that stage, if any
+  const bool gone = (int)lc >= tail;
 
   // stage s (past the end: the last one again, into a buffer nobody reads)
   auto issue = [&](int s, int buf) __attribute__((always_inline)) {
-    const int k = k0 + min(s, nk - 1) * kKB;
+    s = min(s, nk - 1);
+    const int k = k0 + s * kKB;
+    const uint32_t back = TAIL && gone && s == cut ? lc : 0;
     unsigned char* st = ring + buf * STAGE + wave * 1024;
 #pragma unroll
-    for (int i = 0; i < LX; ++i) load_lds(bx, rx * lda, st + i * 4096, vx[i], k);
+    for (int i = 0; i < LX; ++i) load_lds(bx, rx * lda, st + i * 4096, vx[i] - back, k);
 #pragma unroll
-    for (int i = 0; i < LW; ++i) load_lds(bw, rw * ldb, st + BM * kKB + i * 4096, vw[i], k);
+    for (int i = 0; i < LW; ++i) load_lds(bw, rw * ldb, st + BM * kKB + i * 4096, vw[i] - back, k);
+  };
+  auto clear = [&](int buf) __attribute__((always_inline)) {
+    if (!gone) return;
+    unsigned char* st = ring + buf * STAGE + tid * 16;
+#pragma unroll
+    for (int i = 0; i < LX + LW; ++i) *reinterpret_cast<i32x4*>(st + i * 4096) = i32x4{0, 0, 0, 0};
   };
   // chunk c of row r at slot 8 r + (c ^ ((r / 2) & 7))
   auto frag = [&](const unsigned char* st, int r, int c) __attribute__((always_inline)) {
@@ -115,6 +132,7 @@ void linear_ring_kernel(LinearArgs p) {
 #pragma unroll
   for (int s = 0; s < NS; ++s) issue(s, s);
   vm_wait<(NS - 1) * (LX + LW)>();   // this wave's part of stage 0 landed
+  if (TAIL && cut == 0) clear(0);
   lds_sync();                        // and everyone's
   read(0, 0);
   int buf = 0;
@@ -125,6 +143,7 @@ void linear_ring_kernel(LinearArgs p) {
     spread(std::false_type{});
     __builtin_amdgcn_sched_barrier(0);
     vm_wait<(NS - 2) * (LX + LW)>();
+    if (TAIL && s + 1 == cut) clear(next);
     lds_sync();   // stage s + 1 landed, and nobody reads stage s any more
     issue(s + NS, buf);
     read(next, 0);
@@ -171,8 +190,12 @@ void linear_ring_kernel(LinearArgs p) {
 
 template <typename Ty, int BM, int BN, int NS, int KS, bool YBF16>
 hipError_t tiles(const LinearArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((linear_ring_kernel<Ty, BM, BN, NS, KS, YBF16>), dim3((unsigned)tile_grid(a.T, a.m, BM, BN)),
-                     dim3(kThr * KS), KS * NS * (BM + BN) * kKB, s, a);
+  const dim3 grid((unsigned)tile_grid(a.T, a.m, BM, BN));
+  constexpr int lds = KS * NS * (BM + BN) * kKB;
+  if ((long long)a.n * Ty::kSize % kKB)
+    hipLaunchKernelGGL((linear_ring_kernel<Ty, BM, BN, NS, KS, true, YBF16>), grid, dim3(kThr * KS), lds, s, a);
+  else
+    hipLaunchKernelGGL((linear_ring_kernel<Ty, BM, BN, NS, KS, false, YBF16>), grid, dim3(kThr * KS), lds, s, a);
   return hipGetLastError();
 }
 
@@ -193,7 +216,7 @@ hipError_t launch(const LinearArgs& a, int tile, hipStream_t s) {
 
 bool linear_ring_supported(const LinearArgs& a, int type) {
   const int es = type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1;
-  if ((long long)a.n * es % kKB || a.ldx * es % 16 || a.ldw * es % 16) return false;
+  if ((long long)a.n * es % 16 || a.ldx * es % 16 || a.ldw * es % 16) return false;
   if (((uintptr_t)a.X | (uintptr_t)a.W) & 15) return false;
   // 256 rows within 32-bit offsets
   return a.ldx * es * 256 < (1LL << 31) && a.ldw * es * 256 < (1LL << 31);

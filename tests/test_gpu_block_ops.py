@@ -350,7 +350,7 @@ def test_linear(T, n, m, dt):
 @pytest.mark.parametrize("dt", ["bf16", "f32", "int8"])
 @pytest.mark.parametrize("T, m", [(30, 2047), (130, 4096), (500, 2040), (1030, 2040), (4090, 2056), (16380, 1032),
                                   (16390, 1032)])
-@pytest.mark.parametrize("n", [70, 256])
+@pytest.mark.parametrize("n", [70, 48, 208, 256])
 def test_linear_tiles(T, n, m, dt):
     """Every part of the epilogue, written over the residual; the rows behind stay as they were."""
     import torch

@@ -140,7 +140,8 @@ __device__ __forceinline__ float activate(float z, int act) {
     case POETX_ACT_SILU: return z * logistic<BF16>(z);
     case POETX_ACT_GELU:
       if constexpr (BF16) {
-        const float e = z * half_erfc(z);
+        const float h = half_erfc(z);
+        const float e = h == 0.0f ? 0.0f : z * h;   // an infinite z too
         return z > 0.0f ? z - e : e;
       } else {
         return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));

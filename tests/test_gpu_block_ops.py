@@ -490,6 +490,92 @@ def test_rows_beyond_32_bits(dt):
         assert torch.equal(got, want) and torch.equal(gw, gw2)
 
 
+def test_linear_activations_of_infinities():
+    """+inf of a sum passes every activation; large negative sums end at zero."""
+    import torch
+    import orthogonal_equivalence_cayley_amd as oec
+    for dt in (torch.bfloat16, torch.float32):
+        for T in (1, 40, 300):
+            X = torch.zeros(T, 64, dtype=dt, device="cuda")
+            X[:, 0] = 1
+            W = torch.zeros(24, 64, dtype=dt, device="cuda")
+            W[0, 0], W[1, 0], W[2, 0] = math.inf, -1e30, 1e30
+            for act in ACTS:
+                y = oec.linear(X, W, act=act).double()
+                assert bool((y[:, 0] == math.inf).all()), (act, T)
+                assert bool((y[:, 2] == float(W[2, 0])).all()) and bool((y[:, 3:] == 0).all())
+                assert bool((y[:, 1] == (float(W[1, 0]) if act == "none" else 0)).all())
+
+
+# ------------------------------------------------------------------ large
+def test_norm_past_4_gib():
+    """Rows past 2^32 bytes, and more of them than one launch counts."""
+    import torch
+    import orthogonal_equivalence_cayley_amd as oec
+    for T, dim in ((1100003, 2048), (2 ** 23 + 5, 8)):
+        log(f"norm {T} x {dim}")
+        g = torch.Generator("cuda").manual_seed(T)
+        x = torch.empty(T, dim, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+        w = (1 + 0.2 * rand(gen(1), dim))
+        rows = torch.tensor([0, 1, T // 2, 2 ** 20 + 1, T - 6, T - 1])
+        xc = x[rows.cuda()].cpu()
+        h, s, y = norm_ref(xc, xc, w, 1e-6, "bf16")
+        o = oec.add_rms_norm(x, w.cuda(), residual=x, save=True, H=x)
+        close("h", x[rows.cuda()], h.double(), torch.zeros(1, dtype=torch.float64))
+        close("y", o.Y[rows.cuda()], y, (HALF["bf16"] + 4 * U) * y.abs())
+        close("rstd", o.rstd[rows.cuda()], s, 2 * U * s)
+        G_X, g_w = oec.add_rms_norm_backward(o.Y, x, w.cuda(), o.rstd, G_X=o.Y)
+        dx, mag, dc, _, _ = back_ref(y.bfloat16(), None, h, w, s.float())
+        # the gradient is y itself, rounded: 2^-8 of it through a linear map of slope s w and s h c
+        close("dx", G_X[rows.cuda()], dx, HALF["bf16"] * dx.abs() + 80 * U * (mag + dc) + HALF["bf16"] * 2 * (mag + dc))
+        assert torch.isfinite(g_w).all()
+        del x, o, G_X
+
+
+def test_linear_past_4_gib():
+    """Activations past 2^32 bytes, and a result of more than 2^32 elements."""
+    import torch
+    for T, n, m, dt in ((1100003, 2048, 264, "bf16"), (2100001, 2048, 256, "int8"), (1100003, 64, 4096, "bf16"),
+                        (1100003, 1001, 40, "bf16")):
+        import orthogonal_equivalence_cayley_amd as oec
+        log(f"linear {T} x {n} -> {m} {dt}")
+        g = torch.Generator("cuda").manual_seed(T)
+        kw = {}
+        if dt == "int8":
+            X = torch.empty(T, n, dtype=torch.int8, device="cuda").random_(-127, 128, generator=g)
+            W = torch.empty(m, n, dtype=torch.int8, device="cuda").random_(-127, 128, generator=g)
+            kw = dict(x_scale=torch.rand(T, device="cuda", generator=g) * 0.01,
+                      w_scale=torch.rand(m, device="cuda", generator=g) * 0.001)
+        else:
+            X = torch.empty(T, n, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+            W = torch.empty(m, n, dtype=torch.bfloat16, device="cuda").normal_(0, n ** -0.5, generator=g)
+        y = oec.linear(X, W, **kw)
+        rows = torch.tensor([0, 255, 2 ** 20 - 1, 2 ** 20, 2 ** 20 + 300, T - 257, T - 256, T - 1]).cuda()
+        c = dict(X=X[rows].cpu(), W=W.cpu(), sx=None, sw=None, b=None, mul=None, res=None)
+        if dt == "int8":
+            c.update(sx=kw["x_scale"][rows].cpu(), sw=kw["w_scale"].cpu())
+        v, tol = linear_ref(c, "none", HALF["bf16"])
+        close("rows", y[rows], v, tol)
+        del X, W, y
+
+
+def test_clip_past_4_gib():
+    import torch
+    import orthogonal_equivalence_cayley_amd as oec
+    for dt, n in ((torch.float32, 2 ** 30 + 12345), (torch.bfloat16, 2 ** 31 + 77)):
+        log(f"clip {n} {dt}")
+        g = torch.full((n,), 0.5, dtype=dt, device="cuda")
+        g[-1] = 1.0
+        norm = math.sqrt(0.25 * (n - 1) + 1)
+        got = oec.clip_grads([g], 1.0, out=[g])
+        assert abs(float(got) - norm) <= 2 * U * norm
+        c = torch.tensor(1.0 / (norm + 1e-6), dtype=torch.float64)
+        half = HALF["bf16" if dt == torch.bfloat16 else "f32"]
+        for i, v in ((0, 0.5), (n // 2, 0.5), (n - 2, 0.5), (n - 1, 1.0)):
+            assert abs(float(g[i]) - v * float(c)) <= (half + 2 * U) * v * float(c)
+        del g
+
+
 # ------------------------------------------------------------------ clip
 def clip_ref(grads, max_norm):
     import torch

@@ -5,8 +5,8 @@
 // integers), the epilogue in fp32, one rounding at the end.
 //
 // Four kernels:
-//  * one token (up to four where rows are unaligned), linear_rows: every wave takes
-//    rows of W whole and multiplies on the vector units: bound by the weight's bytes.
+//  * one to four tokens, linear_rows: every wave takes a row of W and multiplies on
+//    the vector units: bound by the weight's bytes (2048 to 5632 bf16 6.1 us).
 //  * linear_pipe (k_linear_pipe.hip) and linear_ring (k_linear_ring.hip): tiles
 //    filled by direct-to-LDS loads, for rows of whole 128- and 16-byte pieces.
 //  * linear_tile: tiles filled through registers, any sizes and alignment.
@@ -22,61 +22,51 @@ using namespace lin;
 
 // ------------------------------------------------------------------ single tokens
 constexpr int kRowThr = 256;
-constexpr int kRowsPerWave = 2;
-
+// One row of W to a wave (two rows 6.4 against 6.1 us at 2048 to 5632 bf16, 8.9
+// against 7.7 at 5632 to 2048; a row split over two waves 8.4 and 7.0); TT tokens.
 template <typename Ty, int TT, bool YBF16>
 __global__ __launch_bounds__(kRowThr) void linear_rows_kernel(LinearArgs a) {
-  constexpr int R = kRowsPerWave;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int c0 = (blockIdx.x * (kRowThr / 64) + wave) * R;
-  if (c0 >= a.m) return;
+  const int lane = threadIdx.x & 63;
+  const int c = (int)blockIdx.x * (kRowThr / 64) + (threadIdx.x >> 6);
+  if (c >= a.m) return;
   const long long kb = (long long)a.n * Ty::kSize;
-  const char* w[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    w[r] = static_cast<const char*>(a.W) + (long long)min(c0 + r, a.m - 1) * a.ldw * Ty::kSize;
+  const char* const w = static_cast<const char*>(a.W) + (long long)c * a.ldw * Ty::kSize;
   const char* x[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t)
     x[t] = static_cast<const char*>(a.X) + (long long)min((long long)t, a.T - 1) * a.ldx * Ty::kSize;
-  typename Ty::Sum acc[TT][R] = {};
+  typename Ty::Sum acc[TT] = {};
   // pieces of 1 KB, four at a time with all their loads out first
   constexpr int U = 4;
-  long long k = lane * 16;
-  for (; k - lane * 16 + 1024 * U <= kb; k += 1024 * U) {
-    i32x4 wv[U][R], xv[U][TT];
+  const long long k = lane * 16;
+  long long p = 0;
+  for (; p + 1024 * U <= kb; p += 1024 * U) {
+    i32x4 wv[U], xv[U][TT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      __builtin_memcpy(&wv[u], w + p + k + u * 1024, 16);
 #pragma unroll
-      for (int r = 0; r < R; ++r) __builtin_memcpy(&wv[u][r], w[r] + k + u * 1024, 16);
-#pragma unroll
-      for (int t = 0; t < TT; ++t) __builtin_memcpy(&xv[u][t], x[t] + k + u * 1024, 16);
+      for (int t = 0; t < TT; ++t) __builtin_memcpy(&xv[u][t], x[t] + p + k + u * 1024, 16);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int r = 0; r < R; ++r) Ty::dot(wv[u][r], xv[u][t], acc[t][r]);
+      for (int t = 0; t < TT; ++t) Ty::dot(wv[u], xv[u][t], acc[t]);
   }
-  for (; k - lane * 16 < kb; k += 1024) {
-    i32x4 wv[R], xv[TT];
+  for (; p < kb; p += 1024) {
+    const i32x4 wv = load16<Ty::kSize>(w, p + k, kb);
+    i32x4 xv[TT];
 #pragma unroll
-    for (int r = 0; r < R; ++r) wv[r] = load16<Ty::kSize>(w[r], k, kb);
+    for (int t = 0; t < TT; ++t) xv[t] = load16<Ty::kSize>(x[t], p + k, kb);
 #pragma unroll
-    for (int t = 0; t < TT; ++t) xv[t] = load16<Ty::kSize>(x[t], k, kb);
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-      for (int r = 0; r < R; ++r) Ty::dot(wv[r], xv[t], acc[t][r]);
+    for (int t = 0; t < TT; ++t) Ty::dot(wv, xv[t], acc[t]);
   }
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) acc[t][r] += __shfl_xor(acc[t][r], o);
-    if (lane == t && t < a.T) finish<YBF16>(a, acc[t], t, c0);
+    for (int o = 32; o > 0; o >>= 1) acc[t] += __shfl_xor(acc[t], o);
+    const typename Ty::Sum o[1] = {acc[t]};
+    if (lane == t && t < a.T) finish<YBF16>(a, o, t, c);
   }
 }
 
@@ -252,7 +242,7 @@ hipError_t launch_tiles(const LinearArgs& a, int type, int tile, hipStream_t s) 
 
 template <typename Ty, int TT, bool YBF16>
 hipError_t rows(const LinearArgs& a, hipStream_t s) {
-  const int per = kRowThr / 64 * kRowsPerWave;
+  constexpr int per = kRowThr / 64;
   hipLaunchKernelGGL((linear_rows_kernel<Ty, TT, YBF16>), dim3((unsigned)((a.m + per - 1) / per)), dim3(kRowThr), 0, s,
                      a);
   return hipGetLastError();
@@ -315,9 +305,12 @@ int cheapest(const Cost (&costs)[N], const LinearArgs& a, F allowed) {
 
 hipError_t launch_piece(const LinearArgs& a, int type, hipStream_t s) {
   const bool ring = linear_ring_supported(a, type);
-  // One token goes by rows (2048 to 5632 bf16 6.4 us, 7.0 in tiles); with 2 to 4 the
-  // tiles are as fast or faster (2 tokens, 4096 to 11008 INT8 11.4 against 9.7 us).
-  if (a.T == 1 || (a.T <= 4 && !ring)) return launch_rows(a, type, s);
+  // Few tokens go by rows while the vector units keep up with the weight: one INT8
+  // token (two, 2048 to 5632: 7.1 us by rows, 5.6 in tiles), two bf16 (2048 to 2048
+  // 4.4 against 6.6 us; four, 2048 to 5632, 9.1 against 7.2), four fp32 (2048 to 2048
+  // 7.5 against 15.8 us), and up to four where rows are ragged.
+  const long long few = !ring || type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1;
+  if (a.T <= few) return launch_rows(a, type, s);
   if (!ring)
     return launch_tiles(a, type, type == LINEAR_F32 ? cheapest(kTilesF32, a, [](int) { return true; })
                                                     : cheapest(kTiles, a, [](int) { return true; }), s);

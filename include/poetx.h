@@ -431,6 +431,8 @@ poetx_status poetx_rms_norm_backward(const poetx_norm_backward_desc* desc, const
  *     sw fp32 [m] (NULL otherwise): X W^T = (float(sum_j q_tj q_cj) sx_t) sw_c,
  *     the sum exact in 32-bit integers; n <= 131071.
  *   y_dtype: POETX_FP32 always; POETX_BF16 with dtype POETX_BF16 or POETX_INT8.
+ *   ws device, poetx_linear_workspace(desc) bytes (0, and ws may be NULL, but for
+ *     small results of a long n, which several workgroups share).
  * The order of a sum depends on sizes, strides and alignment alone. T = 0 is a
  * no-op. m <= 2^24 (POETX_ERR_SHAPE). */
 typedef enum {
@@ -447,9 +449,11 @@ typedef struct {
   int32_t act;              /* poetx_act                                       */
   int64_t ld_x, ld_w, ld_y, ld_mul, ld_res;
 } poetx_linear_desc;
+/* Goes by the sizes and the dtype alone; 0 for a bad description. */
+size_t poetx_linear_workspace(const poetx_linear_desc* desc);
 poetx_status poetx_linear(const poetx_linear_desc* desc, const void* X, const void* W, const float* sx,
                           const float* sw, const float* bias, const void* mul, const void* res, void* Y,
-                          void* stream);
+                          void* ws, size_t ws_bytes, void* stream);
 
 /* Global norm of count gradient tensors, and their clipping by it:
  *   norm = sqrt(sum of all squares) (64-bit sums, norm_out rounded once),

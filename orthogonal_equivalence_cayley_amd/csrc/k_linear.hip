@@ -88,7 +88,7 @@ template <int BM, int BN, int KB, int KS>
 constexpr int tile_lds() {
   return KS * 2 * (BM + BN) * KB;
 }
-template <typename Ty, int BM, int BN, int KB, int KS, bool YBF16>
+template <typename Ty, int BM, int BN, int KB, int KS, bool PART, bool YBF16>
 __global__ __launch_bounds__(256 * KS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void linear_tile_kernel(LinearArgs a) {
   constexpr int CPR = KB / 16;
@@ -139,8 +139,9 @@ void linear_tile_kernel(LinearArgs a) {
   };
   typename Ty::Acc acc[TM][TN] = {};
   // the same number of stages for every group: those behind the end hold zeros
-  const int stages = (int)((kb + (long long)KB * KS - 1) / ((long long)KB * KS));
-  const long long first = (long long)grp * KB, step = (long long)KB * KS;
+  const long long step = (long long)KB * KS * (PART ? a.splits : 1);
+  const int stages = (int)((kb + step - 1) / step);
+  const long long first = (long long)((PART ? (int)blockIdx.y * KS : 0) + grp) * KB;
   constexpr int Q = KB / 64;   // slabs of a stage
   static_assert(Q % 2 == 0, "fragment sets alternate across stages");
   i32x4 xf[2][TM], wf[2][TN];
@@ -207,16 +208,20 @@ void linear_tile_kernel(LinearArgs a) {
       const long long t = t0 + wm + i * 16 + (lane & 15);
       const int c = c0 + wn + j * 16 + 4 * (lane >> 4);
       if (t < a.T && c < a.m) {
-        const typename Ty::Sum o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        finish<YBF16>(a, o, t, c);
+        if constexpr (PART) {
+          store_part<Ty>(a, blockIdx.y, t, c, acc[i][j]);
+        } else {
+          const typename Ty::Sum o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+          finish<YBF16>(a, o, t, c);
+        }
       }
     }
 }
 
-template <typename Ty, int BM, int BN, int KB, int KS, bool YBF16>
+template <typename Ty, int BM, int BN, int KB, int KS, bool YBF16, bool PART = false>
 void tiles(const LinearArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((linear_tile_kernel<Ty, BM, BN, KB, KS, YBF16>), dim3((unsigned)tile_grid(a.T, a.m, BM, BN)),
-                     dim3(256 * KS), (tile_lds<BM, BN, KB, KS>()), s, a);
+  hipLaunchKernelGGL((linear_tile_kernel<Ty, BM, BN, KB, KS, PART, YBF16>),
+                     dim3((unsigned)tile_grid(a.T, a.m, BM, BN), PART ? (unsigned)a.splits : 1u), dim3(256 * KS), (tile_lds<BM, BN, KB, KS>()), s, a);
 }
 
 template <typename Ty, bool YBF16>
@@ -232,6 +237,14 @@ hipError_t launch_tiles(const LinearArgs& a, int tile, hipStream_t s) {
   return hipGetLastError();
 }
 hipError_t launch_tiles(const LinearArgs& a, int type, int tile, hipStream_t s) {
+  if (a.splits > 1) {   // sums only: the type of Y does not matter
+    switch (type) {
+      case LINEAR_F32: tiles<TypeF32, 32, 32, 256, 2, false, true>(a, s); break;
+      case LINEAR_BF16: tiles<TypeBf16, 32, 32, 256, 2, false, true>(a, s); break;
+      default: tiles<TypeI8, 32, 32, 256, 2, false, true>(a, s);
+    }
+    return hipGetLastError();
+  }
   switch (type) {
     case LINEAR_F32: return launch_tiles<TypeF32, false>(a, tile, s);
     case LINEAR_BF16:
@@ -303,27 +316,76 @@ int cheapest(const Cost (&costs)[N], const LinearArgs& a, F allowed) {
   return best;
 }
 
+long long few_rows(int type, bool ring) { return !ring || type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1; }
+
+// The sums of all splits of 4 columns of a row, in order, and the epilogue
+template <typename Ty, bool YBF16>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a) {
+  typedef typename Ty::Acc Acc;
+  typedef typename Ty::Sum S;
+  const int quads = (a.m + 3) / 4;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.T * quads) return;
+  const long long t = i / quads;
+  const int c = (int)(i - t * quads) * 4;
+  Acc v = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int z = 0; z < a.splits; ++z)
+    v += *reinterpret_cast<const Acc*>(static_cast<const S*>(a.part) + part_row(a, z, t) + c);
+  const S o[4] = {v[0], v[1], v[2], v[3]};
+  finish<YBF16>(a, o, t, c);
+}
+template <typename Ty, bool YBF16>
+hipError_t join(const LinearArgs& a, hipStream_t s) {
+  const long long n = a.T * ((a.m + 3) / 4);
+  hipLaunchKernelGGL((linear_join_kernel<Ty, YBF16>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+hipError_t launch_join(const LinearArgs& a, int type, hipStream_t s) {
+  switch (type) {
+    case LINEAR_F32: return join<TypeF32, false>(a, s);
+    case LINEAR_BF16: return a.y_bf16 ? join<TypeBf16, true>(a, s) : join<TypeBf16, false>(a, s);
+  }
+  return a.y_bf16 ? join<TypeI8, true>(a, s) : join<TypeI8, false>(a, s);
+}
+
 hipError_t launch_piece(const LinearArgs& a, int type, hipStream_t s) {
   const bool ring = linear_ring_supported(a, type);
-  // Few tokens go by rows while the vector units keep up with the weight: one INT8
+  // Few tokens go by rows (few_rows) while the vector units keep up with the weight: one INT8
   // token (two, 2048 to 5632: 7.1 us by rows, 5.6 in tiles), two bf16 (2048 to 2048
   // 4.4 against 6.6 us; four, 2048 to 5632, 9.1 against 7.2), four fp32 (2048 to 2048
   // 7.5 against 15.8 us), and up to four where rows are ragged.
-  const long long few = !ring || type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1;
-  if (a.T <= few) return launch_rows(a, type, s);
-  if (!ring)
-    return launch_tiles(a, type, type == LINEAR_F32 ? cheapest(kTilesF32, a, [](int) { return true; })
-                                                    : cheapest(kTiles, a, [](int) { return true; }), s);
-  const bool pipe = linear_pipe_supported(a, type);
-  const long long stages = ((long long)a.n * (type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1) + 127) / 128;
+  if (a.T <= few_rows(type, ring)) return launch_rows(a, type, s);
+  if (a.splits > 1) {
+    const hipError_t e = ring ? launch_linear_ring(a, type, LINEAR_TILE_32_SPLIT, s)
+                              : launch_tiles(a, type, LINEAR_TILE_32_SPLIT, s);
+    return e == hipSuccess ? launch_join(a, type, s) : e;
+  }
+  const bool pipe = ring && linear_pipe_supported(a, type);
   const auto allowed = [&](int tile) {
-    return tile == LINEAR_TILE_256 ? pipe : tile == LINEAR_TILE_32_SPLIT ? stages % 2 == 0 : true;
+    return tile == LINEAR_TILE_256 ? pipe : true;
   };
+  if (!ring)
+    return launch_tiles(a, type, type == LINEAR_F32 ? cheapest(kTilesF32, a, allowed) : cheapest(kTiles, a, allowed), s);
   const int tile = type == LINEAR_F32 ? cheapest(kRingF32, a, allowed) : cheapest(kRing, a, allowed);
   return tile == LINEAR_TILE_256 ? launch_linear_pipe(a, type, s) : launch_linear_ring(a, type, tile, s);
 }
 
 }  // namespace
+
+// Where a grid of 32 x 32 tiles fills at most half the CUs and n is long, several
+// workgroups share n: as many as fill the CUs, each with at least 16 stages of 128
+// bytes. Worth its second launch (3 us) from 96 stages on, fp32, whose stages take
+// the matrix units four times as long, from 24: LINEAR_SPLIT_FIGURES
+int linear_splits(const LinearArgs& a, int type) {
+  const int es = type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1;
+  const long long stages = ((long long)a.n * es + 127) / 128;
+  const long long tiles = ((a.T + 31) / 32) * ((a.m + 31) / 32);
+  if (a.T <= 4 || tiles > 128) return 1;
+  if (stages < (type == LINEAR_F32 ? 24 : 96)) return 1;
+  const long long per = type == LINEAR_F32 ? 8 : 16;
+  return (int)std::max(1LL, std::min({32LL, 256 / tiles, stages / per}));
+}
 
 hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s) {
   if (a.T <= 0 || a.m <= 0 || a.n <= 0 || a.m > kLinearMaxRows) return hipErrorInvalidValue;

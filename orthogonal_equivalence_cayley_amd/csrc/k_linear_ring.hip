@@ -7,7 +7,9 @@
 // loads and products one after the other: 31 against 22 us a 1024 x 2048 x 2048
 // bf16 product in 128 x 128 tiles; more stages in flight changed nothing.) With
 // KS = 2 a second group of four waves takes the other half of n, for grids that
-// leave CUs idle (16 x 2048 x 5632 7.5 -> 7.0 us, 16 x 5632 x 2048 14.1 -> 11.5 us).
+// leave CUs idle (16 x 2048 x 5632 7.5 -> 7.0 us, 16 x 5632 x 2048 14.1 -> 11.5 us),
+// and with PART several workgroups share n and leave their sums to linear_join
+// (k_linear.hip).
 //
 // Rows past the last token or weight row are clamped to it (not stored).
 // Requirements (linear_ring_supported): n and row strides of whole 16 bytes.
@@ -39,9 +41,9 @@ __device__ __forceinline__ void load_lds(const char* base, int bytes, unsigned c
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)to, 16, off, k, 0, 0);
 }
 
-// TAIL: n is no multiple of 128 bytes (its own kernel: the extra work costs the
-// others 10 %)
-template <typename Ty, int BM, int BN, int NS, int KS, bool TAIL, bool YBF16>
+// TAIL: n is no multiple of 128 bytes, or its stages none of KS (its own kernel: the
+// extra work costs the others 10 %)
+template <typename Ty, int BM, int BN, int NS, int KS, bool TAIL, bool PART, bool YBF16>
 __global__ __launch_bounds__(kThr * KS)
 __attribute__((amdgpu_waves_per_eu(std::max(2, KS), std::max(2, KS))))
 void linear_ring_kernel(LinearArgs p) {
@@ -71,27 +73,32 @@ void linear_ring_kernel(LinearArgs p) {
   const char* const bw = static_cast<const char*>(p.W) + (long long)n0 * ldb;
   const long long kb = (long long)p.n * Ty::kSize;
   const int stages = (int)((kb + kKB - 1) / kKB);
-  const int nk = stages / KS;   // stages of a group, a piece of n in a row
-  const int k0 = grp_k * nk * kKB;
-  // A last stage that n cuts: the lanes whose chunks lie behind the row's end load
-  // the stage's first chunk in their place, and write zeros over it once it landed
-  const int tail = (int)(kb - (long long)(stages - 1) * kKB);
-  const int cut = tail < kKB && grp_k == KS - 1 ? nk - 1 : nk;   // that stage, if any
-  const bool gone = (int)lc >= tail;
+  const int groups = PART ? KS * p.splits : KS;
+  const int nk = (stages + groups - 1) / groups;   // stages of a group, a piece of n in a row
+  const int k0 = ((PART ? (int)blockIdx.y * KS : 0) + grp_k) * nk * kKB;
+  // With TAIL a group's last stages may be cut by the row's end or lie behind it:
+  // lanes whose chunks are gone load the row's stage from its start instead (a stage
+  // behind the end: the row's first), and write zeros over it once it landed
+  auto ends = [&](int s) __attribute__((always_inline)) { return k0 + (long long)(s + 1) * kKB > kb; };
+  auto gone = [&](int s) __attribute__((always_inline)) { return k0 + (long long)s * kKB + lc >= kb; };
 
   // stage s (past the end: the last one again, into a buffer nobody reads)
   auto issue = [&](int s, int buf) __attribute__((always_inline)) {
     s = min(s, nk - 1);
-    const int k = k0 + s * kKB;
-    const uint32_t back = TAIL && gone && s == cut ? lc : 0;
+    int k = k0 + s * kKB;
+    uint32_t back = 0;
+    if (TAIL && ends(s)) {
+      back = gone(s) ? lc : 0;
+      k = k < kb ? k : 0;
+    }
     unsigned char* st = ring + buf * STAGE + wave * 1024;
 #pragma unroll
     for (int i = 0; i < LX; ++i) load_lds(bx, rx * lda, st + i * 4096, vx[i] - back, k);
 #pragma unroll
     for (int i = 0; i < LW; ++i) load_lds(bw, rw * ldb, st + BM * kKB + i * 4096, vw[i] - back, k);
   };
-  auto clear = [&](int buf) __attribute__((always_inline)) {
-    if (!gone) return;
+  auto clear = [&](int s, int buf) __attribute__((always_inline)) {
+    if (!gone(s)) return;
     unsigned char* st = ring + buf * STAGE + tid * 16;
 #pragma unroll
     for (int i = 0; i < LX + LW; ++i) *reinterpret_cast<i32x4*>(st + i * 4096) = i32x4{0, 0, 0, 0};
@@ -132,7 +139,7 @@ void linear_ring_kernel(LinearArgs p) {
 #pragma unroll
   for (int s = 0; s < NS; ++s) issue(s, s);
   vm_wait<(NS - 1) * (LX + LW)>();   // this wave's part of stage 0 landed
-  if (TAIL && cut == 0) clear(0);
+  if (TAIL && ends(0)) clear(0, 0);
   lds_sync();                        // and everyone's
   read(0, 0);
   int buf = 0;
@@ -143,7 +150,7 @@ void linear_ring_kernel(LinearArgs p) {
     spread(std::false_type{});
     __builtin_amdgcn_sched_barrier(0);
     vm_wait<(NS - 2) * (LX + LW)>();
-    if (TAIL && s + 1 == cut) clear(next);
+    if (TAIL && s + 1 < nk && ends(s + 1)) clear(s + 1, next);
     lds_sync();   // stage s + 1 landed, and nobody reads stage s any more
     issue(s + NS, buf);
     read(next, 0);
@@ -182,20 +189,24 @@ void linear_ring_kernel(LinearArgs p) {
       const long long t = (long long)m0 + wm + i * 16 + (lane & 15);
       const int c = n0 + wn + j * 16 + 4 * (lane >> 4);
       if (t < p.T && c < p.m) {
-        const typename Ty::Sum o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        finish<YBF16>(p, o, t, c);
+        if constexpr (PART) {
+          store_part<Ty>(p, blockIdx.y, t, c, acc[i][j]);
+        } else {
+          const typename Ty::Sum o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+          finish<YBF16>(p, o, t, c);
+        }
       }
     }
 }
 
-template <typename Ty, int BM, int BN, int NS, int KS, bool YBF16>
+template <typename Ty, int BM, int BN, int NS, int KS, bool YBF16, bool PART = false>
 hipError_t tiles(const LinearArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)tile_grid(a.T, a.m, BM, BN));
+  const dim3 grid((unsigned)tile_grid(a.T, a.m, BM, BN), PART ? (unsigned)a.splits : 1u);
   constexpr int lds = KS * NS * (BM + BN) * kKB;
-  if ((long long)a.n * Ty::kSize % kKB)
-    hipLaunchKernelGGL((linear_ring_kernel<Ty, BM, BN, NS, KS, true, YBF16>), grid, dim3(kThr * KS), lds, s, a);
+  if ((long long)a.n * Ty::kSize % ((long long)kKB * KS * (PART ? a.splits : 1)))
+    hipLaunchKernelGGL((linear_ring_kernel<Ty, BM, BN, NS, KS, true, PART, YBF16>), grid, dim3(kThr * KS), lds, s, a);
   else
-    hipLaunchKernelGGL((linear_ring_kernel<Ty, BM, BN, NS, KS, false, YBF16>), grid, dim3(kThr * KS), lds, s, a);
+    hipLaunchKernelGGL((linear_ring_kernel<Ty, BM, BN, NS, KS, false, PART, YBF16>), grid, dim3(kThr * KS), lds, s, a);
   return hipGetLastError();
 }
 
@@ -223,6 +234,13 @@ bool linear_ring_supported(const LinearArgs& a, int type) {
 }
 
 hipError_t launch_linear_ring(const LinearArgs& a, int type, int tile, hipStream_t s) {
+  if (a.splits > 1) {   // sums only: the type of Y does not matter
+    switch (type) {
+      case LINEAR_F32: return tiles<TypeF32, 32, 32, 4, 2, false, true>(a, s);
+      case LINEAR_BF16: return tiles<TypeBf16, 32, 32, 4, 2, false, true>(a, s);
+    }
+    return tiles<TypeI8, 32, 32, 4, 2, false, true>(a, s);
+  }
   switch (type) {
     case LINEAR_F32: return launch<TypeF32, false>(a, tile, s);
     case LINEAR_BF16: return a.y_bf16 ? launch<TypeBf16, true>(a, tile, s) : launch<TypeBf16, false>(a, tile, s);

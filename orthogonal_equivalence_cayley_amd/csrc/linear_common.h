@@ -232,5 +232,16 @@ __device__ __forceinline__ void finish(const LinearArgs& a, const S (&acc)[N], l
   else finish_cols<BF16, ACT, true>(a, acc, t, c, a.m - c);
 }
 
+// The sums of split `z` of a shared n: 4 columns of one row (c a multiple of 4; the
+// rows of `part` are as long as m up to a multiple of 4)
+__device__ __forceinline__ long long part_row(const LinearArgs& a, int z, long long t) {
+  return ((long long)z * a.T + t) * ((a.m + 3) / 4 * 4);
+}
+template <typename Ty>
+__device__ __forceinline__ void store_part(const LinearArgs& a, int z, long long t, int c,
+                                           const typename Ty::Acc& v) {
+  *reinterpret_cast<typename Ty::Acc*>(static_cast<typename Ty::Sum*>(a.part) + part_row(a, z, t) + c) = v;
+}
+
 }  // namespace lin
 }  // namespace poetx

@@ -291,7 +291,12 @@ struct LinearArgs {
   long long ldx, ldw, ldy, ldm, ldr;
   int act;       // poetx_act
   int y_bf16;    // Y, mul and res are bf16 (else fp32)
+  // where n is shared by `splits` workgroups a tile: their sums, splits x T x (m up to
+  // a multiple of 4), fp32 (LINEAR_I8: int32)
+  void* part = nullptr;
+  int splits = 1;
 };
+int linear_splits(const LinearArgs& a, int type);   // those launch_linear wants; 1: no `part`
 constexpr int kLinearMaxRows = 1 << 24;   // rows of W: column tiles of a launch stay countable
 hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s);
 // 256 x 256 tiles with one load pipeline (k_linear_pipe.hip): bf16 and INT8

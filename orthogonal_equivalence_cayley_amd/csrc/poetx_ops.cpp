@@ -60,6 +60,22 @@ int size_of(int dtype) { return dtype == POETX_FP32 ? 4 : dtype == POETX_BF16 ? 
 bool real_type(int dtype) { return dtype == POETX_FP32 || dtype == POETX_BF16; }
 
 constexpr int64_t kMaxRows = 0x7fffffff;
+
+int linear_type(const poetx_linear_desc* d) {
+  return d->dtype == POETX_INT8 ? poetx::LINEAR_I8 : d->dtype == POETX_BF16 ? poetx::LINEAR_BF16
+                                                                             : poetx::LINEAR_F32;
+}
+poetx_status linear_desc(const poetx_linear_desc* d) {
+  if (!d || d->T < 0) return POETX_ERR_INVALID_ARG;
+  if (d->m < 1 || d->m > poetx::kLinearMaxRows || d->n < 1 || d->T > kMaxRows) return POETX_ERR_SHAPE;
+  const bool q = d->dtype == POETX_INT8;
+  if (!q && !real_type(d->dtype)) return POETX_ERR_DTYPE;
+  if (d->y_dtype != POETX_FP32 && !(d->y_dtype == POETX_BF16 && d->dtype != POETX_FP32)) return POETX_ERR_DTYPE;
+  if (d->act < POETX_ACT_NONE || d->act > POETX_ACT_GELU_TANH) return POETX_ERR_INVALID_ARG;
+  // 128 * 128 * n stays within 32-bit integers
+  if (q && d->n > 131071) return POETX_ERR_UNSUPPORTED;
+  return POETX_OK;
+}
 constexpr int32_t kMaxTensors = 1 << 20;
 constexpr int64_t kMaxElems = int64_t(1) << 37;   // of one gradient tensor: a launch counts chunks in 31 bits
 
@@ -138,17 +154,22 @@ poetx_status poetx_rms_norm_backward(const poetx_norm_backward_desc* d, const vo
   return launched(poetx::launch_rms_norm_backward(a, d->dtype == POETX_BF16, s));
 }
 
+size_t poetx_linear_workspace(const poetx_linear_desc* d) {
+  if (linear_desc(d) != POETX_OK || d->T == 0) return 0;
+  poetx::LinearArgs a{};   // the split goes by the sizes alone
+  a.T = d->T;
+  a.m = d->m;
+  a.n = d->n;
+  const int splits = poetx::linear_splits(a, linear_type(d));
+  return splits > 1 ? (size_t)splits * d->T * ((d->m + 3) / 4 * 4) * 4 : 0;
+}
+
 poetx_status poetx_linear(const poetx_linear_desc* d, const void* X, const void* W, const float* sx,
                           const float* sw, const float* bias, const void* mul, const void* res, void* Y,
-                          void* stream) {
-  if (!d || d->T < 0) return POETX_ERR_INVALID_ARG;
-  if (d->m < 1 || d->m > poetx::kLinearMaxRows || d->n < 1 || d->T > kMaxRows) return POETX_ERR_SHAPE;
+                          void* ws, size_t ws_bytes, void* stream) {
+  const poetx_status ok = linear_desc(d);
+  if (ok != POETX_OK) return ok;
   const bool q = d->dtype == POETX_INT8;
-  if (!q && !real_type(d->dtype)) return POETX_ERR_DTYPE;
-  if (d->y_dtype != POETX_FP32 && !(d->y_dtype == POETX_BF16 && d->dtype != POETX_FP32)) return POETX_ERR_DTYPE;
-  if (d->act < POETX_ACT_NONE || d->act > POETX_ACT_GELU_TANH) return POETX_ERR_INVALID_ARG;
-  // 128 * 128 * n stays within 32-bit integers
-  if (q && d->n > 131071) return POETX_ERR_UNSUPPORTED;
   if (d->T == 0) return POETX_OK;
   if (!X || !W || !Y || q != (sx != nullptr) || q != (sw != nullptr)) return POETX_ERR_INVALID_ARG;
   const int es = size_of(d->dtype), ys = size_of(d->y_dtype);
@@ -164,7 +185,17 @@ poetx_status poetx_linear(const poetx_linear_desc* d, const void* X, const void*
   if ((overlap(y, mu) && !same(y, mu)) || (overlap(y, re) && !same(y, re))) return POETX_ERR_INVALID_ARG;
   poetx::LinearArgs a{X, W, sx, sw, bias, mul, res, Y, d->T, d->m, d->n,
                       x.ld, w.ld, y.ld, mu.ld, re.ld, d->act, d->y_dtype == POETX_BF16 ? 1 : 0};
-  const int type = q ? poetx::LINEAR_I8 : d->dtype == POETX_BF16 ? poetx::LINEAR_BF16 : poetx::LINEAR_F32;
+  const int type = linear_type(d);
+  const size_t need = poetx_linear_workspace(d);
+  if (need) {
+    if (!aligned(ws, 16)) return POETX_ERR_ALIGNMENT;
+    if (!ws || ws_bytes < need) return POETX_ERR_WORKSPACE;
+    const Mat part{ws, 1, (int64_t)need, (int64_t)need, 1};
+    for (const Mat& m : {x, w, y, mu, re, vec(sx, d->T), vec(sw, d->m), vec(bias, d->m)})
+      if (overlap(part, m)) return POETX_ERR_INVALID_ARG;
+    a.part = ws;
+    a.splits = poetx::linear_splits(a, type);
+  }
   return launched(poetx::launch_linear(a, type, (hipStream_t)stream));
 }
 

@@ -62,7 +62,7 @@ EXPORTED = (
     "poetx_scatter_cols", "poetx_timing_enable", "poetx_timing_read", "poetx_timing_reset",
     "poetx_forward_noalloc", "poetx_forward_noalloc_max_bytes",
     "poetx_add_rms_norm", "poetx_rms_norm_backward", "poetx_rms_norm_backward_workspace",
-    "poetx_linear", "poetx_clip_grads", "poetx_clip_grads_workspace",
+    "poetx_linear", "poetx_linear_workspace", "poetx_clip_grads", "poetx_clip_grads_workspace",
 )
 
 STAGES = ("build", "gather", "block_fwd", "w0_fwd", "scatter", "dq", "block_bwd", "w0_bwd",
@@ -156,7 +156,8 @@ def _load() -> ctypes.CDLL:
         "poetx_add_rms_norm": (st, [ctypes.POINTER(NormDesc)] + [vp] * 8),
         "poetx_rms_norm_backward": (st, [ctypes.POINTER(NormBackwardDesc)] + [vp] * 8 + [sz, vp]),
         "poetx_rms_norm_backward_workspace": (sz, [i64, i32]),
-        "poetx_linear": (st, [ctypes.POINTER(LinearDesc)] + [vp] * 9),
+        "poetx_linear": (st, [ctypes.POINTER(LinearDesc)] + [vp] * 9 + [sz, vp]),
+        "poetx_linear_workspace": (sz, [ctypes.POINTER(LinearDesc)]),
         "poetx_clip_grads": (st, [i32, vp, vp, vp, vp, ctypes.c_double, vp, vp, sz, vp]),
         "poetx_clip_grads_workspace": (sz, [i32]),
         "poetx_timing_enable": (st, [ctypes.c_uint32]),

@@ -57,22 +57,24 @@ void norms() {
 void products() {
   for (int dtype : {POETX_FP32, POETX_BF16, POETX_INT8})
     for (int64_t T : {1, 3, 20, 130, 700, 16384, 70000})
-      for (int n : {1, 70, 256, 4096})
+      for (int n : {1, 70, 256, 4096, 30000})
         for (int m : {1, 31, 264, 4096, 1 << 24})
           for (int act = POETX_ACT_NONE; act <= POETX_ACT_GELU_TANH; ++act) {
             const int y = dtype == POETX_FP32 ? POETX_FP32 : POETX_BF16;
             poetx_linear_desc d{T, m, n, dtype, y, act, n, n, m, m, m + 3};
             const float* s = dtype == POETX_INT8 ? fdev(3) : nullptr;
-            EXPECT(poetx_linear(&d, dev(1), dev(2), s, s, fdev(4), dev(5), dev(6), dev(7), nullptr) ==
+            const size_t wsb = poetx_linear_workspace(&d);
+            char* const ws = wsb ? dev(8) : nullptr;
+            EXPECT(poetx_linear(&d, dev(1), dev(2), s, s, fdev(4), dev(5), dev(6), dev(7), ws, wsb, nullptr) ==
                    POETX_ERR_HIP);
-            EXPECT(poetx_linear(&d, dev(1), dev(2), s, s, nullptr, dev(5), nullptr, dev(5), nullptr) ==
+            EXPECT(poetx_linear(&d, dev(1), dev(2), s, s, nullptr, dev(5), nullptr, dev(5), ws, wsb, nullptr) ==
                    POETX_ERR_HIP);
-            EXPECT(poetx_linear(&d, dev(1), dev(2), s, s, nullptr, nullptr, dev(6), dev(2), nullptr) ==
+            EXPECT(poetx_linear(&d, dev(1), dev(2), s, s, nullptr, nullptr, dev(6), dev(2), ws, wsb, nullptr) ==
                    POETX_ERR_INVALID_ARG);
           }
   poetx_linear_desc d{0x7fffffff, 1, 1, POETX_BF16, POETX_BF16, 0, INT64_MAX, 1, 1, 1, 1};
-  EXPECT(poetx_linear(&d, dev(1), dev(2), nullptr, nullptr, nullptr, nullptr, nullptr, dev(3), nullptr) ==
-         POETX_ERR_SHAPE);
+  EXPECT(poetx_linear(&d, dev(1), dev(2), nullptr, nullptr, nullptr, nullptr, nullptr, dev(3), nullptr, 0,
+                      nullptr) == POETX_ERR_SHAPE);
 }
 
 void clips() {

@@ -78,12 +78,13 @@ def test_norm_backward_workspace():
 
 
 def linear(T=4, m=32, n=64, dtype=px.POETX_BF16, y_dtype=px.POETX_BF16, act=0, ld=(64, 64, 32, 32, 32), X=A, W=B,
-           sx=None, sw=None, bias=C, mul=D, res=E, Y=F, null=False):
+           sx=None, sw=None, bias=C, mul=D, res=E, Y=F, null=False, ws=None, wsb=0):
     d = px.LinearDesc(T, m, n, dtype, y_dtype, act, *ld)
-    return L.poetx_linear(None if null else d, X, W, sx, sw, bias, mul, res, Y, None)
+    return L.poetx_linear(None if null else d, X, W, sx, sw, bias, mul, res, Y, ws, wsb, None)
 
 
 Q = dict(dtype=px.POETX_INT8, sx=G, sw=H)
+LONG = dict(T=8, n=16384, ld=(16384, 16384, 32, 32, 32))
 
 
 @pytest.mark.parametrize("kw, status", [
@@ -102,9 +103,20 @@ Q = dict(dtype=px.POETX_INT8, sx=G, sw=H)
     (dict(Q, sx=G + 2), ALIGN), (dict(mul=D + 1), ALIGN), (dict(res=E + 1), ALIGN),
     (dict(Y=A), INV), (dict(Y=B), INV), (dict(Y=C), INV), (dict(Y=D + 2), INV), (dict(Y=E + 64), INV),
     (dict(Q, Y=G), INV), (dict(Y=D, ld=(64, 64, 64, 32, 32)), INV),
+    # a long n, shared by workgroups whose sums need room
+    (dict(LONG), WS), (dict(LONG, ws=H), WS), (dict(LONG, ws=H + 8, wsb=1 << 20), ALIGN),
+    (dict(LONG, ws=A, wsb=1 << 20), INV), (dict(LONG, ws=F, wsb=1 << 20), INV),
 ])
 def test_linear_refusals(kw, status):
     assert linear(**kw) == status
+
+
+def test_linear_workspace():
+    f = L.poetx_linear_workspace
+    d = lambda T, m, n, dt=px.POETX_BF16: px.LinearDesc(T, m, n, dt, px.POETX_FP32, 0)  # noqa: E731
+    assert f(None) == 0 and f(d(0, 32, 16384)) == 0 and f(d(8, 0, 16384)) == 0
+    assert f(d(1, 32, 65536)) == 0 and f(d(8, 32, 256)) == 0 and f(d(16384, 4096, 4096)) == 0
+    assert f(d(8, 31, 16384)) % (8 * 32 * 4) == 0 and f(d(8, 31, 16384)) >= 2 * 8 * 32 * 4
 
 
 def clip(grads=(A, B), ns=(10, 20), dtypes=(0, 1), outs=(C, D), max_norm=1.0, norm=E, ws=H, wsb=None, count=None):

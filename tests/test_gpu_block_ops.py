@@ -332,7 +332,8 @@ def run_linear(c, act, **kw):
 LINEAR_SIZES = [(1, 1, 1), (1, 64, 16), (1, 2048, 300), (1, 77, 129), (2, 1000, 33), (3, 136, 40), (4, 4112, 17),
                 (5, 64, 64), (7, 100, 50), (16, 256, 130), (17, 333, 31), (24, 4096, 48), (33, 512, 100),
                 (64, 1040, 96), (65, 64, 128), (100, 1, 100), (127, 8, 5), (128, 128, 128), (129, 100, 257),
-                (256, 2048, 256), (300, 1005, 200), (513, 320, 256), (1031, 192, 384), (2000, 130, 77)]
+                (256, 2048, 256), (300, 1005, 200), (513, 320, 256), (1031, 192, 384), (2000, 130, 77),
+                (14, 7184, 76), (33, 4112, 100), (9, 5311, 256), (40, 16400, 33), (6, 16384, 40), (70, 6160, 70)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32", "int8"])

@@ -373,17 +373,19 @@ hipError_t launch_piece(const LinearArgs& a, int type, hipStream_t s) {
 
 }  // namespace
 
-// Where a grid of 32 x 32 tiles fills at most half the CUs and n is long, several
-// workgroups share n: as many as fill the CUs, each with at least 16 stages of 128
-// bytes. Worth its second launch (3 us) from 96 stages on, fp32, whose stages take
-// the matrix units four times as long, from 24: LINEAR_SPLIT_FIGURES
+// Where 32 x 32 tiles fill at most a third of the CUs and n is long, several
+// workgroups share n: as many as fill the CUs, each with at least 12 stages of 128
+// bytes (fp32, whose stages take the matrix units four times as long, 6). It pays for
+// the second launch from 48 stages on (bf16 53 x 4624 x 80 13.5 -> 9.4 us, 73 stages;
+// 6 x 2816 x 102 7.4 -> 8.6 us, 44), fp32 from 20 (62 x 700 x 256 9.4 -> 8.5 us), and
+// not for two workgroups a tile (16 x 11008 x 4096 INT8 11.8 -> 13.9 us).
 int linear_splits(const LinearArgs& a, int type) {
   const int es = type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1;
   const long long stages = ((long long)a.n * es + 127) / 128;
   const long long tiles = ((a.T + 31) / 32) * ((a.m + 31) / 32);
-  if (a.T <= 4 || tiles > 128) return 1;
-  if (stages < (type == LINEAR_F32 ? 24 : 96)) return 1;
-  const long long per = type == LINEAR_F32 ? 8 : 16;
+  if (a.T <= 4 || tiles > 85) return 1;
+  if (stages < (type == LINEAR_F32 ? 20 : 48)) return 1;
+  const long long per = type == LINEAR_F32 ? 6 : 12;
   return (int)std::max(1LL, std::min({32LL, 256 / tiles, stages / per}));
 }
 

@@ -753,6 +753,47 @@ def test_graphs_share_nothing():
             assert all(torch.equal(p, q) for p, q in zip(a, b)), it
 
 
+def test_shared_sums_on_two_streams_and_graphs():
+    """Products whose n several workgroups share: calls side by side on two streams, and two graphs of them
+    replayed side by side, each have sums of their own."""
+    import torch
+    import orthogonal_equivalence_cayley_amd as oec
+    from orthogonal_equivalence_cayley_amd import poetx as px
+    g = gen(12)
+    T, n, m = 9, 16384, 72
+    assert px.LIB.poetx_linear_workspace(px.LinearDesc(T, m, n, px.POETX_BF16, px.POETX_BF16, 0)) > 0
+    W = rand(g, m, n, dtype="bf16", scale=1 / 128).cuda()
+    xs = [rand(g, T, n, dtype="bf16").cuda() for _ in range(2)]
+    want = [oec.linear(x, W) for x in xs]
+    assert not torch.equal(want[0], want[1])
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                got.append(oec.linear(x, W))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs, outs = [], []
+    for x in xs:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append([oec.linear(x, W) for _ in range(3)])
+        graphs.append(gr)
+    for it in range(4):
+        for x in xs:
+            x.mul_(1.25)
+        want = [oec.linear(x, W) for x in xs]
+        torch.cuda.synchronize()
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+        torch.cuda.synchronize()
+        for o, v in zip(outs, want):
+            assert all(torch.equal(y, v) for y in o), it
+
+
 def test_merged_block():
     """A feed-forward as it is served: norm, gate and up and down with merged POET-X layers, dense and INT8."""
     import torch

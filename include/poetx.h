@@ -432,7 +432,7 @@ poetx_status poetx_rms_norm_backward(const poetx_norm_backward_desc* desc, const
  *     the sum exact in 32-bit integers; n <= 131071.
  *   y_dtype: POETX_FP32 always; POETX_BF16 with dtype POETX_BF16 or POETX_INT8.
  *   ws device, poetx_linear_workspace(desc) bytes (0, and ws may be NULL, but for
- *     small results of a long n, which several workgroups share).
+ *     small results of a long n and more than 4 tokens, which workgroups share).
  * The order of a sum depends on sizes, strides and alignment alone. T = 0 is a
  * no-op. m <= 2^24 (POETX_ERR_SHAPE). */
 typedef enum {

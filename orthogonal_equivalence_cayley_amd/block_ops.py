@@ -180,7 +180,7 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     ld_m = m if mul is None else _matrix("mul", mul, dev, shape, yt)
     ld_r = m if residual is None else _matrix("residual", residual, dev, shape, yt)
     d = _px.LinearDesc(T, m, n, _PX_DTYPE[dt], _PX_DTYPE[yt], _ACT[act], ld_x, ld_w, ld_y, ld_m, ld_r)
-    wsb = _LIB.poetx_linear_workspace(d)
+    wsb = _LIB.poetx_linear_workspace(d) if T > 4 else 0
     ws = torch.empty(wsb, dtype=torch.uint8, device=X.device) if wsb else None
     _call(_LIB.poetx_linear, "poetx_linear", dev, d, X.data_ptr(), W.data_ptr(), sx, sw, b, _ptr(mul),
           _ptr(residual), out.data_ptr(), _ptr(ws), wsb)

@@ -226,9 +226,8 @@ __global__ __launch_bounds__(kThr) void add_rms_norm_kernel(NormArgs a) {
 }
 
 // Rows too long for registers: one workgroup to a row, which is read again for
-// each pass (from the caches mostly). x and r are read again, never H, so H may
-// be x or r only where the registers hold the row; here the sum is taken from H
-// once it is written.
+// each pass (from the caches mostly). Where H is written its values are what is
+// read again, each by the thread that wrote it, so H may be X or R itself.
 template <typename E>
 __global__ __launch_bounds__(kThr) void add_rms_norm_long_kernel(NormArgs a) {
   __shared__ double red[4];

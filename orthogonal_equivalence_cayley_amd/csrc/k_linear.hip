@@ -392,9 +392,10 @@ int linear_splits(const LinearArgs& a, int type) {
 hipError_t launch_linear(const LinearArgs& a, int type, hipStream_t s) {
   if (a.T <= 0 || a.m <= 0 || a.n <= 0 || a.m > kLinearMaxRows) return hipErrorInvalidValue;
   if (a.y_bf16 && type == LINEAR_F32) return hipErrorInvalidValue;
-  // A launch counts threads in 32 bits: at most 2^22 of the smallest tiles. One
-  // launch for any size but results of 2^32 elements and more.
-  const long long step = std::max(256LL, (1LL << 32) / a.m / 256 * 256);
+  // A launch counts threads in 32 bits: at most 2^22 of the smallest tiles, of 512
+  // threads. One launch for any size but results of 2^32 elements and more, the
+  // columns counted in whole tiles of 32.
+  const long long step = std::max(256LL, (1LL << 22) / ((a.m + 31) / 32) * 32 / 256 * 256);
   const int es = type == LINEAR_F32 ? 4 : type == LINEAR_BF16 ? 2 : 1, ys = a.y_bf16 ? 2 : 4;
   const auto off = [](const void* p, long long bytes) {
     return p ? static_cast<const void*>(static_cast<const char*>(p) + bytes) : nullptr;

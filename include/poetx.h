@@ -434,7 +434,8 @@ poetx_status poetx_rms_norm_backward(const poetx_norm_backward_desc* desc, const
  *   ws device, poetx_linear_workspace(desc) bytes (0, and ws may be NULL, but for
  *     small results of a long n and more than 4 tokens, which workgroups share).
  * The order of a sum depends on sizes, strides and alignment alone. T = 0 is a
- * no-op. m <= 2^24 (POETX_ERR_SHAPE). */
+ * no-op. m <= 2^24 (POETX_ERR_SHAPE). A sum of -inf is 0 behind POETX_ACT_RELU and
+ * POETX_ACT_GELU, NaN behind POETX_ACT_SILU and POETX_ACT_GELU_TANH. */
 typedef enum {
   POETX_ACT_NONE = 0,
   POETX_ACT_RELU = 1,

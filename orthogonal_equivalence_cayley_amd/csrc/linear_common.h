@@ -133,6 +133,33 @@ __device__ __forceinline__ float half_erfc(float x) {
   p = fmaf(p, t, 0.254829592f);
   return 0.5f * p * t * __expf(-y * y);
 }
+// z (1 + erf(z / sqrt 2)) / 2 = max(z, 0) - a Q(a) with a = |z| and the normal
+// distribution's tail Q(a) = t P(1 - 2 t) exp(-a^2 / 2), t = 1 / (1 + 0.265 a): P of
+// degree 8 fitted for the least relative error over 0 <= a <= 13.3, 1.1e-8 (a
+// Chebyshev basis, least squares with weights raised where the error is largest).
+// Nothing cancels, so the result is within 14 units of 2^-24 of its own size down to
+// where exp(-a^2 / 2) leaves the normal range (1 + erf: 4 % off at -5, zero at -5.5);
+// the bits a^2 and its product with log2(e) lose go back in behind the exponential.
+// 16384 x 256 x 4096 bf16 to fp32: 103 us; 110 with 1 + erff, 137 with the library's
+// erfcf.
+__device__ __forceinline__ float gelu(float z) {
+  const float m = fabsf(z), a = m > 16.0f ? 16.0f : m;   // infinities end at Q = 0; NaN stays
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.265f, a, 1.0f)), q = fmaf(-2.0f, t, 1.0f);
+  float p = fmaf(1.207531476e-4f, q, 1.64155385e-4f);
+  p = fmaf(p, q, -1.113167465e-3f);
+  p = fmaf(p, q, 1.363363395e-4f);
+  p = fmaf(p, q, 1.048083255e-2f);
+  p = fmaf(p, q, -4.103577954e-2f);
+  p = fmaf(p, q, 9.442066913e-2f);
+  p = fmaf(p, q, -1.56393656e-1f);
+  p = fmaf(p, q, 1.989619743e-1f);
+  constexpr float kC = -0.72134752044f, kCLow = -0.72134752044448170368 - (double)kC;   // -log2(e) / 2
+  const float s = a * a, k = s * kC;
+  const float low = fmaf(fmaf(a, a, -s), kC, fmaf(s, kCLow, fmaf(s, kC, -k)));
+  float e = __builtin_amdgcn_exp2f(k);
+  e = fmaf(e, low * 0.69314718056f, e);
+  return fmaxf(z, 0.0f) - a * (t * p * e);
+}
 template <bool BF16>
 __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
@@ -144,7 +171,7 @@ __device__ __forceinline__ float activate(float z, int act) {
         const float e = h == 0.0f ? 0.0f : z * h;   // an infinite z too
         return z > 0.0f ? z - e : e;
       } else {
-        return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        return gelu(z);
       }
     case POETX_ACT_GELU_TANH: {
       const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);

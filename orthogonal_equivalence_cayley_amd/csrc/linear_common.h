@@ -122,42 +122,45 @@ __device__ __forceinline__ float logistic(float z) {
   if constexpr (BF16) return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
   else return 1.0f / (1.0f + expf(-z));
 }
-// erfc(|x| / sqrt 2) / 2 within 0.75e-7 (Abramowitz and Stegun 7.1.26), for
-// results that are rounded to bf16
-__device__ __forceinline__ float half_erfc(float x) {
-  const float y = fabsf(x) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, y, 1.0f));
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  return 0.5f * p * t * __expf(-y * y);
-}
 // z (1 + erf(z / sqrt 2)) / 2 = max(z, 0) - a Q(a) with a = |z| and the normal
-// distribution's tail Q(a) = t P(1 - 2 t) exp(-a^2 / 2), t = 1 / (1 + 0.265 a): P of
-// degree 8 fitted for the least relative error over 0 <= a <= 13.3, 1.1e-8 (a
-// Chebyshev basis, least squares with weights raised where the error is largest).
-// Nothing cancels, so the result is within 14 units of 2^-24 of its own size down to
-// where exp(-a^2 / 2) leaves the normal range (1 + erf: 4 % off at -5, zero at -5.5);
-// the bits a^2 and its product with log2(e) lose go back in behind the exponential.
-// 16384 x 256 x 4096 bf16 to fp32: 103 us; 110 with 1 + erff, 137 with the library's
-// erfcf.
+// distribution's tail Q(a) = t P(1 - 2 t) exp(-a^2 / 2), t = 1 / (1 + 0.265 a), P
+// fitted for the least relative error over 0 <= a <= 13.3 (a Chebyshev basis, least
+// squares with weights raised where the error is largest): 1.1e-8 with degree 8, and
+// 6.2e-7 with 6, for results that are rounded to bf16. Nothing cancels, so the result
+// is within 14 units of 2^-24 of its own size down to where exp(-a^2 / 2) leaves the
+// normal range (1 + erf: 4 % off at -5, zero at -5.5); the bits a^2 and its product
+// with log2(e) lose go back in behind the exponential, but for bf16: 11 and (3 / 2)
+// z^2 units more. 16384 x 256 x 4096 bf16 to fp32 103 us (110 with 1 + erff, 137 with
+// the library's erfcf), to bf16 91 us (93.5 with degree 8).
+template <bool BF16>
 __device__ __forceinline__ float gelu(float z) {
   const float m = fabsf(z), a = m > 16.0f ? 16.0f : m;   // infinities end at Q = 0; NaN stays
   const float t = __builtin_amdgcn_rcpf(fmaf(0.265f, a, 1.0f)), q = fmaf(-2.0f, t, 1.0f);
-  float p = fmaf(1.207531476e-4f, q, 1.64155385e-4f);
-  p = fmaf(p, q, -1.113167465e-3f);
-  p = fmaf(p, q, 1.363363395e-4f);
-  p = fmaf(p, q, 1.048083255e-2f);
-  p = fmaf(p, q, -4.103577954e-2f);
-  p = fmaf(p, q, 9.442066913e-2f);
-  p = fmaf(p, q, -1.56393656e-1f);
-  p = fmaf(p, q, 1.989619743e-1f);
+  float p;
+  if constexpr (BF16) {
+    p = fmaf(-1.059172291e-3f, q, 2.527494554e-4f);
+    p = fmaf(p, q, 1.047615789e-2f);
+    p = fmaf(p, q, -4.106033863e-2f);
+    p = fmaf(p, q, 9.44208143e-2f);
+    p = fmaf(p, q, -1.563923402e-1f);
+    p = fmaf(p, q, 1.989619594e-1f);
+  } else {
+    p = fmaf(1.207531476e-4f, q, 1.64155385e-4f);
+    p = fmaf(p, q, -1.113167465e-3f);
+    p = fmaf(p, q, 1.363363395e-4f);
+    p = fmaf(p, q, 1.048083255e-2f);
+    p = fmaf(p, q, -4.103577954e-2f);
+    p = fmaf(p, q, 9.442066913e-2f);
+    p = fmaf(p, q, -1.56393656e-1f);
+    p = fmaf(p, q, 1.989619743e-1f);
+  }
   constexpr float kC = -0.72134752044f, kCLow = -0.72134752044448170368 - (double)kC;   // -log2(e) / 2
   const float s = a * a, k = s * kC;
-  const float low = fmaf(fmaf(a, a, -s), kC, fmaf(s, kCLow, fmaf(s, kC, -k)));
   float e = __builtin_amdgcn_exp2f(k);
-  e = fmaf(e, low * 0.69314718056f, e);
+  if constexpr (!BF16) {
+    const float low = fmaf(fmaf(a, a, -s), kC, fmaf(s, kCLow, fmaf(s, kC, -k)));
+    e = fmaf(e, low * 0.69314718056f, e);
+  }
   return fmaxf(z, 0.0f) - a * (t * p * e);
 }
 template <bool BF16>
@@ -165,14 +168,7 @@ __device__ __forceinline__ float activate(float z, int act) {
   switch (act) {
     case POETX_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
     case POETX_ACT_SILU: return z * logistic<BF16>(z);
-    case POETX_ACT_GELU:
-      if constexpr (BF16) {
-        const float h = half_erfc(z);
-        const float e = h == 0.0f ? 0.0f : z * h;   // an infinite z too
-        return z > 0.0f ? z - e : e;
-      } else {
-        return gelu(z);
-      }
+    case POETX_ACT_GELU: return gelu<BF16>(z);
     case POETX_ACT_GELU_TANH: {
       const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
       // (1 + tanh u) / 2 is the logistic function of 2 u

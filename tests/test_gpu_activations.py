@@ -57,3 +57,21 @@ def test_gelu_of_negative_arguments_fp32(T, n, dt):
     tol = 14 * U * v.abs()
     bad = (y - v).abs() > tol
     assert not bad.any(), [(float(a), float(b), float(c)) for a, b, c in zip(z[bad][:5], y[bad][:5], v[bad][:5])]
+
+
+@pytest.mark.parametrize("T, n", [(1, 8), (40, 3), (300, 8), (16390, 64)])
+def test_gelu_of_negative_arguments_bf16(T, n):
+    """bf16 results by half a step of their own, far into the tail, and the limits at the ends."""
+    import torch
+    log(f"gelu bf16 T={T} n={n}")
+    z = torch.linspace(-13, 6, 1032).bfloat16()
+    z[-3:] = torch.tensor([-math.inf, math.inf, math.nan]).bfloat16()
+    y = at_arguments(z, "gelu", T, n, torch.bfloat16, torch.bfloat16)
+    assert y[-3] == 0 and y[-2] == math.inf and math.isnan(y[-1])
+    z, y = z[:-3].double(), y[:-3]
+    v = gelu_exact(z)
+    # the steps above with a fit of 10.5 units; the exponential's argument z^2 / 2 is off by three of its roundings,
+    # (3 / 2) z^2 units; half a step
+    tol = ((25 + 2 * z ** 2) * U + 2.0 ** -8) * v.abs()
+    bad = (y - v).abs() > tol
+    assert not bad.any(), [(float(a), float(b), float(c)) for a, b, c in zip(z[bad][:5], y[bad][:5], v[bad][:5])]

@@ -410,7 +410,9 @@ poetx_status poetx_add_rms_norm(const poetx_norm_desc* desc, const void* X, cons
  *   G [T, dim]    G_H [T, dim] or NULL    H [T, dim]: h (X where there was no r)
  *   w fp32 [dim]  rstd fp32 [T]           G_X [T, dim]: dx; may be G or G_H itself
  *   g_w fp32 [dim]                        ws poetx_rms_norm_backward_workspace bytes
- * Deterministic: sums run in a fixed order. T = 0 writes zero g_w. */
+ * The terms of g_w are fp32, their sums 64-bit but for the partial sums of at most
+ * 512 shares of the rows, each rounded to fp32 once. Deterministic: sums run in a
+ * fixed order. T = 0 writes zero g_w. */
 typedef struct {
   int64_t T;
   int32_t dim;

@@ -5,8 +5,9 @@
 // integers), the epilogue in fp32, one rounding at the end.
 //
 // Four kernels:
-//  * one to four tokens, linear_rows: every wave takes a row of W and multiplies on
-//    the vector units: bound by the weight's bytes (2048 to 5632 bf16 6.1 us).
+//  * few tokens (few_rows: one to four), linear_rows: every wave takes a row of W and
+//    multiplies on the vector units: bound by the weight's bytes (one token, 2048 to
+//    5632 bf16 6.1 us).
 //  * linear_pipe (k_linear_pipe.hip) and linear_ring (k_linear_ring.hip): tiles
 //    filled by direct-to-LDS loads, for rows of whole 128- and 16-byte pieces.
 //  * linear_tile: tiles filled through registers, any sizes and alignment.
@@ -278,7 +279,9 @@ hipError_t launch_rows(const LinearArgs& a, int type, hipStream_t s) {
 // the row): `first` for a grid of up to 256 tiles, one to a CU, and `round` for
 // every 256 tiles of a grid where the CUs are full; measured at 2048 x 2048
 // weights and 80 to 16384 tokens. bf16 and INT8 cost the same a byte; fp32 is bound
-// by its matrix rate, so its cost goes by the tile's area. E.g. bf16 1024 tokens:
+// by its matrix rate, so its cost goes by the tile's area. What a tile takes to start
+// and in its epilogue is not counted apart: at n of a few stages the choice can be
+// off (2455 x 256 x 3352 bf16 23.8 us, the vendor library 20.5). E.g. bf16 1024 tokens:
 // 128 x 128 26.5 us, 128 x 64 15.7, 64 x 64 16.8, 32 x 32 27.9; 16384 tokens: 256 x
 // 256 108 us, 128 x 128 141, 128 x 64 173.
 struct Cost {

@@ -7,9 +7,9 @@
 // loads and products one after the other: 31 against 22 us a 1024 x 2048 x 2048
 // bf16 product in 128 x 128 tiles; more stages in flight changed nothing.) With
 // KS = 2 a second group of four waves takes the other half of n, for grids that
-// leave CUs idle (16 x 2048 x 5632 7.5 -> 7.0 us, 16 x 5632 x 2048 14.1 -> 11.5 us),
-// and with PART several workgroups share n and leave their sums to linear_join
-// (k_linear.hip).
+// leave CUs idle (bf16, the weight from memory: 16 x 2048 x 5632 10.8 -> 8.9 us, 16 x
+// 4096 x 4096 17.5 -> 14.9 us), and with PART several workgroups share n and leave
+// their sums to linear_join (k_linear.hip).
 //
 // Rows past the last token or weight row are clamped to it (not stored).
 // Requirements (linear_ring_supported): n and row strides of whole 16 bytes.

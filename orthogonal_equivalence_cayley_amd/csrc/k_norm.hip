@@ -9,9 +9,9 @@
 // dx), 7 with an INT8 output. A row is read once and stays in registers, one
 // wave or four to a row, 16-byte loads at any element alignment, every load of a
 // row (and, backward, of the next row) out before the first is used. Measured
-// with the inputs cold: 16384 x 2048 bf16 forward 43 us (6.2 TB/s; a kernel that
-// only adds two arrays into two others reaches 5.3 to 6.1 TB/s here), backward 45
-// + 5 us; 16384 x 4096 to INT8 85 us (5.5 TB/s); one row of 2048 2.7 us.
+// with the inputs cold: 16384 x 2048 bf16 forward 43 to 45 us (6.0 to 6.2 TB/s; a kernel that
+// only adds two arrays into two others reaches 5.3 to 6.1 TB/s here), backward 46
+// + 5 us; 16384 x 4096 to INT8 85 us (5.6 TB/s); one row of 2048 2.4 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -405,7 +405,7 @@ __global__ __launch_bounds__(kThr) void rms_norm_cols_kernel(NormBackArgs a, int
 
 // dw[c] = sum over the parts, in 64 bits and in a fixed order: 32 columns per
 // workgroup, its 32 half-waves take parts a stride apart, 16 loads out at once
-// (512 parts of 2048 columns 4.7 us, 502 of 1365 3.8 us; 5.4 with the loads behind
+// (512 parts of 2048 columns 5.0 us, 502 of 1365 3.9 us; 5.4 with the loads behind
 // the last whole batch one by one)
 constexpr int kRedThr = 1024, kRedCols = 32;
 __global__ __launch_bounds__(kRedThr) void sum_parts_kernel(const float* part, int nparts, int dim,
@@ -462,6 +462,10 @@ bool with_nv(int dim, int per, F f) {
   return true;
 }
 
+// Rows from which one wave takes a row: forward the border is here (1024 x 512 bf16
+// 3.6 against 4.3 us, 512 x 1024 4.6 against 3.9); backward four waves stay ahead up
+// to some 2000 rows (1024 x 1024 bf16 11.4 against 8.8 us, 2048 x 512 9.7 against 9.8,
+// 4096 x 512 11.5 against 13.8).
 constexpr long long kManyRows = 1024;
 
 template <typename E>

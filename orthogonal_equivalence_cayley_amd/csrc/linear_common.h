@@ -123,21 +123,26 @@ __device__ __forceinline__ float logistic(float z) {
   else return 1.0f / (1.0f + expf(-z));
 }
 // z (1 + erf(z / sqrt 2)) / 2 = max(z, 0) - a Q(a) with a = |z| and the normal
-// distribution's tail Q(a) = t P(1 - 2 t) exp(-a^2 / 2), t = 1 / (1 + 0.265 a), P
+// distribution's tail Q(a) = t P(q) exp(-a^2 / 2), t = 1 / (1 + c a), q = 1 - 2 t, P
 // fitted for the least relative error over 0 <= a <= 13.3 (a Chebyshev basis, least
-// squares with weights raised where the error is largest): 1.1e-8 with degree 8, and
+// squares with weights raised where the error is largest): 7.5e-9 with degree 9, and
 // 6.2e-7 with 6, for results that are rounded to bf16. Nothing cancels, so the result
-// is within 14 units of 2^-24 of its own size down to where exp(-a^2 / 2) leaves the
-// normal range (1 + erf: 4 % off at -5, zero at -5.5); the bits a^2 and its product
-// with log2(e) lose go back in behind the exponential, but for bf16: 11 and (3 / 2)
-// z^2 units more. 16384 x 256 x 4096 bf16 to fp32 103 us (110 with 1 + erff, 137 with
-// the library's erfcf), to bf16 91 us (93.5 with degree 8).
+// is within 14 units of 2^-24 of its own size (bf16: 11 and (3 / 2) z^2 more) down to
+// where exp(-a^2 / 2) leaves the normal range; 1 + erf is 4 % off at -5 and zero at
+// -5.5. Near a = 0 the tail moves three times as fast as t, so fp32 results put back
+// what the reciprocal lost (c a is exact there), and what a^2 and its product with
+// log2(e) lost goes back in behind the exponential: 0.7 units rms in 0 .. 1 and 1.2 in
+// -1 .. 0, about as 1 + erf, against 1.5 and 2.6. 16384 x 256 x 4096 bf16 to fp32 110 us
+// (111 with 1 + erff, 137 with the library's erfcf), to bf16 88 us.
 template <bool BF16>
 __device__ __forceinline__ float gelu(float z) {
   const float m = fabsf(z), a = m > 16.0f ? 16.0f : m;   // infinities end at Q = 0; NaN stays
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.265f, a, 1.0f)), q = fmaf(-2.0f, t, 1.0f);
-  float p;
+  constexpr float kC = -0.72134752044f, kCLow = -0.72134752044448170368 - (double)kC;   // -log2(e) / 2
+  const float s = a * a, k = s * kC;
+  float e = __builtin_amdgcn_exp2f(k), t, p;
   if constexpr (BF16) {
+    t = __builtin_amdgcn_rcpf(fmaf(0.265f, a, 1.0f));
+    const float q = fmaf(-2.0f, t, 1.0f);
     p = fmaf(-1.059172291e-3f, q, 2.527494554e-4f);
     p = fmaf(p, q, 1.047615789e-2f);
     p = fmaf(p, q, -4.106033863e-2f);
@@ -145,23 +150,24 @@ __device__ __forceinline__ float gelu(float z) {
     p = fmaf(p, q, -1.563923402e-1f);
     p = fmaf(p, q, 1.989619594e-1f);
   } else {
-    p = fmaf(1.207531476e-4f, q, 1.64155385e-4f);
-    p = fmaf(p, q, -1.113167465e-3f);
-    p = fmaf(p, q, 1.363363395e-4f);
-    p = fmaf(p, q, 1.048083255e-2f);
-    p = fmaf(p, q, -4.103577954e-2f);
-    p = fmaf(p, q, 9.442066913e-2f);
-    p = fmaf(p, q, -1.56393656e-1f);
-    p = fmaf(p, q, 1.989619743e-1f);
-  }
-  constexpr float kC = -0.72134752044f, kCLow = -0.72134752044448170368 - (double)kC;   // -log2(e) / 2
-  const float s = a * a, k = s * kC;
-  float e = __builtin_amdgcn_exp2f(k);
-  if constexpr (!BF16) {
+    const float ca = 0.25f * a;
+    t = __builtin_amdgcn_rcpf(1.0f + ca);
+    const float d = t * fmaf(-ca, t, 1.0f - t);
+    const float q = fmaf(-2.0f, d, fmaf(-2.0f, t, 1.0f));
+    t += d;
+    p = fmaf(-3.142248372e-5f, q, 4.828958238e-5f);
+    p = fmaf(p, q, 3.938651346e-4f);
+    p = fmaf(p, q, -8.796188821e-4f);
+    p = fmaf(p, q, -1.882281462e-3f);
+    p = fmaf(p, q, 1.510112642e-2f);
+    p = fmaf(p, q, -4.663071063e-2f);
+    p = fmaf(p, q, 9.678422074e-2f);
+    p = fmaf(p, q, -1.519741526e-1f);
+    p = fmaf(p, q, 1.888212839e-1f);
     const float low = fmaf(fmaf(a, a, -s), kC, fmaf(s, kCLow, fmaf(s, kC, -k)));
     e = fmaf(e, low * 0.69314718056f, e);
   }
-  return fmaxf(z, 0.0f) - a * (t * p * e);
+  return fmaf(-a, t * p * e, fmaxf(z, 0.0f));
 }
 template <bool BF16>
 __device__ __forceinline__ float activate(float z, int act) {

@@ -72,9 +72,6 @@ __global__ __launch_bounds__(kRowThr) void linear_rows_kernel(LinearArgs a) {
 }
 
 // ------------------------------------------------------------------ tiles
-// Barrier that waits for this wave's LDS traffic only: global loads stay in flight.
-__device__ __forceinline__ void lds_sync() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
 // BM tokens x BN rows of W per workgroup, four waves of BM/2 x BN/2 each, any
 // sizes and alignment. KB bytes of n per stage, two LDS buffers and one barrier a
 // stage; the global loads of the next two stages are under way in registers, and

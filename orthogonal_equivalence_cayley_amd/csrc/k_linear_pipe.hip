@@ -70,14 +70,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __bf16 a = static_cast<__bf16>(lo), b = static_cast<__bf16>(hi);
   return (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
 }
-template <int N>
-__device__ __forceinline__ void vm_wait() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void lds_sync() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 // Chunk c (16 bytes) of tile row r at slot 8 r + (c ^ ((r / 2) & 7)): the 16 rows
 // a quarter of a wave reads at one chunk fall in distinct banks. The swizzle only
 // permutes the chunk bits below a row's base, so a fragment's address is

@@ -26,14 +26,6 @@ using namespace lin;
 constexpr int kThr = 256;
 constexpr int kKB = 128;          // bytes of a row per stage
 
-template <int N>
-__device__ __forceinline__ void vm_wait() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void lds_sync() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 // 16 bytes per lane from base + off + k (below `bytes`) to lane * 16 behind `to`
 __device__ __forceinline__ void load_lds(const char* base, int bytes, unsigned char* to, uint32_t off, int k) {
   const __amdgpu_buffer_rsrc_t rs =

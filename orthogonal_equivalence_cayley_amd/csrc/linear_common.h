@@ -62,6 +62,16 @@ struct TypeF32 {
   }
 };
 
+// This wave's loads and stores but for the last N are done.
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Barrier that waits for this wave's LDS traffic only: global loads stay in flight.
+__device__ __forceinline__ void lds_sync() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // 16 bytes of a row of kb bytes from byte k on; what is behind its end counts as
 // zero and is not read. Global loads take any alignment on this target. A chunk
 // the end cuts is the row's last 16 bytes, moved into place, so that it costs one

@@ -75,3 +75,23 @@ def test_gelu_of_negative_arguments_bf16(T, n):
     tol = ((25 + 2 * z ** 2) * U + 2.0 ** -8) * v.abs()
     bad = (y - v).abs() > tol
     assert not bad.any(), [(float(a), float(b), float(c)) for a, b, c in zip(z[bad][:5], y[bad][:5], v[bad][:5])]
+
+
+@pytest.mark.parametrize("dt, out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("T, n", [(1, 8), (40, 3), (300, 8), (16390, 64)])
+def test_limits(T, n, dt, out):
+    """Infinite, largest and NaN sums, as the header states them."""
+    import torch
+    if dt == "f32" and T > 300:
+        T = 300
+    log(f"limits T={T} n={n} {dt} to {out}")
+    t = {"f32": torch.float32, "bf16": torch.bfloat16}
+    big = torch.finfo(t[dt]).max
+    z = torch.tensor([math.inf, big, -big, -math.inf, math.nan] + [0.0] * 1027)
+    at_end = {"none": -math.inf, "relu": 0.0, "gelu": 0.0, "silu": math.nan, "gelu_tanh": math.nan}
+    for act, end in at_end.items():
+        y = at_arguments(z, act, T, n, t[dt], t[out])
+        assert y[0] == math.inf and y[1] == big, act
+        assert y[2] == (-big if act == "none" else 0.0), act
+        assert y[3] == end or (math.isnan(end) and math.isnan(y[3])), act
+        assert math.isnan(y[4]) and not y[5:].any(), act

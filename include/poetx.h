@@ -424,6 +424,83 @@ poetx_status poetx_rms_norm_backward(const poetx_norm_backward_desc* desc, const
                                      const void* H, const float* w, const float* rstd, void* G_X,
                                      float* g_w, void* ws, size_t ws_bytes, void* stream);
 
+/* Dropout. An element of row t and column c is dropped where its 16 bits lie below
+ * q = rint(65536 p), and scaled by 65536 / (65536 - q) where not (q = 65536: all are
+ * dropped), so the mean stays for every p. The bits are a function of the seed, the
+ * site, t and c alone: Philox 4x32-10 of the counter (c / 8, t, site, 0) under the
+ * 64-bit key `seed`, 16 of its 128 bits for each of the 8 columns, the lower half of
+ * the first word first. No mask is stored: a call with the same rule makes the same
+ * one, forward or backward, whatever kernel or sizes. */
+typedef struct {
+  double p;                  /* 0 <= p <= 1; 0 drops nothing                    */
+  uint64_t seed;
+  const uint64_t* seed_dev;  /* device [1], or NULL: added to the seed when the
+                                kernel runs, so that a captured graph can be
+                                replayed with other masks                       */
+  uint32_t site;             /* which dropout of a model and step               */
+} poetx_dropout_rule;
+
+/* y = round(drop(x)), or round(r + drop(x)); the backward is the same call on the
+ * gradient, without R. A dropped infinity or NaN is 0.
+ *   X, Y [T, dim] (dtype)   R [T, dim] (dtype) or NULL; Y may be X or R itself
+ * T = 0 is a no-op. dim <= 2^24 (POETX_ERR_SHAPE). */
+typedef struct {
+  int64_t T;
+  int32_t dim;
+  int32_t dtype;             /* POETX_FP32 or POETX_BF16                        */
+  int64_t ld_x, ld_r, ld_y;
+  poetx_dropout_rule drop;
+} poetx_dropout_desc;
+poetx_status poetx_dropout(const poetx_dropout_desc* desc, const void* X, const void* R, void* Y, void* stream);
+
+/* Dropout, residual addition and layer norm:
+ *   h = round(drop(x) + r),  m = mean_j h_j,  s = (mean_j (h_j - m)^2 + eps)^(-1/2),
+ *   y_j = (h_j - m) s w_j + b_j, statistics in 64 bits, the rest in fp32, one rounding.
+ *   X [T, dim] (dtype)      R [T, dim] (dtype) or NULL
+ *   w fp32 [dim]            b fp32 [dim] or NULL (zero)
+ *   H [T, dim] (dtype) or NULL: h; may be X or R itself
+ *   Y [T, dim], scale: as in poetx_add_rms_norm, INT8 rows by the same rule
+ *   mean, rstd fp32 [T] or NULL: m and s, for the backward.
+ * T = 0 is a no-op. No row is touched behind the T-th. dim <= 2^24 (POETX_ERR_SHAPE),
+ * also in the backward. */
+typedef struct {
+  int64_t T;
+  int32_t dim;
+  int32_t dtype;             /* POETX_FP32 or POETX_BF16                        */
+  int32_t y_dtype;           /* dtype, or POETX_INT8                            */
+  int64_t ld_x, ld_r, ld_h, ld_y;
+  double eps;                /* finite, >= 0                                    */
+  poetx_dropout_rule drop;
+} poetx_layer_norm_desc;
+poetx_status poetx_add_layer_norm(const poetx_layer_norm_desc* desc, const void* X, const void* R, const float* w,
+                                  const float* b, void* H, void* Y, float* scale, float* mean, float* rstd,
+                                  void* stream);
+
+/* Backward of poetx_add_layer_norm (y_dtype = dtype, the same rule) from G = dL/dY and
+ * G_H, the gradient that reaches h through the residual stream: u = (h - m) s,
+ *   dr = round(dh),  dh = gh + s (g w - mean_j(g w) - u mean_j(g w u)),
+ *   dx = round(drop(dh)),  g_w[j] = sum_t g_tj u_tj,  g_b[j] = sum_t g_tj (overwritten)
+ *   G [T, dim]    G_H [T, dim] or NULL    H [T, dim]: h (X where it is x itself)
+ *   w fp32 [dim]  mean, rstd fp32 [T]     g_w, g_b fp32 [dim]
+ *   G_X [T, dim]: dx     G_R [T, dim] or NULL: dr, with dropout only (without, dr is
+ *     dx). Each may be G or G_H itself.
+ *   ws poetx_layer_norm_backward_workspace bytes
+ * The terms of g_w are fp32, the sums 64-bit but for the partial sums of at most 512
+ * shares of the rows, each rounded to fp32 once. Deterministic. T = 0 writes zero g_w
+ * and g_b. */
+typedef struct {
+  int64_t T;
+  int32_t dim;
+  int32_t dtype;
+  int64_t ld_g, ld_gh, ld_h, ld_gx, ld_gr;
+  poetx_dropout_rule drop;
+} poetx_layer_norm_backward_desc;
+size_t poetx_layer_norm_backward_workspace(int64_t T, int32_t dim);   /* 0 for bad sizes */
+poetx_status poetx_layer_norm_backward(const poetx_layer_norm_backward_desc* desc, const void* G, const void* G_H,
+                                       const void* H, const float* w, const float* mean, const float* rstd,
+                                       void* G_X, void* G_R, float* g_w, float* g_b, void* ws, size_t ws_bytes,
+                                       void* stream);
+
 /* Product with a weight that is not trained (W_out of poetx_merge_weight, or the
  * INT8 rows of poetx_quantize_weight) and its epilogue:
  *   Y = round(act(X W^T + bias) * mul + res), sums and epilogue in fp32.

@@ -1,7 +1,7 @@
 """The operators around a block's linears, through libpoetx: the residual's
-addition with the root-mean-square norm (forward and backward, output in the
-activations' dtype or as INT8 rows with scales), products with a weight that is
-no longer trained (bias, activation, gating operand and residual in the
+addition with the root-mean-square norm or, with dropout in front, the layer norm
+(forward and backward, output in the activations' dtype or as INT8 rows with scales),
+dropout alone, products with a weight that is no longer trained (bias, activation, gating operand and residual in the
 epilogue), and the clipping of all gradients by their global norm.
 
 As for the layers, forward and backward are explicit calls (autograd records
@@ -135,6 +135,153 @@ def add_rms_norm_backward(G_Y: torch.Tensor, H: torch.Tensor, weight: torch.Tens
     _call(_LIB.poetx_rms_norm_backward, "poetx_rms_norm_backward", dev, d, G_Y.data_ptr(), _ptr(G_H),
           H.data_ptr(), w, s, G_X.data_ptr(), gw, ws.data_ptr(), n)
     return G_X, g_weight
+
+
+_NO_DROP = _px.DropoutRule(0.0, 0, None, 0)
+
+
+def _drop_rule(p: float, seed, site: int, dev: int):
+    """The rule of one dropout; seed: a number, or an int64 tensor of one element on GPU dev."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must lie in [0, 1], got {p}")
+    if p == 0:
+        return _NO_DROP
+    if not 0 <= site < 2 ** 32:
+        raise ValueError(f"site must lie in [0, 2^32), got {site}")
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype != torch.int64 or seed.numel() != 1 or seed.get_device() != dev:
+            raise ValueError(f"seed must be a number, or one int64 value on cuda:{dev}")
+        return _px.DropoutRule(p, 0, seed.data_ptr(), site)
+    if not 0 <= seed < 2 ** 64:
+        raise ValueError(f"seed must lie in [0, 2^64), got {seed}")
+    return _px.DropoutRule(p, seed, None, site)
+
+
+def dropout(X: torch.Tensor, p: float, seed, site: int = 0, residual: Optional[torch.Tensor] = None,
+            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """X with elements dropped with probability p (to a multiple of 2^-16) and the others
+    scaled to keep the mean; with residual, the sum of both, rounded once.
+
+    X, residual [T, dim] bf16 or fp32. The mask is a function of seed, site and the
+    element's place: dropout_backward with the same p, seed and site makes it again.
+    site: the number of the dropout in the model (0 .. 2^32 - 1). seed: a number, or an
+    int64 tensor of one element on the GPU, read when the kernel runs (a captured graph
+    is replayed with another mask after seed.add_(1)). out: X or residual itself for an
+    update in place."""
+    dev, dt = X.get_device(), X.dtype
+    ld_x = _matrix("X", X, dev)
+    shape = X.shape
+    T, dim = shape
+    if dt not in _REAL:
+        raise ValueError(f"X: {dt}, expected bfloat16 or float32")
+    rule = _drop_rule(p, seed, site, dev)
+    ld_r = ld_y = dim
+    if residual is not None:
+        ld_r = _matrix("residual", residual, dev, shape, dt)
+    if out is None:
+        out = torch.empty_like(X, memory_format=torch.contiguous_format)
+    else:
+        ld_y = _matrix("out", out, dev, shape, dt)
+    d = _px.DropoutDesc(T, dim, _PX_DTYPE[dt], ld_x, ld_r, ld_y, rule)
+    _call(_LIB.poetx_dropout, "poetx_dropout", dev, d, X.data_ptr(), _ptr(residual), out.data_ptr())
+    return out
+
+
+def dropout_backward(G_Y: torch.Tensor, p: float, seed, site: int = 0,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of dropout's X from dL/dY (that of its residual is G_Y itself)."""
+    return dropout(G_Y, p, seed, site, out=out)
+
+
+class LayerNormOut(NamedTuple):
+    Y: torch.Tensor                  # normalised rows: X's dtype, or INT8
+    H: torch.Tensor                  # drop(X) + residual (X itself with neither)
+    mean: Optional[torch.Tensor]     # fp32 [T], with save
+    rstd: Optional[torch.Tensor]     # fp32 [T], with save
+    scale: Optional[torch.Tensor]    # fp32 [T], with quantize
+
+
+def add_layer_norm(X: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None, eps: float = 1e-5, p: float = 0.0, seed=0, site: int = 0,
+                   quantize: bool = False, save: bool = False, H: Optional[torch.Tensor] = None) -> LayerNormOut:
+    """h = dropout(X) + residual (rounded to the dtype), y = (h - mean h) / sqrt(var h + eps) * weight + bias.
+
+    X, residual [T, dim] bf16 or fp32; weight, bias fp32 [dim]. p, seed, site: as in
+    dropout. H: where h goes, X or residual itself for an update in place (default: a new
+    tensor). quantize: y as INT8 rows, y = scale * Y. save: keep mean and rstd for
+    add_layer_norm_backward."""
+    dev, dt = X.get_device(), X.dtype
+    ld_x = _matrix("X", X, dev)
+    shape = X.shape
+    T, dim = shape
+    if dt not in _REAL:
+        raise ValueError(f"X: {dt}, expected bfloat16 or float32")
+    rule = _drop_rule(p, seed, site, dev)
+    w = _vector("weight", weight, dim, dev)
+    b = None if bias is None else _vector("bias", bias, dim, dev)
+    ld_r = ld_h = dim
+    if residual is not None:
+        ld_r = _matrix("residual", residual, dev, shape, dt)
+    if H is not None:
+        ld_h = _matrix("H", H, dev, shape, dt)
+    elif residual is not None or p > 0:
+        H = torch.empty_like(X, memory_format=torch.contiguous_format)
+    code = _PX_DTYPE[dt]
+    Y = torch.empty_like(X, dtype=torch.int8 if quantize else dt, memory_format=torch.contiguous_format)
+    rows = torch.empty(2 * save + quantize, T, dtype=torch.float32, device=X.device) if save or quantize else None
+    mean, rstd = (rows[0], rows[1]) if save else (None, None)
+    scale = rows[-1] if quantize else None
+    d = _px.LayerNormDesc(T, dim, code, _px.POETX_INT8 if quantize else code, ld_x, ld_r, ld_h, dim, eps, rule)
+    _call(_LIB.poetx_add_layer_norm, "poetx_add_layer_norm", dev, d, X.data_ptr(), _ptr(residual), w, b, _ptr(H),
+          Y.data_ptr(), _ptr(scale), _ptr(mean), _ptr(rstd))
+    return LayerNormOut(Y, X if H is None else H, mean, rstd, scale)
+
+
+class LayerNormGrads(NamedTuple):
+    G_X: torch.Tensor
+    G_R: torch.Tensor                # of the residual: G_X itself without dropout
+    g_weight: torch.Tensor           # fp32 [dim]
+    g_bias: torch.Tensor             # fp32 [dim]
+
+
+def add_layer_norm_backward(G_Y: torch.Tensor, H: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
+                            rstd: torch.Tensor, G_H: Optional[torch.Tensor] = None, p: float = 0.0, seed=0,
+                            site: int = 0, G_X: Optional[torch.Tensor] = None,
+                            G_R: Optional[torch.Tensor] = None) -> LayerNormGrads:
+    """The gradients of add_layer_norm from dL/dY and, with G_H, the gradient that
+    reaches h through the residual stream. H, mean and rstd are those of the forward, p,
+    seed and site too. G_X, G_R: where they go, G_Y or G_H itself for an update in place
+    (G_R with dropout only)."""
+    dev, dt = G_Y.get_device(), G_Y.dtype
+    ld_g = _matrix("G_Y", G_Y, dev)
+    shape = G_Y.shape
+    T, dim = shape
+    if dt not in _REAL:
+        raise ValueError(f"G_Y: {dt}, expected bfloat16 or float32")
+    rule = _drop_rule(p, seed, site, dev)
+    ld_h = _matrix("H", H, dev, shape, dt)
+    w, m, s = _vector("weight", weight, dim, dev), _vector("mean", mean, T, dev), _vector("rstd", rstd, T, dev)
+    ld_gh = dim if G_H is None else _matrix("G_H", G_H, dev, shape, dt)
+    ld_gx = ld_gr = dim
+    if G_X is None:
+        G_X = torch.empty_like(G_Y, memory_format=torch.contiguous_format)
+    else:
+        ld_gx = _matrix("G_X", G_X, dev, shape, dt)
+    # p that rounds to no dropout at all: dr is dx
+    drops = round(p * 65536) > 0
+    if G_R is not None:
+        if not drops:
+            raise ValueError("G_R goes with dropout: without, it is G_X")
+        ld_gr = _matrix("G_R", G_R, dev, shape, dt)
+    elif drops:
+        G_R = torch.empty_like(G_Y, memory_format=torch.contiguous_format)
+    gw, gb = torch.empty(2, dim, dtype=torch.float32, device=G_Y.device).unbind(0)
+    n = _LIB.poetx_layer_norm_backward_workspace(T, dim)
+    ws = torch.empty(n, dtype=torch.uint8, device=G_Y.device)
+    d = _px.LayerNormBackwardDesc(T, dim, _PX_DTYPE[dt], ld_g, ld_gh, ld_h, ld_gx, ld_gr, rule)
+    _call(_LIB.poetx_layer_norm_backward, "poetx_layer_norm_backward", dev, d, G_Y.data_ptr(), _ptr(G_H), H.data_ptr(), w,
+          m, s, G_X.data_ptr(), _ptr(G_R), gw.data_ptr(), gb.data_ptr(), ws.data_ptr(), n)
+    return LayerNormGrads(G_X, G_X if G_R is None else G_R, gw, gb)
 
 
 def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",

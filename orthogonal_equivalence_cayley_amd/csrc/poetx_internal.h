@@ -259,6 +259,52 @@ constexpr int kNormRegDim = 4096;   // rows up to this length stay in registers 
 int norm_backward_parts(long long T);
 hipError_t launch_rms_norm_backward(const NormBackArgs& a, int bf16, hipStream_t s);
 
+// out[c] (c < dim0) and out1[c - dim0] = the sum of parts x dim partial sums (k_norm.hip)
+hipError_t launch_sum_parts(const float* part, int parts, int dim, float* out, int dim0, float* out1, hipStream_t s);
+
+// Which elements are dropped (dropout_common.h); threshold 0: none.
+struct DropArgs {
+  uint64_t seed;
+  const uint64_t* seed_dev;   // added to the seed, or null
+  uint32_t site;
+  uint32_t threshold;         // of 65536
+  float scale;
+};
+// Y = drop(X) (+ R) (k_dropout.hip); row strides in elements.
+struct DropoutArgs {
+  const void* X; const void* R; void* Y;   // R may be null
+  long long T; int dim;
+  long long ldx, ldr, ldy;
+  DropArgs drop;
+  uint32_t row0;   // the first row's number in the generator's counter (set by the launcher)
+};
+hipError_t launch_dropout(const DropoutArgs& a, int bf16, hipStream_t s);
+
+// Dropout, residual addition and layer norm (k_layer_norm.hip).
+struct LayerNormArgs {
+  const void* X; const void* R; const float* w; const float* b;   // R, b may be null
+  void* H; void* Y; float* scale; float* mean; float* rstd;       // H, mean, rstd may be null; scale with quant
+  long long T; int dim; int quant;
+  long long ldx, ldr, ldh, ldy;
+  double eps;
+  DropArgs drop;
+  uint32_t row0;
+};
+hipError_t launch_add_layer_norm(const LayerNormArgs& a, int bf16, hipStream_t s);
+struct LayerNormBackArgs {
+  const void* G; const void* GH; const void* H; const float* w; const float* mean; const float* rstd;   // GH may be null
+  void* GX; void* GR;      // GR (with dropout) may be null
+  float* dw; float* db;
+  float* part;             // layer_norm_backward_parts x 2 dim partial sums
+  float* rowc;             // 2 T values, for rows past layer_norm_back_reg_dim only
+  long long T; int dim;
+  long long ldg, ldgh, ldh, ldgx, ldgr;
+  DropArgs drop;
+};
+int layer_norm_backward_parts(long long T);
+int layer_norm_back_reg_dim(int bf16);   // rows up to this length stay in registers
+hipError_t launch_layer_norm_backward(const LayerNormBackArgs& a, int bf16, hipStream_t s);
+
 // Sum of squares and scaling of many tensors (k_clip.hip).
 struct ClipItem {
   const void* g; void* out;

@@ -62,6 +62,7 @@ EXPORTED = (
     "poetx_scatter_cols", "poetx_timing_enable", "poetx_timing_read", "poetx_timing_reset",
     "poetx_forward_noalloc", "poetx_forward_noalloc_max_bytes",
     "poetx_add_rms_norm", "poetx_rms_norm_backward", "poetx_rms_norm_backward_workspace",
+    "poetx_dropout", "poetx_add_layer_norm", "poetx_layer_norm_backward", "poetx_layer_norm_backward_workspace",
     "poetx_linear", "poetx_linear_workspace", "poetx_clip_grads", "poetx_clip_grads_workspace",
 )
 
@@ -103,6 +104,36 @@ class NormBackwardDesc(ctypes.Structure):
         ("T", ctypes.c_int64), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
         ("ld_g", ctypes.c_int64), ("ld_gh", ctypes.c_int64), ("ld_h", ctypes.c_int64),
         ("ld_gx", ctypes.c_int64),
+    ]
+
+
+class DropoutRule(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("seed_dev", ctypes.c_void_p),
+                ("site", ctypes.c_uint32)]
+
+
+class DropoutDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("ld_x", ctypes.c_int64), ("ld_r", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+        ("drop", DropoutRule),
+    ]
+
+
+class LayerNormDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("y_dtype", ctypes.c_int32),
+        ("ld_x", ctypes.c_int64), ("ld_r", ctypes.c_int64), ("ld_h", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64), ("eps", ctypes.c_double), ("drop", DropoutRule),
+    ]
+
+
+class LayerNormBackwardDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("ld_g", ctypes.c_int64), ("ld_gh", ctypes.c_int64), ("ld_h", ctypes.c_int64),
+        ("ld_gx", ctypes.c_int64), ("ld_gr", ctypes.c_int64), ("drop", DropoutRule),
     ]
 
 
@@ -156,6 +187,10 @@ def _load() -> ctypes.CDLL:
         "poetx_add_rms_norm": (st, [ctypes.POINTER(NormDesc)] + [vp] * 8),
         "poetx_rms_norm_backward": (st, [ctypes.POINTER(NormBackwardDesc)] + [vp] * 8 + [sz, vp]),
         "poetx_rms_norm_backward_workspace": (sz, [i64, i32]),
+        "poetx_dropout": (st, [ctypes.POINTER(DropoutDesc)] + [vp] * 4),
+        "poetx_add_layer_norm": (st, [ctypes.POINTER(LayerNormDesc)] + [vp] * 10),
+        "poetx_layer_norm_backward": (st, [ctypes.POINTER(LayerNormBackwardDesc)] + [vp] * 11 + [sz, vp]),
+        "poetx_layer_norm_backward_workspace": (sz, [i64, i32]),
         "poetx_linear": (st, [ctypes.POINTER(LinearDesc)] + [vp] * 9 + [sz, vp]),
         "poetx_linear_workspace": (sz, [ctypes.POINTER(LinearDesc)]),
         "poetx_clip_grads": (st, [i32, vp, vp, vp, vp, ctypes.c_double, vp, vp, sz, vp]),

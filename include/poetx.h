@@ -535,6 +535,44 @@ poetx_status poetx_linear(const poetx_linear_desc* desc, const void* X, const vo
                           const float* sw, const float* bias, const void* mul, const void* res, void* Y,
                           void* ws, size_t ws_bytes, void* stream);
 
+/* Cross entropy of a vocabulary's product, whose logits are never stored:
+ *   z_tv = sum_k x_tk w_vk,  lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_t,target(t)
+ *   X [T, n], W [V, n] (dtype)    target device int64 [T]
+ *   loss, lse fp32 [T]: a target equal to ignore_index has loss 0; another one outside
+ *     0 .. V - 1 has loss NaN.
+ *   ws poetx_linear_cross_entropy_workspace(desc) bytes
+ * Logits are sums in fp32. T = 0 is a no-op. No row is touched behind the T-th. T, V <=
+ * 2^24, n <= 2^16 (POETX_ERR_SHAPE), also in the backward. ld_gx, ld_gw and g_count are
+ * the backward's. */
+typedef struct {
+  int64_t T;
+  int32_t V, n;
+  int32_t dtype;             /* POETX_FP32 or POETX_BF16                        */
+  int64_t ld_x, ld_w, ld_gx, ld_gw;
+  int64_t g_count;           /* 1 or T                                          */
+  int64_t ignore_index;
+} poetx_cross_entropy_desc;
+size_t poetx_linear_cross_entropy_workspace(const poetx_cross_entropy_desc* desc);   /* 0 for a bad description */
+poetx_status poetx_linear_cross_entropy(const poetx_cross_entropy_desc* desc, const void* X, const void* W,
+                                        const int64_t* target, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                        void* stream);
+
+/* Its backward from g = dL/dloss, the logits computed again in pieces of the vocabulary:
+ *   d_tv = g_t (exp(z_tv - lse_t) - [v = target(t)]), 0 for ignored tokens,
+ *   G_X = round(d W),  G_W = round(d^T X) (overwritten).
+ *   g fp32 [g_count]: one for each token, or one for all    lse of the forward
+ *   G_X [T, n], G_W [V, n] (dtype); either may be NULL
+ *   ws poetx_linear_cross_entropy_backward_workspace(desc, need_x, need_w) bytes
+ * POETX_BF16: d is rounded to bf16 before the products that take it, without the factor
+ * g where it is one for all. Products are summed in fp32. A token whose target is neither
+ * in the vocabulary nor ignored makes its row of G_X and all of G_W NaN. What an ignored
+ * token's x holds reaches no gradient. Deterministic. T = 0 writes zero G_W. */
+size_t poetx_linear_cross_entropy_backward_workspace(const poetx_cross_entropy_desc* desc, int32_t need_x,
+                                                     int32_t need_w);
+poetx_status poetx_linear_cross_entropy_backward(const poetx_cross_entropy_desc* desc, const float* g, const void* X,
+                                                 const void* W, const int64_t* target, const float* lse, void* G_X,
+                                                 void* G_W, void* ws, size_t ws_bytes, void* stream);
+
 /* Global norm of count gradient tensors, and their clipping by it:
  *   norm = sqrt(sum of all squares) (64-bit sums, norm_out rounded once),
  *   c = min(1, max_norm / (norm + 1e-6)) as fp32,  out = round(c g).

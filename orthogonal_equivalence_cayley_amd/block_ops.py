@@ -1,8 +1,9 @@
 """The operators around a block's linears, through libpoetx: the residual's
 addition with the root-mean-square norm or, with dropout in front, the layer norm
 (forward and backward, output in the activations' dtype or as INT8 rows with scales),
-dropout alone, products with a weight that is no longer trained (bias, activation, gating operand and residual in the
-epilogue), and the clipping of all gradients by their global norm.
+dropout alone, products with a weight that is no longer trained (bias, activation,
+gating operand and residual in the epilogue), the cross entropy of a vocabulary's product
+without its logits, and the clipping of all gradients by their global norm.
 
 As for the layers, forward and backward are explicit calls (autograd records
 nothing), torch provides memory and the current stream of the tensors' device,
@@ -332,6 +333,74 @@ def linear(X: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     _call(_LIB.poetx_linear, "poetx_linear", dev, d, X.data_ptr(), W.data_ptr(), sx, sw, b, _ptr(mul),
           _ptr(residual), out.data_ptr(), _ptr(ws), wsb)
     return out
+
+
+class CrossEntropyOut(NamedTuple):
+    loss: torch.Tensor               # fp32 [T], 0 for ignored tokens
+    lse: torch.Tensor                # fp32 [T]: log sum exp of the token's logits, for the backward
+
+
+def _vocabulary(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor):
+    dev, dt = X.get_device(), X.dtype
+    ld_x, ld_w = _matrix("X", X, dev), _matrix("W", W, dev, None, dt)
+    if dt not in _REAL:
+        raise ValueError(f"X: {dt}, expected bfloat16 or float32")
+    T, n = X.shape
+    V, k = W.shape
+    if k != n:
+        raise ValueError(f"W: {k} columns for {n} of X")
+    if target.shape != (T,) or target.dtype != torch.int64 or target.get_device() != dev or not target.is_contiguous():
+        raise ValueError(f"target must be {T} contiguous int64 values on cuda:{dev}")
+    return dev, _px.CrossEntropyDesc(T, V, n, _PX_DTYPE[dt], ld_x, ld_w, n, n, 1, 0)
+
+
+def linear_cross_entropy(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
+                         ignore_index: int = -100) -> CrossEntropyOut:
+    """loss_t = log sum_v exp(x_t . w_v) - x_t . w_target(t), the logits X W^T never stored.
+
+    X [T, n], W [V, n] bf16 or fp32; target int64 [T]: a row of W, or ignore_index for a
+    token that does not count (loss 0; any other value outside the vocabulary: NaN)."""
+    dev, d = _vocabulary(X, W, target)
+    d.ignore_index = ignore_index
+    loss, lse = torch.empty(2, d.T, dtype=torch.float32, device=X.device).unbind(0)
+    n = _LIB.poetx_linear_cross_entropy_workspace(d)
+    ws = torch.empty(n, dtype=torch.uint8, device=X.device)
+    _call(_LIB.poetx_linear_cross_entropy, "poetx_linear_cross_entropy", dev, d, X.data_ptr(), W.data_ptr(),
+          target.data_ptr(), loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), n)
+    return CrossEntropyOut(loss, lse)
+
+
+def linear_cross_entropy_backward(G: torch.Tensor, X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
+                                  lse: torch.Tensor, ignore_index: int = -100, need_x: bool = True,
+                                  need_w: bool = True, G_X: Optional[torch.Tensor] = None,
+                                  G_W: Optional[torch.Tensor] = None):
+    """(G_X, G_W) from G = dL/dloss: fp32, one value for each token or one for all (the
+    mean's 1 / count). lse is linear_cross_entropy's. need_x, need_w: which are wanted (the
+    other is None). G_X, G_W: where they go, in X's dtype, overwritten."""
+    dev, d = _vocabulary(X, W, target)
+    T, dt = d.T, X.dtype
+    if G.numel() == 1:
+        G = G.reshape(1)
+    g = _vector("G", G, G.numel() if G.numel() == 1 else T, dev)
+    ls = _vector("lse", lse, T, dev)
+    if not need_x and not need_w:
+        raise ValueError("no gradient is wanted")
+    if (G_X is not None and not need_x) or (G_W is not None and not need_w):
+        raise ValueError("a place for a gradient that is not wanted")
+    if G_X is not None:
+        d.ld_gx = _matrix("G_X", G_X, dev, X.shape, dt)
+    elif need_x:
+        G_X = torch.empty_like(X, memory_format=torch.contiguous_format)
+    if G_W is not None:
+        d.ld_gw = _matrix("G_W", G_W, dev, W.shape, dt)
+    elif need_w:
+        G_W = torch.empty_like(W, memory_format=torch.contiguous_format)
+    d.ignore_index, d.g_count = ignore_index, G.numel()
+    n = _LIB.poetx_linear_cross_entropy_backward_workspace(d, need_x, need_w)
+    ws = torch.empty(n, dtype=torch.uint8, device=X.device)
+    _call(_LIB.poetx_linear_cross_entropy_backward, "poetx_linear_cross_entropy_backward", dev, d, g, X.data_ptr(),
+          W.data_ptr(), target.data_ptr(), ls, _ptr(G_X), _ptr(G_W), ws.data_ptr(), n)
+    return G_X, G_W
 
 
 class MergedLinear:

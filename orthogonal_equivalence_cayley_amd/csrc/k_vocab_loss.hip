@@ -1,0 +1,562 @@
+// The cross entropy of a vocabulary's product without its logits, forward and backward,
+// for any sizes, strides and alignment (k_vocab_loss_pipe.hip: many tokens in bf16):
+//
+//   z_tv = sum_k x_tk w_vk,  lse_t = log sum_v exp(z_tv),  loss_t = lse_t - z_t,target
+//   d_tv = g_t (exp(z_tv - lse_t) - [v = target]),  dX = d W,  dW = d^T X
+//
+// Forward: a tile of logits stays in registers, where each row's maximum and sum of
+// exponentials over the tile's columns are taken; vocab_join_kernel joins them. Backward,
+// in pieces of the vocabulary: the tile is multiplied again and left as d (in the
+// operands' type, which the products that follow take; d of a row sums to 0, so what its
+// rounding to bf16 costs is of the size of the result's own), then d W is added into dX
+// (fp32 across pieces, one rounding at the end) and d^T X is the piece's dW.
+//
+// Tiles as in linear_tile_kernel (k_linear.hip): four waves of BM/2 x BN/2, 128 bytes of
+// the summed axis a stage, two LDS buffers, the next two stages under way in registers.
+// An operand whose rows run along the other axis (W in d W, both in d^T X) is kept the way
+// it comes, 128 bytes' worth of summed rows of BM or BN columns, and read across: bf16 by
+// the transposing LDS read, fp32 by words. Its rows are padded by 32 bytes (fp32 16) and
+// every eight of them (bf16) by 128 more, so that the rows a read takes together fall in
+// distinct banks.
+#include <algorithm>
+
+#include "linear_common.h"
+#include "vocab_loss.h"
+
+namespace poetx {
+namespace {
+
+using namespace lin;
+using namespace vocab;
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kThr = 256;
+constexpr int kKB = 128;   // bytes of the summed axis a stage
+
+// An operand: R rows (of the result's axis) by 128 bytes of the summed axis a stage
+template <typename Ty, int R, bool ACROSS>
+struct Operand;
+
+// rows along the summed axis
+template <typename Ty, int R>
+struct Operand<Ty, R, false> {
+  static constexpr int ES = Ty::kSize, L = R / 32, BYTES = R * kKB;
+  const char* p[L];
+  __device__ __forceinline__ void init(const void* base, long long ld, int r0, int rows, int) {
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      p[i] = static_cast<const char*>(base) + (long long)min(r0 + i * 32 + (int)threadIdx.x / 8, rows - 1) * ld * ES;
+  }
+  // of the stage from element k0 on; zero from kend on
+  __device__ __forceinline__ void fetch(i32x4 (&r)[L], int k0, int kend) const {
+    const long long k = (long long)k0 * ES + (threadIdx.x % 8) * 16, kb = (long long)kend * ES;
+    if (k0 + kKB / ES <= kend) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) __builtin_memcpy(&r[i], p[i] + k, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < L; ++i) r[i] = load16<ES>(p[i], k, kb);
+    }
+  }
+  static __device__ __forceinline__ int slot(int r, int c) { return r * 8 + (c ^ ((r / 2) & 7)); }
+  static __device__ __forceinline__ void keep(char* st, const i32x4 (&r)[L]) {
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      reinterpret_cast<i32x4*>(st)[slot(i * 32 + (int)threadIdx.x / 8, (int)threadIdx.x % 8)] = r[i];
+  }
+  // 16 bytes along the summed axis of row r + (lane & 15), chunk 4 q + (lane >> 4)
+  static __device__ __forceinline__ i32x4 frag(const char* st, int r, int q, int lane) {
+    return reinterpret_cast<const i32x4*>(st)[slot(r + (lane & 15), q * 4 + (lane >> 4))];
+  }
+};
+
+// rows across it
+template <typename Ty, int R>
+struct Operand<Ty, R, true> {
+  static constexpr int ES = Ty::kSize, L = R / 32, K = kKB / ES;
+  static constexpr int CPR = R * ES / 16, RPL = kThr / CPR;   // chunks of a summed row, summed rows a load
+  static constexpr int PITCH = R * ES + (ES == 2 ? 32 : 16), BYTES = K * PITCH + (ES == 2 ? K / 8 * 128 : 0);
+  static_assert(RPL * L == K, "whole loads");
+  const char* p;   // the first summed row's first chunk of this thread
+  long long ld, c, cb;
+  bool whole;
+  __device__ __forceinline__ void init(const void* base, long long ld_, int r0, int rows, int) {
+    p = static_cast<const char*>(base);
+    ld = ld_ * ES;
+    c = (long long)r0 * ES + (threadIdx.x % CPR) * 16;
+    cb = (long long)rows * ES;
+    whole = r0 + R <= rows;
+  }
+  __device__ __forceinline__ void fetch(i32x4 (&r)[L], int k0, int kend) const {
+    const int k = k0 + (int)threadIdx.x / CPR;
+    if (whole && k0 + K <= kend) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) __builtin_memcpy(&r[i], p + (long long)(k + i * RPL) * ld + c, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        r[i] = i32x4{0, 0, 0, 0};
+        if (k + i * RPL < kend && c < cb) r[i] = load16<ES>(p + (long long)(k + i * RPL) * ld, c, cb);
+      }
+    }
+  }
+  static __device__ __forceinline__ int at(int k) { return k * PITCH + (ES == 2 ? (k >> 3) * 128 : 0); }
+  static __device__ __forceinline__ void keep(char* st, const i32x4 (&r)[L]) {
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      *reinterpret_cast<i32x4*>(st + at((int)threadIdx.x / CPR + i * RPL) + ((int)threadIdx.x % CPR) * 16) = r[i];
+  }
+  static __device__ __forceinline__ i32x4 frag(const char* st, int r, int q, int lane) {
+    if constexpr (ES == 2) {
+      // 16 lanes read a 4 x 16 block, lane i its 8 bytes of summed row i / 4, and get column i
+      const int k = 32 * q + 8 * (lane >> 4) + (lane >> 2 & 3), col = r + 4 * (lane & 3);
+      typedef short i16x8 __attribute__((ext_vector_type(8)));
+      const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) i16x4*)(st + at(k) + col * 2));
+      const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) i16x4*)(st + at(k + 4) + col * 2));
+      const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      return __builtin_bit_cast(i32x4, v);
+    } else {
+      const int k = 16 * q + 4 * (lane >> 4), col = r + (lane & 15);
+      i32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const int*>(st + at(k + i) + col * 4);
+      return v;
+    }
+  }
+};
+
+enum Mode { STATS, GRAD, DX, DW };
+
+template <typename Ty, int BM, int BN, Mode M>
+struct Tile {
+  using A = Operand<Ty, BM, M == DW>;
+  using B = Operand<Ty, BN, M == DX || M == DW>;
+  static constexpr int STAGE = A::BYTES + B::BYTES;
+  static_assert(STAGE % 16 == 0 && A::BYTES % 16 == 0, "16-byte pieces");
+};
+
+template <bool F32>
+__device__ __forceinline__ void put(const void* base, long long at, const float (&v)[4], int cols) {
+  if constexpr (F32) {
+    float* const p = static_cast<float*>(const_cast<void*>(base)) + at;
+    if (cols >= 4) {
+      *reinterpret_cast<Pack<float, 4>*>(p) = Pack<float, 4>{{v[0], v[1], v[2], v[3]}};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < cols) p[i] = v[i];
+    }
+  } else {
+    uint16_t* const p = static_cast<uint16_t*>(const_cast<void*>(base)) + at;
+    Pack<uint16_t, 4> o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.v[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[i]));
+    if (cols >= 4) {
+      *reinterpret_cast<Pack<uint16_t, 4>*>(p) = o;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < cols) p[i] = o.v[i];
+    }
+  }
+}
+
+template <typename Ty, int BM, int BN, Mode MODE>
+__global__ __launch_bounds__(kThr) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void vocab_tile_kernel(VocabArgs a) {
+  using Cfg = Tile<Ty, BM, BN, MODE>;
+  using OA = typename Cfg::A;
+  using OB = typename Cfg::B;
+  constexpr bool F32 = Ty::kSize == 4;
+  constexpr int KE = kKB / Ty::kSize;          // elements of the summed axis a stage
+  constexpr int TM = BM / 32, TN = BN / 32;    // 16 x 16 tiles of a wave
+  extern __shared__ __align__(16) char lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
+  const int rows = MODE == DW ? a.vp : (int)a.T, cols = MODE == STATS || MODE == GRAD ? a.vp : a.n;
+  int m0, n0;
+  if (!tile_origin(rows, cols, BM, BN, m0, n0)) return;
+  int k0 = 0, kend = MODE == DX ? a.vp : MODE == DW ? (int)a.T : a.n;
+  if (MODE == DX && a.splits > 1) {
+    const int per = ((kend + a.splits - 1) / a.splits + KE - 1) / KE * KE;
+    k0 = min(kend, (int)blockIdx.y * per);
+    kend = min(kend, k0 + per);
+  }
+  const char* const w = static_cast<const char*>(a.W) + (long long)a.v0 * a.ldw * Ty::kSize;
+  OA oa;
+  OB ob;
+  if constexpr (MODE == STATS || MODE == GRAD) {
+    oa.init(a.X, a.ldx, m0, rows, 0);
+    ob.init(w, a.ldw, n0, cols, 0);
+  } else if constexpr (MODE == DX) {
+    oa.init(a.dS, a.ldp, m0, rows, 0);
+    ob.init(w, a.ldw, n0, cols, 0);
+  } else {
+    oa.init(a.dS, a.ldp, m0, rows, 0);
+    ob.init(a.Xm, a.ldm, n0, cols, 0);
+  }
+  i32x4 ar[2][OA::L], br[2][OB::L];   // two stages under way
+  auto fetch = [&](int k, int set) __attribute__((always_inline)) {
+    oa.fetch(ar[set], k, kend);
+    ob.fetch(br[set], k, kend);
+  };
+  auto keep = [&](int buf, int set) __attribute__((always_inline)) {
+    OA::keep(lds + buf * Cfg::STAGE, ar[set]);
+    OB::keep(lds + buf * Cfg::STAGE + OA::BYTES, br[set]);
+  };
+  typename Ty::Acc acc[TM][TN] = {};
+  i32x4 af[2][TM], bf[2][TN];
+  auto read = [&](int buf, int q) __attribute__((always_inline)) {
+    const char* const st = lds + buf * Cfg::STAGE;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) af[q][i] = OA::frag(st, wm + i * 16, q, lane);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) bf[q][j] = OB::frag(st + OA::BYTES, wn + j * 16, q, lane);
+  };
+  auto multiply = [&](int q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) Ty::mma(bf[q][j], af[q][i], acc[i][j]);
+  };
+  const int stages = (kend - k0 + KE - 1) / KE;
+  if (stages > 0) {
+    fetch(k0, 0);
+    keep(0, 0);
+    if (stages > 1) fetch(k0 + KE, 1);
+    if (stages > 2) fetch(k0 + 2 * KE, 0);
+    lds_sync();
+    read(0, 0);
+    auto stage = [&](int s, int buf) __attribute__((always_inline)) {
+      // nobody reads the other buffer since the barrier of the stage before
+      if (s + 1 < stages) keep(buf ^ 1, buf ^ 1);
+      if (s + 3 < stages) fetch(k0 + (s + 3) * KE, buf ^ 1);
+      read(buf, 1);
+      multiply(0);
+      lds_sync();
+      if (s + 1 < stages) read(buf ^ 1, 0);
+      multiply(1);
+    };
+    for (int s = 0; s < stages; s += 2) {
+      stage(s, 0);
+      if (s + 1 < stages) stage(s + 1, 1);
+    }
+  }
+
+  // lane l holds row l & 15 of each tile and 4 of its columns, from 4 (l >> 4) on
+  const int r0 = m0 + wm + (lane & 15), c0 = n0 + wn + 4 * (lane >> 4);
+  if constexpr (MODE == STATS) {
+    const int groups = (a.V + BN / 2 - 1) / (BN / 2), group = (n0 + wn) / (BN / 2);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int t = r0 + i * 16;
+      float m = -__builtin_inff(), s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (c0 + j * 16 + v < a.V) m = fmaxf(m, acc[i][j][v]);
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      // all -inf: each term is exp(-inf), not exp(-inf + inf); a NaN stays one
+      const float base = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (c0 + j * 16 + v < a.V) s += exp_of<F32>(acc[i][j][v] - base);
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (t >= rows || group >= groups) continue;
+      if (lane < 16) a.part[(long long)t * groups + group] = float2{m, s};
+      const long long target = a.target[t];
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (c0 + j * 16 + v == target && target < a.V) a.zt[t] = acc[i][j][v];
+    }
+  } else if constexpr (MODE == GRAD) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int t = r0 + i * 16;
+      if (t >= rows) continue;
+      const Row r = row_of(a, t);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int c = c0 + j * 16;
+        if (c >= cols) continue;
+        float d[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) d[v] = grad_of<F32>(r, acc[i][j][v], (long long)a.v0 + c + v);
+        put<F32>(a.dS, t * a.ldp + c, d, cols - c);
+      }
+    }
+  } else {
+    const float scale = a.g_each ? 1.0f : *a.g;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int t = r0 + i * 16;
+      if (t >= rows) continue;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int c = c0 + j * 16;
+        if (c >= cols) continue;
+        float o[4];
+        if (MODE == DX && a.acc) {
+          float4* const to = reinterpret_cast<float4*>(a.acc + ((long long)blockIdx.y * a.T + t) * a.lda + c);
+          float4 v = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+          if (a.v0 > 0) {
+            const float4 b = *to;
+            v = float4{v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w};
+          }
+          *to = v;
+          continue;
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[v] = acc[i][j][v] * scale;
+        if constexpr (MODE == DX) put<F32>(a.GX, t * a.ldgx + c, o, cols - c);
+        else put<F32>(a.GW, (long long)(a.v0 + t) * a.ldgw + c, o, cols - c);
+      }
+    }
+  }
+}
+
+// A row's lse and loss from the parts of its columns, by G lanes a row
+template <int G>
+__global__ __launch_bounds__(kThr) void vocab_join_kernel(VocabArgs a, int groups) {
+  __shared__ float2 red[kThr / 64];
+  const long long t = (long long)blockIdx.x * (kThr / G) + threadIdx.x / G;
+  if (t >= a.T) return;   // whole workgroups where G = kThr
+  const int lane = threadIdx.x % G;
+  const float2* const p = a.part + t * groups;
+  float m = -__builtin_inff();
+  for (int i = lane; i < groups; i += G) m = fmaxf(m, p[i].x);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if constexpr (G > 64) {
+    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64].x = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThr / 64; ++i) m = fmaxf(m, red[i].x);
+    __syncthreads();
+  }
+  // sums of up to 2^24 terms, in 64 bits
+  double s = 0.0;
+  const float base = m == -__builtin_inff() ? 0.0f : m;
+  for (int i = lane; i < groups; i += G) s += (double)p[i].y * (double)expf(p[i].x - base);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+  if constexpr (G > 64) {
+    double* const sums = reinterpret_cast<double*>(red);
+    if (threadIdx.x % 64 == 0) sums[threadIdx.x / 64] = s;
+    __syncthreads();
+    s = sums[0];
+#pragma unroll
+    for (int i = 1; i < kThr / 64; ++i) s += sums[i];
+  }
+  if (lane != 0) return;
+  const double lse = (double)base + log(s);
+  const long long target = a.target[t];
+  const bool ignored = target == a.ignore, bad = target < 0 || target >= a.V;
+  a.lse_out[t] = (float)lse;
+  a.loss[t] = ignored ? 0.0f : bad ? __builtin_nanf("") : (float)(lse - (double)a.zt[t]);
+}
+
+// Xm = X with zeros in ignored rows (a padded token's activations may be anything, and
+// 0 times infinity would reach dW), columns up to ldm and rows up to a.Tm zero too
+template <typename E>
+__global__ __launch_bounds__(kThr) void vocab_mask_kernel(VocabArgs a) {
+  constexpr int N = 16 / sizeof(E);
+  const int nv = (int)(a.ldm / N);
+  for (long long t = blockIdx.x; t < a.Tm; t += gridDim.x) {
+    const bool none = t >= a.T || a.target[t] == a.ignore;
+    const char* const from = static_cast<const char*>(a.X) + t * a.ldx * (long long)sizeof(E);
+    E* const to = static_cast<E*>(a.Xm) + t * a.ldm;
+    for (int c = threadIdx.x; c < nv; c += kThr) {
+      i32x4 v = {0, 0, 0, 0};
+      if (!none) v = load16<sizeof(E)>(from, (long long)c * 16, (long long)a.n * sizeof(E));
+      reinterpret_cast<i32x4*>(to)[c] = v;
+    }
+  }
+}
+
+// dX = round(factor * the sum of the splits' parts)
+template <bool F32>
+__global__ __launch_bounds__(kThr) void vocab_finish_kernel(VocabArgs a) {
+  const int quads = (a.n + 3) / 4;
+  const float scale = a.g_each ? 1.0f : *a.g;
+  const long long count = a.T * quads;
+  for (long long i = (long long)blockIdx.x * kThr + threadIdx.x; i < count; i += (long long)gridDim.x * kThr) {
+    const long long t = i / quads;
+    const int c = (int)(i - t * quads) * 4;
+    float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int z = 0; z < a.splits; ++z) {
+      const float4 b = *reinterpret_cast<const float4*>(a.acc + (z * a.T + t) * a.lda + c);
+      v = float4{v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w};
+    }
+    const float o[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+    put<F32>(a.GX, t * a.ldgx + c, o, a.n - c);
+  }
+}
+
+// V rows of n elements of zeros (4 or 2 bytes each)
+template <typename E>
+__global__ __launch_bounds__(kThr) void vocab_zero_kernel(E* p, int V, int n, long long ld) {
+  for (long long v = blockIdx.x; v < V; v += gridDim.x)
+    for (int c = threadIdx.x; c < n; c += kThr) p[v * ld + c] = E(0);
+}
+
+template <typename Ty, int BM, int BN, Mode M>
+hipError_t tiles(const VocabArgs& a, hipStream_t s) {
+  const long long rows = M == DW ? a.vp : a.T;
+  const int cols = M == STATS || M == GRAD ? a.vp : a.n;
+  hipLaunchKernelGGL((vocab_tile_kernel<Ty, BM, BN, M>),
+                     dim3((unsigned)tile_grid(rows, cols, BM, BN), M == DX ? (unsigned)a.splits : 1u), dim3(kThr),
+                     (2 * Tile<Ty, BM, BN, M>::STAGE), s, a);
+  return hipGetLastError();
+}
+template <typename Ty, Mode M>
+hipError_t tiles(const VocabArgs& a, int tile, hipStream_t s) {
+  switch (tile) {
+    case VOCAB_TILE_128: return tiles<Ty, 128, 128, M>(a, s);
+    case VOCAB_TILE_64: return tiles<Ty, 64, 64, M>(a, s);
+    case VOCAB_TILE_32x64: return tiles<Ty, 32, 64, M>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+template <Mode M>
+hipError_t tiles(const VocabArgs& a, int bf16, int tile, hipStream_t s) {
+  return bf16 ? tiles<TypeBf16, M>(a, tile, s) : tiles<TypeF32, M>(a, tile, s);
+}
+
+// The largest tile that leaves few CUs idle
+int tile_of(long long rows, long long cols) {
+  const auto count = [&](int bm, int bn) { return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn); };
+  if (rows > 64 && count(128, 128) >= 200) return VOCAB_TILE_128;
+  if (rows > 32) return VOCAB_TILE_64;
+  return VOCAB_TILE_32x64;
+}
+int group_cols(int tile) { return tile == VOCAB_TILE_128 ? 64 : 32; }
+
+constexpr long long kRoom = 256LL << 20;   // bytes that a part of the work may take as workspace
+size_t padded(size_t b) { return (b + 255) / 256 * 256; }
+
+}  // namespace
+
+hipError_t launch_vocab_zero(void* p, int V, int n, long long ld, int es, hipStream_t s) {
+  const dim3 grid((unsigned)std::min(V, 1 << 16));
+  if (es == 4) hipLaunchKernelGGL((vocab_zero_kernel<uint32_t>), grid, dim3(kThr), 0, s, static_cast<uint32_t*>(p), V, n, ld);
+  else hipLaunchKernelGGL((vocab_zero_kernel<uint16_t>), grid, dim3(kThr), 0, s, static_cast<uint16_t*>(p), V, n, ld);
+  return hipGetLastError();
+}
+
+VocabPlan vocab_forward_plan(long long T, int V, int) {
+  VocabPlan p{};
+  p.tile = tile_of(T, V);
+  p.groups = (V + group_cols(p.tile) - 1) / group_cols(p.tile);
+  // tokens of a launch: as many as their parts leave room for, and their tiles can be counted
+  const long long most = std::min(kRoom / (8LL * p.groups), (1LL << 34) / V);
+  p.rows = std::min(T, std::max(256LL, most / 256 * 256));
+  p.bytes = padded((size_t)p.rows * p.groups * 8) + padded((size_t)p.rows * 4);
+  return p;
+}
+
+hipError_t launch_vocab_forward(const VocabArgs& in, int bf16, void* ws, hipStream_t s) {
+  const VocabPlan p = vocab_forward_plan(in.T, in.V, in.n);
+  const int es = bf16 ? 2 : 4;
+  for (long long t = 0; t < in.T; t += p.rows) {
+    VocabArgs a = in;
+    a.T = std::min(p.rows, in.T - t);
+    a.X = static_cast<const char*>(in.X) + t * in.ldx * es;
+    a.target = in.target + t;
+    a.loss = in.loss + t;
+    a.lse_out = in.lse_out + t;
+    a.part = static_cast<float2*>(ws);
+    a.zt = reinterpret_cast<float*>(static_cast<char*>(ws) + padded((size_t)p.rows * p.groups * 8));
+    a.v0 = 0;
+    a.vp = a.V;
+    int groups = p.groups;
+    hipError_t e;
+    e = tiles<STATS>(a, bf16, p.tile, s);
+    if (e != hipSuccess) return e;
+    if (a.T >= 1024)
+      hipLaunchKernelGGL((vocab_join_kernel<64>), dim3((unsigned)((a.T + 3) / 4)), dim3(kThr), 0, s, a, groups);
+    else
+      hipLaunchKernelGGL((vocab_join_kernel<kThr>), dim3((unsigned)a.T), dim3(kThr), 0, s, a, groups);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, bool gw) {
+  VocabBackPlan p{};
+  const int es = bf16 ? 2 : 4;
+  p.Tm = (T + 63) / 64 * 64;
+  p.ldm = (n + 7) / 8 * 8;
+  p.lda = (n + 3) / 4 * 4;
+  // columns of a piece: those whose d leaves room, in whole tiles, the pieces alike
+  const long long most = std::max(256LL, std::min(kRoom / (p.Tm * es), (1LL << 36) / n) / 256 * 256);
+  const long long pieces = (V + most - 1) / most;
+  p.vp = (int)std::min<long long>(most, ((V + pieces - 1) / pieces + 255) / 256 * 256);
+  p.pieces = (V + p.vp - 1) / p.vp;
+  p.grad_tile = tile_of(T, std::min(p.vp, V));
+  p.dw_tile = tile_of(std::min(p.vp, V), n);
+  p.dx_tile = tile_of(T, n);
+  // few tiles of dX share the vocabulary's piece
+  const int bm = p.dx_tile == VOCAB_TILE_128 ? 128 : p.dx_tile == VOCAB_TILE_64 ? 64 : 32, bn = bm == 128 ? 128 : 64;
+  const long long tiles = ((T + bm - 1) / bm) * ((n + bn - 1) / bn);
+  p.splits = (int)std::max(1LL, std::min({64LL, 512 / tiles, (long long)std::min(p.vp, V) / 256}));
+  p.acc = gx && (p.splits > 1 || p.pieces > 1);
+  p.at_x = padded((size_t)p.Tm * p.vp * es);
+  p.at_acc = p.at_x + (gw ? padded((size_t)p.Tm * p.ldm * es) : 0);
+  p.bytes = p.at_acc + (p.acc ? padded((size_t)p.splits * T * p.lda * 4) : 0);
+  return p;
+}
+
+hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStream_t s) {
+  const VocabBackPlan p = vocab_backward_plan(in.T, in.V, in.n, bf16, in.GX != nullptr, in.GW != nullptr);
+  VocabArgs a = in;
+  a.dS = ws;
+  a.ldp = p.vp;
+  a.Xm = static_cast<char*>(ws) + p.at_x;
+  a.ldm = p.ldm;
+  a.Tm = p.Tm;
+  a.acc = p.acc ? reinterpret_cast<float*>(static_cast<char*>(ws) + p.at_acc) : nullptr;
+  a.lda = p.lda;
+  a.splits = p.splits;
+  hipError_t e;
+  if (a.GW) {
+    const dim3 grid((unsigned)std::min<long long>(a.Tm, 1 << 16));
+    if (bf16) hipLaunchKernelGGL((vocab_mask_kernel<uint16_t>), grid, dim3(kThr), 0, s, a);
+    else hipLaunchKernelGGL((vocab_mask_kernel<float>), grid, dim3(kThr), 0, s, a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  for (long long v = 0; v < a.V; v += p.vp) {
+    a.v0 = (int)v;
+    a.vp = (int)std::min<long long>(p.vp, a.V - v);
+    e = tiles<GRAD>(a, bf16, p.grad_tile, s);
+    if (e != hipSuccess) return e;
+    if (a.GX) {
+      e = tiles<DX>(a, bf16, p.dx_tile, s);
+      if (e != hipSuccess) return e;
+    }
+    if (a.GW) {
+      e = tiles<DW>(a, bf16, p.dw_tile, s);
+      if (e != hipSuccess) return e;
+    }
+  }
+  if (!a.acc) return hipSuccess;
+  const long long quads = a.T * ((a.n + 3) / 4);
+  const dim3 grid((unsigned)std::min<long long>((quads + kThr - 1) / kThr, 1 << 16));
+  if (bf16) hipLaunchKernelGGL((vocab_finish_kernel<false>), grid, dim3(kThr), 0, s, a);
+  else hipLaunchKernelGGL((vocab_finish_kernel<true>), grid, dim3(kThr), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace poetx

@@ -356,4 +356,46 @@ enum LinearTile {
 };
 hipError_t launch_linear_ring(const LinearArgs& a, int type, int tile, hipStream_t s);
 
+// Cross entropy of X W^T without its logits (k_vocab_loss.hip); row strides in elements.
+struct VocabArgs {
+  const void* X; const void* W; const int64_t* target;
+  long long T; int V, n;
+  long long ldx, ldw;
+  long long ignore;                 // the target of tokens that do not count
+  // forward
+  float* loss; float* lse_out;
+  float2* part;                     // maximum and sum of exponentials, T x groups of columns
+  float* zt;                        // T logits of the targets
+  // backward
+  const float* lse; const float* g; // T of each, or one g (g_each 0) that the results are multiplied by
+  int g_each;
+  void* GX; void* GW;               // each may be null
+  long long ldgx, ldgw;
+  void* dS; long long ldp;          // Tm x ldp: dL/dz of a piece of the vocabulary
+  void* Xm; long long ldm, Tm;      // Tm x ldm: X with zeros for ignored tokens and behind the last row and column
+  float* acc; long long lda;        // splits x T x lda parts of dX, or null: GX is written at once
+  int splits;
+  int v0, vp;                       // the piece: its first row of W and how many
+};
+enum VocabTile { VOCAB_TILE_128, VOCAB_TILE_64, VOCAB_TILE_32x64 };
+struct VocabPlan {
+  int tile, groups;
+  long long rows;   // tokens of a launch
+  size_t bytes;
+};
+struct VocabBackPlan {
+  long long Tm, ldm, lda, pieces;
+  int vp, grad_tile, dx_tile, dw_tile, splits;
+  bool acc;
+  size_t at_x, at_acc, bytes;
+};
+constexpr int kVocabMax = 1 << 24;        // tokens of a call, rows of W
+constexpr int kVocabMaxDim = 1 << 16;
+// by the sizes alone
+VocabPlan vocab_forward_plan(long long T, int V, int n);
+VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, bool gw);
+hipError_t launch_vocab_forward(const VocabArgs& a, int bf16, void* ws, hipStream_t s);
+hipError_t launch_vocab_backward(const VocabArgs& a, int bf16, void* ws, hipStream_t s);
+hipError_t launch_vocab_zero(void* p, int V, int n, long long ld, int es, hipStream_t s);
+
 }  // namespace poetx

@@ -1,6 +1,6 @@
-// Host side of the calls that train around a block's linears (dropout, layer norm):
-// argument checks and launches. The arithmetic runs in the kernels declared in
-// poetx_internal.h.
+// Host side of the calls that train around a block's linears (dropout, layer norm,
+// the vocabulary's cross entropy): argument checks and launches. The arithmetic
+// runs in the kernels declared in poetx_internal.h.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -24,6 +24,16 @@ bool drop_rule(const poetx_dropout_rule& r, poetx::DropArgs& d) {
   d.scale = threshold < 65536 ? (float)(65536.0 / (double)(65536 - threshold)) : 0.0f;
   return true;
 }
+
+poetx_status vocab_desc(const poetx_cross_entropy_desc* d) {
+  if (!d || d->T < 0) return POETX_ERR_INVALID_ARG;
+  if (d->V < 1 || d->V > poetx::kVocabMax || d->n < 1 || d->n > poetx::kVocabMaxDim || d->T > poetx::kVocabMax)
+    return POETX_ERR_SHAPE;
+  if (!real_type(d->dtype)) return POETX_ERR_DTYPE;
+  return POETX_OK;
+}
+Mat bytes_at(const void* p, size_t n) { return Mat{p, 1, (int64_t)n, (int64_t)n, 1}; }
+
 Mat seed_of(const poetx_dropout_rule& r) { return Mat{r.seed_dev, 1, 8, 8, 1}; }
 
 }  // namespace
@@ -127,6 +137,100 @@ poetx_status poetx_layer_norm_backward(const poetx_layer_norm_backward_desc* d, 
                              part + (size_t)poetx::layer_norm_backward_parts(d->T) * d->dim * 2, d->T, d->dim,
                              g.ld, gh.ld, h.ld, gx.ld, gr.ld, rule};
   return launched(poetx::launch_layer_norm_backward(a, d->dtype == POETX_BF16, s));
+}
+
+size_t poetx_linear_cross_entropy_workspace(const poetx_cross_entropy_desc* d) {
+  if (vocab_desc(d) != POETX_OK || d->T == 0) return 0;
+  return poetx::vocab_forward_plan(d->T, d->V, d->n).bytes;
+}
+
+poetx_status poetx_linear_cross_entropy(const poetx_cross_entropy_desc* d, const void* X, const void* W,
+                                        const int64_t* target, float* loss, float* lse, void* ws, size_t ws_bytes,
+                                        void* stream) {
+  const poetx_status ok = vocab_desc(d);
+  if (ok != POETX_OK || d->T == 0) return ok;
+  if (!X || !W || !target || !loss || !lse) return POETX_ERR_INVALID_ARG;
+  const int es = size_of(d->dtype);
+  Mat x{X, d->T, d->n, d->ld_x, es}, w{W, d->V, d->n, d->ld_w, es};
+  if (!strides_ok(x) || !strides_ok(w)) return POETX_ERR_SHAPE;
+  if (!aligned(X, es) || !aligned(W, es) || !aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4) ||
+      !aligned(ws, 16))
+    return POETX_ERR_ALIGNMENT;
+  const size_t need = poetx_linear_cross_entropy_workspace(d);
+  if (!ws || ws_bytes < need) return POETX_ERR_WORKSPACE;
+  const Mat in[] = {x, w, bytes_at(target, (size_t)d->T * 8)};
+  const Mat out[] = {vec(loss, d->T), vec(lse, d->T), bytes_at(ws, need)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Mat& m : in)
+      if (overlap(out[i], m)) return POETX_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return POETX_ERR_INVALID_ARG;
+  }
+  poetx::VocabArgs a{};
+  a.X = X;
+  a.W = W;
+  a.target = target;
+  a.T = d->T;
+  a.V = d->V;
+  a.n = d->n;
+  a.ldx = x.ld;
+  a.ldw = w.ld;
+  a.ignore = d->ignore_index;
+  a.loss = loss;
+  a.lse_out = lse;
+  return launched(poetx::launch_vocab_forward(a, d->dtype == POETX_BF16, ws, (hipStream_t)stream));
+}
+
+size_t poetx_linear_cross_entropy_backward_workspace(const poetx_cross_entropy_desc* d, int32_t need_x, int32_t need_w) {
+  if (vocab_desc(d) != POETX_OK || d->T == 0) return 0;
+  return poetx::vocab_backward_plan(d->T, d->V, d->n, d->dtype == POETX_BF16, need_x != 0, need_w != 0).bytes;
+}
+
+poetx_status poetx_linear_cross_entropy_backward(const poetx_cross_entropy_desc* d, const float* g, const void* X,
+                                                 const void* W, const int64_t* target, const float* lse, void* G_X,
+                                                 void* G_W, void* ws, size_t ws_bytes, void* stream) {
+  const poetx_status ok = vocab_desc(d);
+  if (ok != POETX_OK) return ok;
+  if (!G_X && !G_W) return POETX_ERR_INVALID_ARG;
+  if (d->g_count != 1 && d->g_count != d->T) return POETX_ERR_SHAPE;
+  const int es = size_of(d->dtype);
+  Mat x{X, d->T, d->n, d->ld_x, es}, w{W, d->V, d->n, d->ld_w, es}, gx{G_X, d->T, d->n, d->ld_gx, es},
+      gw{G_W, d->V, d->n, d->ld_gw, es};
+  if (!strides_ok(x) || !strides_ok(w) || !strides_ok(gx) || !strides_ok(gw)) return POETX_ERR_SHAPE;
+  if (!aligned(X, es) || !aligned(W, es) || !aligned(G_X, es) || !aligned(G_W, es) || !aligned(target, 8) ||
+      !aligned(g, 4) || !aligned(lse, 4) || !aligned(ws, 16))
+    return POETX_ERR_ALIGNMENT;
+  const hipStream_t s = (hipStream_t)stream;
+  if (d->T == 0) return G_W ? launched(poetx::launch_vocab_zero(G_W, d->V, d->n, gw.ld, es, s)) : POETX_OK;
+  if (!g || !X || !W || !target || !lse) return POETX_ERR_INVALID_ARG;
+  const size_t need = poetx_linear_cross_entropy_backward_workspace(d, G_X != nullptr, G_W != nullptr);
+  if (!ws || ws_bytes < need) return POETX_ERR_WORKSPACE;
+  const Mat in[] = {x, w, bytes_at(target, (size_t)d->T * 8), vec(lse, d->T), vec(g, d->g_count)};
+  const Mat out[] = {gx, gw, bytes_at(ws, need)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Mat& m : in)
+      if (overlap(out[i], m)) return POETX_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return POETX_ERR_INVALID_ARG;
+  }
+  poetx::VocabArgs a{};
+  a.X = X;
+  a.W = W;
+  a.target = target;
+  a.T = d->T;
+  a.V = d->V;
+  a.n = d->n;
+  a.ldx = x.ld;
+  a.ldw = w.ld;
+  a.ignore = d->ignore_index;
+  a.lse = lse;
+  a.g = g;
+  a.g_each = d->g_count != 1;
+  a.GX = G_X;
+  a.GW = G_W;
+  a.ldgx = gx.ld;
+  a.ldgw = gw.ld;
+  return launched(poetx::launch_vocab_backward(a, d->dtype == POETX_BF16, ws, s));
 }
 
 }  // extern "C"

@@ -63,6 +63,8 @@ EXPORTED = (
     "poetx_forward_noalloc", "poetx_forward_noalloc_max_bytes",
     "poetx_add_rms_norm", "poetx_rms_norm_backward", "poetx_rms_norm_backward_workspace",
     "poetx_dropout", "poetx_add_layer_norm", "poetx_layer_norm_backward", "poetx_layer_norm_backward_workspace",
+    "poetx_linear_cross_entropy", "poetx_linear_cross_entropy_workspace",
+    "poetx_linear_cross_entropy_backward", "poetx_linear_cross_entropy_backward_workspace",
     "poetx_linear", "poetx_linear_workspace", "poetx_clip_grads", "poetx_clip_grads_workspace",
 )
 
@@ -137,6 +139,14 @@ class LayerNormBackwardDesc(ctypes.Structure):
     ]
 
 
+class CrossEntropyDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64), ("V", ctypes.c_int32), ("n", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64), ("ld_gx", ctypes.c_int64),
+        ("ld_gw", ctypes.c_int64), ("g_count", ctypes.c_int64), ("ignore_index", ctypes.c_int64),
+    ]
+
+
 class LinearDesc(ctypes.Structure):
     _fields_ = [
         ("T", ctypes.c_int64), ("m", ctypes.c_int32), ("n", ctypes.c_int32),
@@ -191,6 +201,10 @@ def _load() -> ctypes.CDLL:
         "poetx_add_layer_norm": (st, [ctypes.POINTER(LayerNormDesc)] + [vp] * 10),
         "poetx_layer_norm_backward": (st, [ctypes.POINTER(LayerNormBackwardDesc)] + [vp] * 11 + [sz, vp]),
         "poetx_layer_norm_backward_workspace": (sz, [i64, i32]),
+        "poetx_linear_cross_entropy": (st, [ctypes.POINTER(CrossEntropyDesc)] + [vp] * 6 + [sz, vp]),
+        "poetx_linear_cross_entropy_workspace": (sz, [ctypes.POINTER(CrossEntropyDesc)]),
+        "poetx_linear_cross_entropy_backward": (st, [ctypes.POINTER(CrossEntropyDesc)] + [vp] * 8 + [sz, vp]),
+        "poetx_linear_cross_entropy_backward_workspace": (sz, [ctypes.POINTER(CrossEntropyDesc), i32, i32]),
         "poetx_linear": (st, [ctypes.POINTER(LinearDesc)] + [vp] * 9 + [sz, vp]),
         "poetx_linear_workspace": (sz, [ctypes.POINTER(LinearDesc)]),
         "poetx_clip_grads": (st, [i32, vp, vp, vp, vp, ctypes.c_double, vp, vp, sz, vp]),

@@ -100,3 +100,57 @@ def test_python_refusals():
                  lambda: oec.add_layer_norm_backward(x, x, w, r, r), lambda: oec.add_layer_norm(x[0], w)):
         with pytest.raises(ValueError):
             call()
+
+
+def loss(T=4, V=32, n=64, dtype=px.POETX_BF16, ld=(64, 64), X=A, W=B, target=C, out=D, lse=E, ws=F, wsb=None, null=False):
+    d = px.CrossEntropyDesc(T, V, n, dtype, *ld, 64, 64, 1, -100)
+    wsb = L.poetx_linear_cross_entropy_workspace(d) if wsb is None else wsb
+    return L.poetx_linear_cross_entropy(None if null else d, X, W, target, out, lse, ws, wsb, None)
+
+
+SIZES = [
+    (dict(null=True), INV), (dict(T=-1), INV), (dict(T=2 ** 24 + 1), SHAPE), (dict(V=0), SHAPE), (dict(V=2 ** 24 + 1), SHAPE),
+    (dict(n=0), SHAPE), (dict(n=2 ** 16 + 1), SHAPE), (dict(dtype=px.POETX_INT8), DTYPE),
+    (dict(X=None), INV), (dict(W=None), INV), (dict(target=None), INV), (dict(lse=None), INV),
+    (dict(X=A + 1), ALIGN), (dict(W=B + 1), ALIGN), (dict(target=C + 4), ALIGN), (dict(lse=E + 2), ALIGN),
+]
+
+
+@pytest.mark.parametrize("kw, status", SIZES + [
+    (dict(T=0), px.POETX_OK), (dict(T=0, X=None, ws=None), px.POETX_OK),
+    (dict(ld=(63, 64)), SHAPE), (dict(ld=(64, 63)), SHAPE), (dict(ld=(MAX64, 64)), SHAPE),
+    (dict(out=None), INV), (dict(out=D + 1), ALIGN), (dict(ws=F + 8), ALIGN), (dict(ws=None), WS), (dict(wsb=0), WS),
+    (dict(out=A), INV), (dict(out=C), INV), (dict(lse=D), INV), (dict(ws=B), INV), (dict(ws=D), INV), (dict(lse=B + 64), INV),
+])
+def test_cross_entropy_refusals(kw, status):
+    assert loss(**kw) == status
+
+
+def loss_back(T=4, V=32, n=64, dtype=px.POETX_BF16, ld=(64, 64, 64, 64), count=1, g=D, X=A, W=B, target=C, lse=E, gx=F, gw=G,
+              ws=H, wsb=None, null=False):
+    d = px.CrossEntropyDesc(T, V, n, dtype, *ld, count, -100)
+    wsb = L.poetx_linear_cross_entropy_backward_workspace(d, gx is not None, gw is not None) if wsb is None else wsb
+    return L.poetx_linear_cross_entropy_backward(None if null else d, g, X, W, target, lse, gx, gw, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw, status", SIZES + [
+    (dict(T=0, gw=None), px.POETX_OK), (dict(gx=None, gw=None), INV), (dict(count=2), SHAPE), (dict(count=0), SHAPE),
+    (dict(ld=(63, 64, 64, 64)), SHAPE), (dict(ld=(64, 63, 64, 64)), SHAPE), (dict(ld=(64, 64, 63, 64)), SHAPE),
+    (dict(ld=(64, 64, 64, 63)), SHAPE), (dict(g=None), INV), (dict(g=D + 2), ALIGN), (dict(gx=F + 1), ALIGN),
+    (dict(gw=G + 1), ALIGN), (dict(ws=H + 8), ALIGN), (dict(ws=None), WS), (dict(wsb=0), WS),
+    (dict(gx=A), INV), (dict(gw=B), INV), (dict(gx=G), INV), (dict(gw=C), INV), (dict(gx=E), INV), (dict(gw=D), INV),
+    (dict(ws=A), INV), (dict(ws=F), INV), (dict(gx=A + 2), INV),
+])
+def test_cross_entropy_backward_refusals(kw, status):
+    assert loss_back(**kw) == status
+
+
+def test_cross_entropy_workspaces():
+    f, b = L.poetx_linear_cross_entropy_workspace, L.poetx_linear_cross_entropy_backward_workspace
+    d = lambda T, V, n, dt=px.POETX_BF16: px.CrossEntropyDesc(T, V, n, dt, n, n, n, n, 1, -100)  # noqa: E731
+    assert f(None) == 0 and f(d(0, 9, 9)) == 0 and f(d(9, 0, 9)) == 0 and b(None, 1, 1) == 0 and b(d(9, 9, 0), 1, 1) == 0
+    assert f(d(1, 32000, 2048)) >= 8 * 32000 // 256
+    # far below the logits of a batch, whichever gradients are wanted
+    assert f(d(16384, 32000, 2048)) < 2 * 16384 * 32000 / 8
+    big = b(d(16384, 32000, 2048), 1, 1)
+    assert b(d(16384, 32000, 2048), 0, 1) <= big and b(d(16384, 32000, 2048), 1, 0) <= big < 2 * 16384 * 32000 * 0.6

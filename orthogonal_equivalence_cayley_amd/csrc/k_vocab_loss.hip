@@ -19,6 +19,7 @@
 // every eight of them (bf16) by 128 more, so that the rows a read takes together fall in
 // distinct banks.
 #include <algorithm>
+#include <cmath>
 
 #include "linear_common.h"
 #include "vocab_loss.h"
@@ -284,7 +285,7 @@ void vocab_tile_kernel(VocabArgs a) {
     for (int i = 0; i < TM; ++i) {
       const int t = r0 + i * 16;
       if (t >= rows) continue;
-      const Row r = row_of(a, t);
+      const Row r = token_of(a, t);
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         const int c = c0 + j * 16;
@@ -367,7 +368,8 @@ __global__ __launch_bounds__(kThr) void vocab_join_kernel(VocabArgs a, int group
 }
 
 // Xm = X with zeros in ignored rows (a padded token's activations may be anything, and
-// 0 times infinity would reach dW), columns up to ldm and rows up to a.Tm zero too
+// 0 times infinity would reach dW), columns up to ldm and rows up to a.Tm zero too; d's rows
+// behind the last token as well
 template <typename E>
 __global__ __launch_bounds__(kThr) void vocab_mask_kernel(VocabArgs a) {
   constexpr int N = 16 / sizeof(E);
@@ -380,6 +382,10 @@ __global__ __launch_bounds__(kThr) void vocab_mask_kernel(VocabArgs a) {
       i32x4 v = {0, 0, 0, 0};
       if (!none) v = load16<sizeof(E)>(from, (long long)c * 16, (long long)a.n * sizeof(E));
       reinterpret_cast<i32x4*>(to)[c] = v;
+    }
+    if (t >= a.T) {
+      i32x4* const d = reinterpret_cast<i32x4*>(static_cast<E*>(a.dS) + t * a.ldp);
+      for (int c = threadIdx.x; c < (int)(a.ldp / N); c += kThr) d[c] = i32x4{0, 0, 0, 0};
     }
   }
 }
@@ -442,6 +448,15 @@ int tile_of(long long rows, long long cols) {
 }
 int group_cols(int tile) { return tile == VOCAB_TILE_128 ? 64 : 32; }
 
+// Whether 256 x 256 tiles (k_vocab_loss_pipe.hip) take less time than 128 x 128 ones: in
+// units of a CU's time for one of the latter, a round of 256 of the former takes 3.5, of
+// 512 of the latter, two to a CU, 2.5, and up to 256 of them 1.5
+bool pipe_pays(long long rows, long long cols) {
+  const auto count = [&](int b) { return ((rows + b - 1) / b) * ((cols + b - 1) / b); };
+  const double pipe = 3.5 * (double)((count(256) + 255) / 256), n = (double)count(128);
+  return pipe <= (n <= 256 ? 1.5 : 2.5 * std::ceil(n / 512));
+}
+
 constexpr long long kRoom = 256LL << 20;   // bytes that a part of the work may take as workspace
 size_t padded(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -457,7 +472,8 @@ hipError_t launch_vocab_zero(void* p, int V, int n, long long ld, int es, hipStr
 VocabPlan vocab_forward_plan(long long T, int V, int) {
   VocabPlan p{};
   p.tile = tile_of(T, V);
-  p.groups = (V + group_cols(p.tile) - 1) / group_cols(p.tile);
+  // 256-column tiles leave parts of 64, whole tiles of them
+  p.groups = std::max((V + group_cols(p.tile) - 1) / group_cols(p.tile), (V + 255) / 256 * 4);
   // tokens of a launch: as many as their parts leave room for, and their tiles can be counted
   const long long most = std::min(kRoom / (8LL * p.groups), (1LL << 34) / V);
   p.rows = std::min(T, std::max(256LL, most / 256 * 256));
@@ -479,9 +495,14 @@ hipError_t launch_vocab_forward(const VocabArgs& in, int bf16, void* ws, hipStre
     a.zt = reinterpret_cast<float*>(static_cast<char*>(ws) + padded((size_t)p.rows * p.groups * 8));
     a.v0 = 0;
     a.vp = a.V;
-    int groups = p.groups;
+    int groups = (a.V + group_cols(p.tile) - 1) / group_cols(p.tile);
     hipError_t e;
-    e = tiles<STATS>(a, bf16, p.tile, s);
+    if (bf16 && vocab_pipe_logits(a) && pipe_pays(a.T, a.V)) {
+      groups = (a.V + 255) / 256 * 4;
+      e = launch_vocab_pipe_stats(a, s);
+    } else {
+      e = tiles<STATS>(a, bf16, p.tile, s);
+    }
     if (e != hipSuccess) return e;
     if (a.T >= 1024)
       hipLaunchKernelGGL((vocab_join_kernel<64>), dim3((unsigned)((a.T + 3) / 4)), dim3(kThr), 0, s, a, groups);
@@ -530,6 +551,7 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
   a.lda = p.lda;
   a.splits = p.splits;
   hipError_t e;
+  const bool pipe_dx = bf16 && a.GX && p.splits == 1 && vocab_pipe_dx(a) && pipe_pays(a.T, a.n);
   if (a.GW) {
     const dim3 grid((unsigned)std::min<long long>(a.Tm, 1 << 16));
     if (bf16) hipLaunchKernelGGL((vocab_mask_kernel<uint16_t>), grid, dim3(kThr), 0, s, a);
@@ -540,18 +562,24 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
   for (long long v = 0; v < a.V; v += p.vp) {
     a.v0 = (int)v;
     a.vp = (int)std::min<long long>(p.vp, a.V - v);
-    e = tiles<GRAD>(a, bf16, p.grad_tile, s);
+    e = bf16 && vocab_pipe_logits(a) && pipe_pays(a.T, a.vp) ? launch_vocab_pipe_grad(a, s)
+                                                            : tiles<GRAD>(a, bf16, p.grad_tile, s);
     if (e != hipSuccess) return e;
     if (a.GX) {
-      e = tiles<DX>(a, bf16, p.dx_tile, s);
+      if (pipe_dx && a.vp % 64) {
+        e = launch_vocab_pad(a, s);
+        if (e != hipSuccess) return e;
+      }
+      e = pipe_dx ? launch_vocab_pipe_dx(a, s) : tiles<DX>(a, bf16, p.dx_tile, s);
       if (e != hipSuccess) return e;
     }
     if (a.GW) {
-      e = tiles<DW>(a, bf16, p.dw_tile, s);
+      e = bf16 && vocab_pipe_dw(a) && pipe_pays(a.vp, a.n) ? launch_vocab_pipe_dw(a, s)
+                                                          : tiles<DW>(a, bf16, p.dw_tile, s);
       if (e != hipSuccess) return e;
     }
   }
-  if (!a.acc) return hipSuccess;
+  if (!a.acc || pipe_dx) return hipSuccess;   // the last piece of the pipelined dX writes it whole
   const long long quads = a.T * ((a.n + 3) / 4);
   const dim3 grid((unsigned)std::min<long long>((quads + kThr - 1) / kThr, 1 << 16));
   if (bf16) hipLaunchKernelGGL((vocab_finish_kernel<false>), grid, dim3(kThr), 0, s, a);

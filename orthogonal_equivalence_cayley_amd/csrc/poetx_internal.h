@@ -396,6 +396,16 @@ VocabPlan vocab_forward_plan(long long T, int V, int n);
 VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, bool gw);
 hipError_t launch_vocab_forward(const VocabArgs& a, int bf16, void* ws, hipStream_t s);
 hipError_t launch_vocab_backward(const VocabArgs& a, int bf16, void* ws, hipStream_t s);
+// 256 x 256 tiles with one load pipeline (k_vocab_loss_pipe.hip), bf16: whether the operands'
+// sizes and alignment allow them, and the launches
+bool vocab_pipe_logits(const VocabArgs& a);
+bool vocab_pipe_dx(const VocabArgs& a);
+bool vocab_pipe_dw(const VocabArgs& a);
+hipError_t launch_vocab_pipe_stats(const VocabArgs& a, hipStream_t s);
+hipError_t launch_vocab_pipe_grad(const VocabArgs& a, hipStream_t s);
+hipError_t launch_vocab_pipe_dx(const VocabArgs& a, hipStream_t s);
+hipError_t launch_vocab_pipe_dw(const VocabArgs& a, hipStream_t s);
+hipError_t launch_vocab_pad(const VocabArgs& a, hipStream_t s);   // zeros in d's columns up to a multiple of 64
 hipError_t launch_vocab_zero(void* p, int V, int n, long long ld, int es, hipStream_t s);
 
 }  // namespace poetx

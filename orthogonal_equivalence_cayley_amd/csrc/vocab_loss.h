@@ -15,20 +15,12 @@ __device__ __forceinline__ float exp_of(float x) {
   else return __expf(x);
 }
 
-// A row's maximum and sum of exponentials over some of its columns. Two of them join
-// into one; an empty one, or one of logits that are all -inf, has m = -inf and s = 0.
-__device__ __forceinline__ float2 join(float2 a, float2 b) {
-  const float m = fmaxf(a.x, b.x);
-  if (m == -__builtin_inff()) return float2{m, a.y + b.y};   // keeps a NaN of either sum
-  return float2{m, a.y * __expf(a.x - m) + b.y * __expf(b.x - m)};
-}
-
 // What the backward needs of a row
 struct Row {
   float lse, factor;
   long long target;   // -1: none (ignored, factor 0)
 };
-__device__ __forceinline__ Row row_of(const VocabArgs& a, long long t) {
+__device__ __forceinline__ Row token_of(const VocabArgs& a, long long t) {
   const long long target = a.target[t];
   if (target == a.ignore) return Row{0.0f, 0.0f, -1};
   // a target outside the vocabulary has no loss: its gradients are NaN

@@ -525,6 +525,7 @@ VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, 
   const long long pieces = (V + most - 1) / most;
   p.vp = (int)std::min<long long>(most, ((V + pieces - 1) / pieces + 255) / 256 * 256);
   p.pieces = (V + p.vp - 1) / p.vp;
+  p.ldp = p.vp + 64;
   p.grad_tile = tile_of(T, std::min(p.vp, V));
   p.dw_tile = tile_of(std::min(p.vp, V), n);
   p.dx_tile = tile_of(T, n);
@@ -533,7 +534,7 @@ VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, 
   const long long tiles = ((T + bm - 1) / bm) * ((n + bn - 1) / bn);
   p.splits = (int)std::max(1LL, std::min({64LL, 512 / tiles, (long long)std::min(p.vp, V) / 256}));
   p.acc = gx && (p.splits > 1 || p.pieces > 1);
-  p.at_x = padded((size_t)p.Tm * p.vp * es);
+  p.at_x = padded((size_t)p.Tm * p.ldp * es);
   p.at_acc = p.at_x + (gw ? padded((size_t)p.Tm * p.ldm * es) : 0);
   p.bytes = p.at_acc + (p.acc ? padded((size_t)p.splits * T * p.lda * 4) : 0);
   return p;
@@ -543,7 +544,7 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
   const VocabBackPlan p = vocab_backward_plan(in.T, in.V, in.n, bf16, in.GX != nullptr, in.GW != nullptr);
   VocabArgs a = in;
   a.dS = ws;
-  a.ldp = p.vp;
+  a.ldp = p.ldp;
   a.Xm = static_cast<char*>(ws) + p.at_x;
   a.ldm = p.ldm;
   a.Tm = p.Tm;

@@ -60,13 +60,38 @@ __device__ __forceinline__ void swap_halves(float& a, float& b) {
   b = __uint_as_float(r1);
 }
 
+// 16 bytes per lane from the buffer's byte `off` + `soff` to lane * 16 behind the LDS address
+// `to`. WRITTEN out for kernels that read by the transposing LDS read: beside the builtin the
+// compiler lets every such read of the wave wait for all its loads (16384 tokens, 8192 rows
+// of 2048: d W 553 -> 421, d^T X 591 -> 422 us). It has no result in registers; vm_wait waits
+// for it. M0, which the compiler keeps to itself, is left as it was; the s_nop is for scalar
+// operands that a vector instruction wrote.
+typedef uint32_t Buffer __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ Buffer buffer_at(const char* p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  return Buffer{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, 0x00020000u};
+}
+template <bool WRITTEN>
+__device__ __forceinline__ void load_lds(const char* p, uint32_t bytes, uint32_t to, uint32_t off, uint32_t soff) {
+  if constexpr (WRITTEN) {
+    uint32_t m0;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
+        : "=&s"(m0)
+        : "s"(to), "v"(off), "s"(buffer_at(p, bytes)), "s"(soff));
+  } else {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, (int)bytes, 0x00020000),
+        (__attribute__((address_space(3))) void*)(uintptr_t)to, 16, off, soff, 0, 0);
+  }
+}
+
 // How the lanes load and read an operand tile whose rows run along the summed axis, or
 // (ACROSS) across it. `w0`: the wave's first row of it.
 template <bool ACROSS>
 struct Side;
 template <>
 struct Side<false> {
-  static constexpr int kReads = 1;   // LDS reads a fragment
   uint32_t base;
   __device__ __forceinline__ void init(int w0, int lane) {
     // chunk c of row r at slot 8 r + (c ^ ((r / 2) & 7)): a step's address is base ^ (step << 5)
@@ -83,7 +108,6 @@ struct Side<false> {
 };
 template <>
 struct Side<true> {
-  static constexpr int kReads = 2;
   uint32_t at[4];
   __device__ __forceinline__ void init(int w0, int lane) {
     // 16 lanes read a 4 x 16 block, lane s its 8 bytes of summed row s / 4, and get column s
@@ -105,7 +129,9 @@ struct Side<true> {
   }
 };
 
-template <Mode MODE>
+// TAIL (DX): the piece of the vocabulary is no multiple of 64 (a branch around the loads
+// parts the products from the reads beside them, so it has its own kernel)
+template <Mode MODE, bool TAIL>
 __global__ __launch_bounds__(kThr) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void vocab_pipe_kernel(VocabArgs p) {
   constexpr bool AX = MODE == DW, BX = MODE == DX || MODE == DW;   // across the summed axis
@@ -148,6 +174,8 @@ void vocab_pipe_kernel(VocabArgs p) {
   };
 
   const int g = tid & 255;   // thread of the loading waves
+  const uint32_t lds_at = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)lds);
   const uint32_t va = Side<AX>::lane_offset(g, lda), vb = Side<BX>::lane_offset(g, ldb);
 
   // Where the loads of one operand stand: the stage's tile and its piece of the sum. Past
@@ -170,30 +198,25 @@ void vocab_pipe_kernel(VocabArgs p) {
   };
   // loads [i0, i1) of operand op (0: A, 1: B) of the cursor's stage into buffer buf
   auto issue = [&](const Cursor& c, int op, int buf, int i0, int i1) __attribute__((always_inline)) {
-    unsigned char* st = lds + buf * kStage + op * kOp + (wave & 3) * 64 * 16;
+    const uint32_t st = lds_at + (uint32_t)(buf * kStage + op * kOp + (wave & 3) * 64 * 16);
     const bool across = op == 0 ? AX : BX;
     const int ld = op == 0 ? lda : ldb;
     const char* base = (op == 0 ? a_base : b_base) +
                        (across ? (long long)c.kt * kKE * ld + c.row * 2LL : c.row * (long long)ld);
     // W ends with the vocabulary: behind its last row the last one is loaded again, for d is zero there
-    const int there = MODE == DX && op == 1 ? p.vp - c.kt * kKE : kKE;
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(base), (short)0, across ? (min(there, kKE) - 1) * ld + kTile * 2 : kTile * ld, 0x00020000);
+    const int there = TAIL && op == 1 ? p.vp - c.kt * kKE : kKE;
+    const uint32_t bytes = (uint32_t)(across ? (min(there, kKE) - 1) * ld + kTile * 2 : kTile * ld);
     const int k = across ? 0 : c.kt * kKB, step = across ? 8 * ld : 32 * ld;
-    if (MODE == DX && op == 1 && there < kKE) {
+    if (TAIL && op == 1 && there < kKE) {
 #pragma unroll
       for (int i = i0; i < i1; ++i) {
         const int kr = g >> 5, row = min(kr + 8 * i, there - 1);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs, (__attribute__((address_space(3))) void*)(st + i * 256 * 16), 16,
-            (uint32_t)(row * ld) + (uint32_t)((g & 31) ^ (4 * (kr & 3))) * 16, 0, 0, 0);
+        load_lds<BX>(base, bytes, st + i * 256 * 16, (uint32_t)(row * ld) + (uint32_t)((g & 31) ^ (4 * (kr & 3))) * 16, 0);
       }
       return;
     }
 #pragma unroll
-    for (int i = i0; i < i1; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs, (__attribute__((address_space(3))) void*)(st + i * 256 * 16), 16, op == 0 ? va : vb, k + i * step, 0, 0);
+    for (int i = i0; i < i1; ++i) load_lds<BX>(base, bytes, st + i * 256 * 16, op == 0 ? va : vb, (uint32_t)(k + i * step));
   };
 
   Side<AX> sa;
@@ -365,9 +388,6 @@ void vocab_pipe_kernel(VocabArgs p) {
 
   auto run = [&](auto ld_tag) {
     constexpr bool LD = decltype(ld_tag)::value;
-    constexpr int kReads = 4 * Side<AX>::kReads + 2 * Side<BX>::kReads;   // LDS reads of a step, beside its 8 products
-    constexpr int kPer = kReads <= 8 ? 1 : 2, kSlots = kReads / kPer;
-    static_assert(kReads % kPer == 0 && kSlots <= 8, "reads between products");
     Cursor ca{}, cw{};   // A stands two stages ahead, B one
     if constexpr (LD) {
       ca = Cursor{0, 0, row_of(0, 0)};
@@ -388,17 +408,6 @@ void vocab_pipe_kernel(VocabArgs p) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) bf[set][j] = sb.frag(st + kOp, j, step);
     };
-    auto spread = [](auto loads) __attribute__((always_inline)) {
-      constexpr int N = decltype(loads)::value;
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (N > 0) __builtin_amdgcn_sched_group_barrier(0x020, (N + kSlots - 1) / kSlots, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, kPer, 0);
-      }
-      if (kSlots < 8) __builtin_amdgcn_sched_group_barrier(0x008, 8 - kSlots, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    };
     read(lds, 0, 0);
 
     int buf = 0;
@@ -413,35 +422,38 @@ void vocab_pipe_kernel(VocabArgs p) {
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-      auto multiply = [&](int set) __attribute__((always_inline)) {
+      // The 8 products of a step, and one after another between them the next step's 6
+      // fragments from `st` and the loads [i0, i1) of op's cursor, in just this order
+      auto step = [&](int set, const unsigned char* next, int kk, const Cursor& c, int op, int into, int i0, int i1)
+                      __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bf[set][j]),
-                                                                __builtin_bit_cast(bf16x8, af[set][i]), acc[i][j], 0, 0, 0);
+        for (int q = 0; q < 8; ++q) {
+          const int i = q / 2, j = q & 1;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, bf[set][j]),
+                                                              __builtin_bit_cast(bf16x8, af[set][i]), acc[i][j], 0, 0, 0);
+          if (q == 0) af[set ^ 1][0] = sa.frag(next, 0, kk);
+          else if (q == 1) bf[set ^ 1][0] = sb.frag(next + kOp, 0, kk);
+          else if (q == 2) bf[set ^ 1][1] = sb.frag(next + kOp, 1, kk);
+          else if (q < 6) af[set ^ 1][q - 2] = sa.frag(next, q - 2, kk);
+          if (i1 - i0 == 8) issue(c, op, into, q, q + 1);
+          else if (i1 - i0 == 4 && (q & 1)) issue(c, op, into, i0 + q / 2, i0 + q / 2 + 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       };
       for (int kt = 0; kt < nk; ++kt, buf ^= 1) {
         const unsigned char* st = lds + buf * kStage;
 #pragma unroll
         for (int kk = 0; kk < kSteps; ++kk) {
-          const int cb = kk & 1, nb = cb ^ 1;
+          const int cb = kk & 1;
           if (kk + 1 < kSteps) {
-            if (LD && kk < 2) issue(cw, 1, buf ^ 1, kk * (kLoads / 2), (kk + 1) * (kLoads / 2));
-            read(st, nb, kk + 1);
-            multiply(cb);
-            if (LD && kk < 2) spread(std::integral_constant<int, kLoads / 2>{});
-            else spread(std::integral_constant<int, 0>{});
+            if (LD && kk < 2) step(cb, st, kk + 1, cw, 1, buf ^ 1, kk * (kLoads / 2), (kk + 1) * (kLoads / 2));
+            else step(cb, st, kk + 1, cw, 1, 0, 0, 0);
           } else {
             // the next stage landed, and this one no longer read by anyone, once every
             // wave is past this barrier
             if constexpr (LD) vm_wait<0>();
             lds_sync();
-            if constexpr (LD) issue(ca, 0, buf, 0, kLoads);
-            read(lds + (buf ^ 1) * kStage, nb, 0);
-            multiply(cb);
-            if constexpr (LD) spread(std::integral_constant<int, kLoads>{});
-            else spread(std::integral_constant<int, 0>{});
+            step(cb, lds + (buf ^ 1) * kStage, 0, ca, 0, buf, 0, LD ? kLoads : 0);
             if constexpr (LD) {
               advance(ca, 0);
               advance(cw, 1);
@@ -466,7 +478,10 @@ hipError_t launch(const VocabArgs& a, hipStream_t s) {
   const long long ntile = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
   // a multiple of 8, so that every XCD's range of tiles has its workgroups
   const long long grid = std::min<long long>((ntile + 7) / 8 * 8, 256);
-  hipLaunchKernelGGL((vocab_pipe_kernel<MODE>), dim3((unsigned)grid), dim3(kThr), kLds, s, a);
+  if (MODE == DX && a.vp % kKE)
+    hipLaunchKernelGGL((vocab_pipe_kernel<MODE, MODE == DX>), dim3((unsigned)grid), dim3(kThr), kLds, s, a);
+  else
+    hipLaunchKernelGGL((vocab_pipe_kernel<MODE, false>), dim3((unsigned)grid), dim3(kThr), kLds, s, a);
   return hipGetLastError();
 }
 

@@ -384,7 +384,7 @@ struct VocabPlan {
   size_t bytes;
 };
 struct VocabBackPlan {
-  long long Tm, ldm, lda, pieces;
+  long long Tm, ldm, ldp, lda, pieces;
   int vp, grad_tile, dx_tile, dw_tile, splits;
   bool acc;
   size_t at_x, at_acc, bytes;

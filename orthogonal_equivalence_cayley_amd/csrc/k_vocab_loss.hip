@@ -369,7 +369,7 @@ __global__ __launch_bounds__(kThr) void vocab_join_kernel(VocabArgs a, int group
 
 // Xm = X with zeros in ignored rows (a padded token's activations may be anything, and
 // 0 times infinity would reach dW), columns up to ldm and rows up to a.Tm zero too; d's rows
-// behind the last token as well
+// behind the last token as well, and its columns from vp to a multiple of 64
 template <typename E>
 __global__ __launch_bounds__(kThr) void vocab_mask_kernel(VocabArgs a) {
   constexpr int N = 16 / sizeof(E);
@@ -382,6 +382,11 @@ __global__ __launch_bounds__(kThr) void vocab_mask_kernel(VocabArgs a) {
       i32x4 v = {0, 0, 0, 0};
       if (!none) v = load16<sizeof(E)>(from, (long long)c * 16, (long long)a.n * sizeof(E));
       reinterpret_cast<i32x4*>(to)[c] = v;
+    }
+    if (a.vp % 64 && t < a.T && threadIdx.x < 64) {
+      // behind a single piece's last column
+      const int c = a.vp + (int)threadIdx.x;
+      if (c < (a.vp + 63) / 64 * 64) static_cast<E*>(a.dS)[t * a.ldp + c] = E(0);
     }
     if (t >= a.T) {
       i32x4* const d = reinterpret_cast<i32x4*>(static_cast<E*>(a.dS) + t * a.ldp);
@@ -416,6 +421,10 @@ __global__ __launch_bounds__(kThr) void vocab_zero_kernel(E* p, int V, int n, lo
     for (int c = threadIdx.x; c < n; c += kThr) p[v * ld + c] = E(0);
 }
 
+// 128 rows by 128 columns, fp32 by 64: two workgroups to a CU, for one wave to a SIMD
+// leaves its matrix unit idle (512 x 512 x 8000 53 -> 45 us)
+constexpr int big_cols(bool bf16) { return bf16 ? 128 : 64; }
+
 template <typename Ty, int BM, int BN, Mode M>
 hipError_t tiles(const VocabArgs& a, hipStream_t s) {
   const long long rows = M == DW ? a.vp : a.T;
@@ -428,7 +437,7 @@ hipError_t tiles(const VocabArgs& a, hipStream_t s) {
 template <typename Ty, Mode M>
 hipError_t tiles(const VocabArgs& a, int tile, hipStream_t s) {
   switch (tile) {
-    case VOCAB_TILE_128: return tiles<Ty, 128, 128, M>(a, s);
+    case VOCAB_TILE_BIG: return tiles<Ty, 128, big_cols(Ty::kSize == 2), M>(a, s);
     case VOCAB_TILE_64: return tiles<Ty, 64, 64, M>(a, s);
     case VOCAB_TILE_32x64: return tiles<Ty, 32, 64, M>(a, s);
   }
@@ -439,23 +448,48 @@ hipError_t tiles(const VocabArgs& a, int bf16, int tile, hipStream_t s) {
   return bf16 ? tiles<TypeBf16, M>(a, tile, s) : tiles<TypeF32, M>(a, tile, s);
 }
 
-// The largest tile that leaves few CUs idle
-int tile_of(long long rows, long long cols) {
-  const auto count = [&](int bm, int bn) { return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn); };
-  if (rows > 64 && count(128, 128) >= 200) return VOCAB_TILE_128;
-  if (rows > 32) return VOCAB_TILE_64;
-  return VOCAB_TILE_32x64;
-}
-int group_cols(int tile) { return tile == VOCAB_TILE_128 ? 64 : 32; }
+// How a product is laid out: its tile, and how many workgroups share the sum of one.
+// `cost` in us, of measured parts: a stage of 128 bytes of the sum takes a tile `alone` on
+// its CU or two beside each other there `pair` (256 x 256 tiles have a CU to themselves), a
+// tile's start and epilogue `ends`.
+struct TileCost {
+  int tile, bm, bn;
+  double alone, pair, ends;
+};
+constexpr TileCost kBf16[] = {{VOCAB_TILE_256, 256, 256, 0.88, 1.76, 9},
+                              {VOCAB_TILE_BIG, 128, 128, 0.85, 1.4, 5},
+                              {VOCAB_TILE_64, 64, 64, 0.75, 1.2, 4},
+                              {VOCAB_TILE_32x64, 32, 64, 0.65, 0.95, 4}};
+constexpr TileCost kF32[] = {{VOCAB_TILE_BIG, 128, 64, 1.6, 2.6, 5},
+                             {VOCAB_TILE_64, 64, 64, 1.0, 1.5, 4},
+                             {VOCAB_TILE_32x64, 32, 64, 0.8, 1.1, 4}};
 
-// Whether 256 x 256 tiles (k_vocab_loss_pipe.hip) take less time than 128 x 128 ones: in
-// units of a CU's time for one of the latter, a round of 256 of the former takes 3.5, of
-// 512 of the latter, two to a CU, 2.5, and up to 256 of them 1.5
-bool pipe_pays(long long rows, long long cols) {
-  const auto count = [&](int b) { return ((rows + b - 1) / b) * ((cols + b - 1) / b); };
-  const double pipe = 3.5 * (double)((count(256) + 255) / 256), n = (double)count(128);
-  return pipe <= (n <= 256 ? 1.5 : 2.5 * std::ceil(n / 512));
+template <size_t N>
+VocabTiles cheapest(const TileCost (&costs)[N], long long rows, long long cols, long long stages, bool wide, bool share) {
+  VocabTiles best{-1, 1, 0.0};
+  for (const TileCost& c : costs) {
+    if (c.tile == VOCAB_TILE_256 && !wide) continue;
+    if (c.bm > 32 && rows <= c.bm / 2 && c.tile != VOCAB_TILE_256) continue;
+    const long long n = ((rows + c.bm - 1) / c.bm) * ((cols + c.bn - 1) / c.bn);
+    const long long slots = c.tile == VOCAB_TILE_256 ? 256 : 512;
+    for (int splits = 1; splits <= (share ? 64 : 1); splits *= 2) {
+      const long long per = (stages + splits - 1) / splits, items = n * splits;
+      if (splits > 1 && (per < 4 || items > slots)) break;
+      // shares are written and read once more, by another launch
+      const double extra = splits > 1 ? 4 + 8e-6 * (double)splits * (double)(rows * cols) / 4.0 : 0.0;
+      const double round = items <= 256 ? per * c.alone : per * c.pair;
+      const double cost = (round + c.ends) * (double)((items + slots - 1) / slots) + extra;
+      if (best.tile < 0 || cost < best.cost) best = VocabTiles{c.tile, splits, cost};
+    }
+  }
+  return best;
 }
+// wide: whether 256 x 256 tiles may be taken
+VocabTiles tiles_of(long long rows, long long cols, long long sum, int bf16, bool wide, bool share = false) {
+  const long long stages = (sum * (bf16 ? 2 : 4) + kKB - 1) / kKB;
+  return bf16 ? cheapest(kBf16, rows, cols, stages, wide, share) : cheapest(kF32, rows, cols, stages, false, share);
+}
+int group_cols(int tile, int bf16) { return tile == VOCAB_TILE_BIG && bf16 ? 64 : 32; }
 
 constexpr long long kRoom = 256LL << 20;   // bytes that a part of the work may take as workspace
 size_t padded(size_t b) { return (b + 255) / 256 * 256; }
@@ -469,20 +503,22 @@ hipError_t launch_vocab_zero(void* p, int V, int n, long long ld, int es, hipStr
   return hipGetLastError();
 }
 
-VocabPlan vocab_forward_plan(long long T, int V, int) {
+VocabPlan vocab_forward_plan(long long T, int V, int n, int bf16) {
   VocabPlan p{};
-  p.tile = tile_of(T, V);
-  // 256-column tiles leave parts of 64, whole tiles of them
-  p.groups = std::max((V + group_cols(p.tile) - 1) / group_cols(p.tile), (V + 255) / 256 * 4);
+  // as the operands' alignment may lead: 256 x 256 tiles (parts of 64 columns, whole tiles of them) or not
+  p.lay[0] = tiles_of(T, V, n, bf16, false);
+  p.lay[1] = tiles_of(T, V, n, bf16, bf16 && T >= 256 && V >= 256);
+  const int cols = group_cols(p.lay[0].tile, bf16);
+  p.groups = std::max((V + cols - 1) / cols, p.lay[1].tile == VOCAB_TILE_256 ? (V + 255) / 256 * 4 : 0);
   // tokens of a launch: as many as their parts leave room for, and their tiles can be counted
-  const long long most = std::min(kRoom / (8LL * p.groups), (1LL << 34) / V);
+  const long long most = std::min(kRoom / (8LL * p.groups), (1LL << 33) / V);
   p.rows = std::min(T, std::max(256LL, most / 256 * 256));
   p.bytes = padded((size_t)p.rows * p.groups * 8) + padded((size_t)p.rows * 4);
   return p;
 }
 
 hipError_t launch_vocab_forward(const VocabArgs& in, int bf16, void* ws, hipStream_t s) {
-  const VocabPlan p = vocab_forward_plan(in.T, in.V, in.n);
+  const VocabPlan p = vocab_forward_plan(in.T, in.V, in.n, bf16);
   const int es = bf16 ? 2 : 4;
   for (long long t = 0; t < in.T; t += p.rows) {
     VocabArgs a = in;
@@ -495,13 +531,14 @@ hipError_t launch_vocab_forward(const VocabArgs& in, int bf16, void* ws, hipStre
     a.zt = reinterpret_cast<float*>(static_cast<char*>(ws) + padded((size_t)p.rows * p.groups * 8));
     a.v0 = 0;
     a.vp = a.V;
-    int groups = (a.V + group_cols(p.tile) - 1) / group_cols(p.tile);
+    int groups;
     hipError_t e;
-    if (bf16 && vocab_pipe_logits(a) && pipe_pays(a.T, a.V)) {
+    if (p.lay[1].tile == VOCAB_TILE_256 && vocab_pipe_logits(a)) {
       groups = (a.V + 255) / 256 * 4;
       e = launch_vocab_pipe_stats(a, s);
     } else {
-      e = tiles<STATS>(a, bf16, p.tile, s);
+      groups = (a.V + group_cols(p.lay[0].tile, bf16) - 1) / group_cols(p.lay[0].tile, bf16);
+      e = tiles<STATS>(a, bf16, p.lay[0].tile, s);
     }
     if (e != hipSuccess) return e;
     if (a.T >= 1024)
@@ -524,19 +561,21 @@ VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, 
   const long long most = std::max(256LL, std::min(kRoom / (p.Tm * es), (1LL << 36) / n) / 256 * 256);
   const long long pieces = (V + most - 1) / most;
   p.vp = (int)std::min<long long>(most, ((V + pieces - 1) / pieces + 255) / 256 * 256);
-  p.pieces = (V + p.vp - 1) / p.vp;
-  p.ldp = p.vp + 64;
-  p.grad_tile = tile_of(T, std::min(p.vp, V));
-  p.dw_tile = tile_of(std::min(p.vp, V), n);
-  p.dx_tile = tile_of(T, n);
-  // few tiles of dX share the vocabulary's piece
-  const int bm = p.dx_tile == VOCAB_TILE_128 ? 128 : p.dx_tile == VOCAB_TILE_64 ? 64 : 32, bn = bm == 128 ? 128 : 64;
-  const long long tiles = ((T + bm - 1) / bm) * ((n + bn - 1) / bn);
-  p.splits = (int)std::max(1LL, std::min({64LL, 512 / tiles, (long long)std::min(p.vp, V) / 256}));
-  p.acc = gx && (p.splits > 1 || p.pieces > 1);
-  p.at_x = padded((size_t)p.Tm * p.ldp * es);
+  const int vp = std::min(p.vp, V);
+  const bool one = V <= p.vp;
+  // as the operands' alignment may lead: 256 x 256 tiles or not
+  p.dx[0] = tiles_of(T, n, vp, bf16, false, true);
+  p.dx[1] = tiles_of(T, n, vp, bf16, bf16 && vocab_pipe_dx(T, n), true);
+  // shares none of which is empty in the first piece (the others only add to theirs)
+  for (VocabTiles& d : p.dx) {
+    const long long stages = ((long long)vp * es + kKB - 1) / kKB, per = (stages + d.splits - 1) / d.splits;
+    d.splits = (int)((stages + per - 1) / per);
+  }
+  const int splits = std::max(p.dx[0].splits, p.dx[1].splits);
+  p.acc = gx && (splits > 1 || !one);
+  p.at_x = padded((size_t)p.Tm * p.vp * es);
   p.at_acc = p.at_x + (gw ? padded((size_t)p.Tm * p.ldm * es) : 0);
-  p.bytes = p.at_acc + (p.acc ? padded((size_t)p.splits * T * p.lda * 4) : 0);
+  p.bytes = p.at_acc + (p.acc ? padded((size_t)splits * T * p.lda * 4) : 0);
   return p;
 }
 
@@ -544,16 +583,18 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
   const VocabBackPlan p = vocab_backward_plan(in.T, in.V, in.n, bf16, in.GX != nullptr, in.GW != nullptr);
   VocabArgs a = in;
   a.dS = ws;
-  a.ldp = p.ldp;
+  a.ldp = p.vp;
   a.Xm = static_cast<char*>(ws) + p.at_x;
   a.ldm = p.ldm;
   a.Tm = p.Tm;
-  a.acc = p.acc ? reinterpret_cast<float*>(static_cast<char*>(ws) + p.at_acc) : nullptr;
   a.lda = p.lda;
-  a.splits = p.splits;
+  const VocabTiles dx = p.dx[bf16 && vocab_pipe_weight(a) ? 1 : 0];
+  const bool wide_dx = dx.tile == VOCAB_TILE_256;
+  a.splits = dx.splits;
+  a.acc = a.splits > 1 || a.V > p.vp ? reinterpret_cast<float*>(static_cast<char*>(ws) + p.at_acc) : nullptr;
   hipError_t e;
-  const bool pipe_dx = bf16 && a.GX && p.splits == 1 && vocab_pipe_dx(a) && pipe_pays(a.T, a.n);
   if (a.GW) {
+    a.vp = a.V <= p.vp ? a.V : p.vp;
     const dim3 grid((unsigned)std::min<long long>(a.Tm, 1 << 16));
     if (bf16) hipLaunchKernelGGL((vocab_mask_kernel<uint16_t>), grid, dim3(kThr), 0, s, a);
     else hipLaunchKernelGGL((vocab_mask_kernel<float>), grid, dim3(kThr), 0, s, a);
@@ -563,24 +604,25 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
   for (long long v = 0; v < a.V; v += p.vp) {
     a.v0 = (int)v;
     a.vp = (int)std::min<long long>(p.vp, a.V - v);
-    e = bf16 && vocab_pipe_logits(a) && pipe_pays(a.T, a.vp) ? launch_vocab_pipe_grad(a, s)
-                                                            : tiles<GRAD>(a, bf16, p.grad_tile, s);
+    const VocabTiles grad = tiles_of(a.T, a.vp, a.n, bf16, bf16 && vocab_pipe_logits(a));
+    e = grad.tile == VOCAB_TILE_256 ? launch_vocab_pipe_grad(a, s) : tiles<GRAD>(a, bf16, grad.tile, s);
     if (e != hipSuccess) return e;
     if (a.GX) {
-      if (pipe_dx && a.vp % 64) {
+      if (wide_dx && a.vp % 64 && (!a.GW || a.v0 > 0)) {
         e = launch_vocab_pad(a, s);
         if (e != hipSuccess) return e;
       }
-      e = pipe_dx ? launch_vocab_pipe_dx(a, s) : tiles<DX>(a, bf16, p.dx_tile, s);
+      e = wide_dx ? launch_vocab_pipe_dx(a, s) : tiles<DX>(a, bf16, dx.tile, s);
       if (e != hipSuccess) return e;
     }
     if (a.GW) {
-      e = bf16 && vocab_pipe_dw(a) && pipe_pays(a.vp, a.n) ? launch_vocab_pipe_dw(a, s)
-                                                          : tiles<DW>(a, bf16, p.dw_tile, s);
+      const VocabTiles dw = tiles_of(a.vp, a.n, a.T, bf16, bf16 && vocab_pipe_dw(a));
+      e = dw.tile == VOCAB_TILE_256 ? launch_vocab_pipe_dw(a, s) : tiles<DW>(a, bf16, dw.tile, s);
       if (e != hipSuccess) return e;
     }
   }
-  if (!a.acc || pipe_dx) return hipSuccess;   // the last piece of the pipelined dX writes it whole
+  // the last piece of an unshared dX in 256 x 256 tiles writes it whole
+  if (!a.GX || !a.acc || (wide_dx && a.splits == 1)) return hipSuccess;
   const long long quads = a.T * ((a.n + 3) / 4);
   const dim3 grid((unsigned)std::min<long long>((quads + kThr - 1) / kThr, 1 << 16));
   if (bf16) hipLaunchKernelGGL((vocab_finish_kernel<false>), grid, dim3(kThr), 0, s, a);

@@ -14,8 +14,8 @@
 //
 // A last tile that would pass the last row or column is moved back to end there, so that
 // every load is inside its operand; what it shares with its neighbour is left to that one.
-// Requirements (vocab_pipe_supported): at least one tile of each axis, n a multiple of 64
-// where it is summed and of 8 where not, 16-byte rows of X and W.
+// Requirements (vocab_pipe_logits and the like): at least one tile of each axis, n a multiple
+// of 8, 16-byte rows of X and W.
 #include <algorithm>
 #include <type_traits>
 
@@ -129,8 +129,9 @@ struct Side<true> {
   }
 };
 
-// TAIL (DX): the piece of the vocabulary is no multiple of 64 (a branch around the loads
-// parts the products from the reads beside them, so it has its own kernel)
+// TAIL: the last stage of a sum is cut, for n (STATS, GRAD) or the piece of the vocabulary
+// (DX) is no multiple of 64 (a branch around the loads parts the products from the reads
+// beside them, so it has its own kernel)
 template <Mode MODE, bool TAIL>
 __global__ __launch_bounds__(kThr) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void vocab_pipe_kernel(VocabArgs p) {
@@ -152,19 +153,23 @@ void vocab_pipe_kernel(VocabArgs p) {
       MODE == DW ? static_cast<const char*>(p.Xm) : static_cast<const char*>(p.W) + (long long)p.v0 * p.ldw * 2;
   const int lda = (int)((MODE == STATS || MODE == GRAD ? p.ldx : p.ldp) * 2);   // bytes, 256 of them below 2^31
   const int ldb = (int)((MODE == DW ? p.ldm : p.ldw) * 2);
-  const int nk = sum / kKE;
+  // DX of few tiles: p.splits workgroups share the sum of one, `per` stages each
+  const int nk_all = (sum + kKE - 1) / kKE;
+  const int per = MODE == DX ? (nk_all + p.splits - 1) / p.splits : nk_all;
+  const int shares = MODE == DX ? (nk_all + per - 1) / per : 1;
 
   // XCD x = blockIdx.x % 8 owns the tiles [ntile x / 8, ntile (x + 1) / 8), walked by its
   // workgroups with a stride of their count, in groups of kGroupRows tile-rows
   const int tn = (cols + kTile - 1) / kTile, tm = (rows + kTile - 1) / kTile;
-  const int ntile = tn * tm;
+  const int ntile = tn * tm * shares;
   const int x = blockIdx.x % 8, sx = blockIdx.x / 8;
   const int nx = (int)gridDim.x / 8 + (x < (int)gridDim.x % 8 ? 1 : 0);
   const int t_first = (int)((long long)ntile * x / 8) + sx, t_end = (int)((long long)ntile * (x + 1) / 8);
   const int t_count = t_first < t_end ? (t_end - t_first + nx - 1) / nx : 0;
   if (t_count == 0) return;
+  auto share = [&](int ti) { return MODE == DX ? __builtin_amdgcn_readfirstlane((t_first + ti * nx) / (tn * tm)) : 0; };
   auto origin = [&](int ti, int& m0, int& n0) {
-    const int lin = t_first + ti * nx;
+    const int lin = t_first + ti * nx - share(ti) * (tn * tm);
     const int grp = lin / (kGroupRows * tn);
     const int first = grp * kGroupRows;
     const int gsz = min(kGroupRows, tm - first);
@@ -181,7 +186,7 @@ void vocab_pipe_kernel(VocabArgs p) {
   // Where the loads of one operand stand: the stage's tile and its piece of the sum. Past
   // the last stage they repeat it, into buffers nobody reads.
   struct Cursor {
-    int ti, kt, row;
+    int ti, kt, end, row;
   };
   auto row_of = [&](int ti, int op) {
     int m0, n0;
@@ -189,12 +194,25 @@ void vocab_pipe_kernel(VocabArgs p) {
     return op == 0 ? min(m0, rows - kTile) : min(n0, cols - kTile);
   };
   auto advance = [&](Cursor& c, int op) {
-    if (c.kt + 1 < nk) {
+    if (c.kt + 1 < c.end) {
       ++c.kt;
     } else if (c.ti + 1 < t_count) {
-      c.kt = 0;
       c.row = row_of(++c.ti, op);
+      c.kt = share(c.ti) * per;
+      c.end = min(c.kt + per, nk_all);
     }
+  };
+  auto start = [&](int op) { return Cursor{0, share(0) * per, min(share(0) * per + per, nk_all), row_of(0, op)}; };
+  // TAIL along n: chunks behind the last column. Their lanes load the stage's first chunk of
+  // the row instead, and write zeros over it once it landed
+  const uint32_t lc = (uint32_t)((g & 7) ^ ((g / 16) & 7)) * 16;
+  constexpr bool CUT = TAIL && !BX;
+  auto gone = [&](int kt) { return kt * kKE + (int)lc / 2 >= sum; };
+  auto clear = [&](int buf) __attribute__((always_inline)) {
+    if (!gone(nk_all - 1)) return;
+#pragma unroll
+    for (int i = 0; i < 2 * kLoads; ++i)
+      *reinterpret_cast<i32x4*>(lds + buf * kStage + i * 4096 + g * 16) = i32x4{0, 0, 0, 0};
   };
   // loads [i0, i1) of operand op (0: A, 1: B) of the cursor's stage into buffer buf
   auto issue = [&](const Cursor& c, int op, int buf, int i0, int i1) __attribute__((always_inline)) {
@@ -204,10 +222,10 @@ void vocab_pipe_kernel(VocabArgs p) {
     const char* base = (op == 0 ? a_base : b_base) +
                        (across ? (long long)c.kt * kKE * ld + c.row * 2LL : c.row * (long long)ld);
     // W ends with the vocabulary: behind its last row the last one is loaded again, for d is zero there
-    const int there = TAIL && op == 1 ? p.vp - c.kt * kKE : kKE;
+    const int there = TAIL && BX && op == 1 ? p.vp - c.kt * kKE : kKE;
     const uint32_t bytes = (uint32_t)(across ? (min(there, kKE) - 1) * ld + kTile * 2 : kTile * ld);
     const int k = across ? 0 : c.kt * kKB, step = across ? 8 * ld : 32 * ld;
-    if (TAIL && op == 1 && there < kKE) {
+    if (TAIL && BX && op == 1 && there < kKE) {
 #pragma unroll
       for (int i = i0; i < i1; ++i) {
         const int kr = g >> 5, row = min(kr + 8 * i, there - 1);
@@ -215,8 +233,9 @@ void vocab_pipe_kernel(VocabArgs p) {
       }
       return;
     }
+    const uint32_t off = (op == 0 ? va : vb) - (CUT && gone(c.kt) ? lc : 0);
 #pragma unroll
-    for (int i = i0; i < i1; ++i) load_lds<BX>(base, bytes, st + i * 256 * 16, op == 0 ? va : vb, (uint32_t)(k + i * step));
+    for (int i = i0; i < i1; ++i) load_lds<BX>(base, bytes, st + i * 256 * 16, off, (uint32_t)(k + i * step));
   };
 
   Side<AX> sa;
@@ -326,8 +345,9 @@ void vocab_pipe_kernel(VocabArgs p) {
     }
   };
   const float scale = MODE == DX || MODE == DW ? (p.g_each ? 1.0f : *p.g) : 1.0f;
-  auto dx = [&](Acc (&acc)[4][2], int m0, int n0, int m1, int n1) __attribute__((always_inline)) {
-    const bool first = p.v0 == 0, last = p.v0 + p.vp == p.V;
+  auto dx = [&](Acc (&acc)[4][2], int m0, int n0, int m1, int n1, int ti) __attribute__((always_inline)) {
+    const bool first = p.v0 == 0, last = p.v0 + p.vp == p.V && p.splits == 1;
+    float* const sums = p.acc + share(ti) * p.T * p.lda;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const long long t = (long long)m0 + wm0 + i * 32 + cm;
@@ -337,7 +357,7 @@ void vocab_pipe_kernel(VocabArgs p) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           old[q][k] = first ? f32x4{0.0f, 0.0f, 0.0f, 0.0f}
-                            : *reinterpret_cast<const f32x4*>(p.acc + t * p.lda + column(n0, q) + 4 * k);
+                            : *reinterpret_cast<const f32x4*>(sums + t * p.lda + column(n0, q) + 4 * k);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float v[8];
@@ -354,7 +374,7 @@ void vocab_pipe_kernel(VocabArgs p) {
         } else {
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<f32x4*>(p.acc + t * p.lda + c + 4 * k) =
+            *reinterpret_cast<f32x4*>(sums + t * p.lda + c + 4 * k) =
                 f32x4{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
         }
       }
@@ -379,10 +399,10 @@ void vocab_pipe_kernel(VocabArgs p) {
       }
     }
   };
-  auto finish = [&](Acc (&acc)[4][2], int m0, int n0, int m1, int n1) __attribute__((always_inline)) {
+  auto finish = [&](Acc (&acc)[4][2], int m0, int n0, int m1, int n1, int ti) __attribute__((always_inline)) {
     if constexpr (MODE == STATS) stats(acc, m0, n0, m1, n1);
     else if constexpr (MODE == GRAD) grad(acc, m0, n0, m1, n1);
-    else if constexpr (MODE == DX) dx(acc, m0, n0, m1, n1);
+    else if constexpr (MODE == DX) dx(acc, m0, n0, m1, n1, ti);
     else dw(acc, m0, n0, m1, n1);
   };
 
@@ -390,8 +410,8 @@ void vocab_pipe_kernel(VocabArgs p) {
     constexpr bool LD = decltype(ld_tag)::value;
     Cursor ca{}, cw{};   // A stands two stages ahead, B one
     if constexpr (LD) {
-      ca = Cursor{0, 0, row_of(0, 0)};
-      cw = Cursor{0, 0, row_of(0, 1)};
+      ca = start(0);
+      cw = start(1);
       issue(ca, 0, 0, 0, kLoads);
       issue(cw, 1, 0, 0, kLoads);
       advance(ca, 0);
@@ -399,6 +419,7 @@ void vocab_pipe_kernel(VocabArgs p) {
       issue(ca, 0, 1, 0, kLoads);   // stage 1's A tile; its B tile goes out in stage 0's first steps
       advance(ca, 0);
       vm_wait<kLoads>();            // stage 0 landed
+      if (CUT && nk_all == 1) clear(0);
     }
     lds_sync();
     i32x4 af[2][4], bf[2][2];
@@ -440,6 +461,7 @@ void vocab_pipe_kernel(VocabArgs p) {
           __builtin_amdgcn_sched_barrier(0);
         }
       };
+      const int nk = MODE == DX ? min(per, nk_all - share(ti) * per) : nk_all;
       for (int kt = 0; kt < nk; ++kt, buf ^= 1) {
         const unsigned char* st = lds + buf * kStage;
 #pragma unroll
@@ -451,7 +473,10 @@ void vocab_pipe_kernel(VocabArgs p) {
           } else {
             // the next stage landed, and this one no longer read by anyone, once every
             // wave is past this barrier
-            if constexpr (LD) vm_wait<0>();
+            if constexpr (LD) {
+              vm_wait<0>();
+              if (CUT && (kt + 2 == nk || nk == 1)) clear(buf ^ 1);
+            }
             lds_sync();
             step(cb, lds + (buf ^ 1) * kStage, 0, ca, 0, buf, 0, LD ? kLoads : 0);
             if constexpr (LD) {
@@ -461,7 +486,7 @@ void vocab_pipe_kernel(VocabArgs p) {
           }
         }
       }
-      finish(acc, m0, n0, m1, n1);
+      finish(acc, m0, n0, m1, n1, ti);
     }
   };
   if (wave < 4) run(std::true_type{});
@@ -475,11 +500,12 @@ template <Mode MODE>
 hipError_t launch(const VocabArgs& a, hipStream_t s) {
   const long long rows = MODE == DW ? (a.vp + 63) / 64 * 64 : a.T;
   const long long cols = MODE == STATS || MODE == GRAD ? a.vp : MODE == DX ? a.n : a.ldm;
-  const long long ntile = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
+  const long long ntile = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile) * (MODE == DX ? a.splits : 1);
   // a multiple of 8, so that every XCD's range of tiles has its workgroups
   const long long grid = std::min<long long>((ntile + 7) / 8 * 8, 256);
-  if (MODE == DX && a.vp % kKE)
-    hipLaunchKernelGGL((vocab_pipe_kernel<MODE, MODE == DX>), dim3((unsigned)grid), dim3(kThr), kLds, s, a);
+  const bool tail = MODE == DX ? a.vp % kKE != 0 : MODE != DW && a.n % kKE != 0;
+  if (tail)
+    hipLaunchKernelGGL((vocab_pipe_kernel<MODE, MODE != DW>), dim3((unsigned)grid), dim3(kThr), kLds, s, a);
   else
     hipLaunchKernelGGL((vocab_pipe_kernel<MODE, false>), dim3((unsigned)grid), dim3(kThr), kLds, s, a);
   return hipGetLastError();
@@ -500,12 +526,11 @@ bool aligned16(const void* p, long long ld) { return ((uintptr_t)p & 15) == 0 &&
 }  // namespace
 
 bool vocab_pipe_logits(const VocabArgs& a) {
-  return a.T >= kTile && a.vp >= kTile && a.n % kKE == 0 && aligned16(a.X, a.ldx) && aligned16(a.W, a.ldw) &&
+  return a.T >= kTile && a.vp >= kTile && a.n % 8 == 0 && aligned16(a.X, a.ldx) && aligned16(a.W, a.ldw) &&
          a.ldx < (1 << 21) && a.ldw < (1 << 21);
 }
-bool vocab_pipe_dx(const VocabArgs& a) {
-  return a.T >= kTile && a.n >= kTile && a.n % 8 == 0 && aligned16(a.W, a.ldw) && a.ldw < (1 << 21) && a.ldp < (1 << 21);
-}
+bool vocab_pipe_dx(long long T, int n) { return T >= kTile && n >= kTile && n % 8 == 0; }
+bool vocab_pipe_weight(const VocabArgs& a) { return aligned16(a.W, a.ldw) && a.ldw < (1 << 21) && a.ldp < (1 << 21); }
 bool vocab_pipe_dw(const VocabArgs& a) { return a.vp > kTile - 64 && a.ldm >= kTile && a.ldp < (1 << 21); }
 
 hipError_t launch_vocab_pipe_stats(const VocabArgs& a, hipStream_t s) { return launch<STATS>(a, s); }

@@ -377,29 +377,40 @@ struct VocabArgs {
   int splits;
   int v0, vp;                       // the piece: its first row of W and how many
 };
-enum VocabTile { VOCAB_TILE_128, VOCAB_TILE_64, VOCAB_TILE_32x64 };
+enum VocabTile {
+  VOCAB_TILE_256,    // k_vocab_loss_pipe.hip
+  VOCAB_TILE_BIG,    // 128 x 128, fp32 128 x 64
+  VOCAB_TILE_64, VOCAB_TILE_32x64
+};
+struct VocabTiles {
+  int tile, splits;
+  double cost;
+};
 struct VocabPlan {
-  int tile, groups;
+  VocabTiles lay[2];   // without and with 256 x 256 tiles
+  int groups;
   long long rows;   // tokens of a launch
   size_t bytes;
 };
 struct VocabBackPlan {
-  long long Tm, ldm, ldp, lda, pieces;
-  int vp, grad_tile, dx_tile, dw_tile, splits;
+  long long Tm, ldm, lda;
+  int vp;
+  VocabTiles dx[2];   // without and with 256 x 256 tiles
   bool acc;
   size_t at_x, at_acc, bytes;
 };
 constexpr int kVocabMax = 1 << 24;        // tokens of a call, rows of W
 constexpr int kVocabMaxDim = 1 << 16;
 // by the sizes alone
-VocabPlan vocab_forward_plan(long long T, int V, int n);
+VocabPlan vocab_forward_plan(long long T, int V, int n, int bf16);
 VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, bool gw);
 hipError_t launch_vocab_forward(const VocabArgs& a, int bf16, void* ws, hipStream_t s);
 hipError_t launch_vocab_backward(const VocabArgs& a, int bf16, void* ws, hipStream_t s);
 // 256 x 256 tiles with one load pipeline (k_vocab_loss_pipe.hip), bf16: whether the operands'
 // sizes and alignment allow them, and the launches
 bool vocab_pipe_logits(const VocabArgs& a);
-bool vocab_pipe_dx(const VocabArgs& a);
+bool vocab_pipe_dx(long long T, int n);
+bool vocab_pipe_weight(const VocabArgs& a);
 bool vocab_pipe_dw(const VocabArgs& a);
 hipError_t launch_vocab_pipe_stats(const VocabArgs& a, hipStream_t s);
 hipError_t launch_vocab_pipe_grad(const VocabArgs& a, hipStream_t s);

@@ -141,7 +141,7 @@ poetx_status poetx_layer_norm_backward(const poetx_layer_norm_backward_desc* d, 
 
 size_t poetx_linear_cross_entropy_workspace(const poetx_cross_entropy_desc* d) {
   if (vocab_desc(d) != POETX_OK || d->T == 0) return 0;
-  return poetx::vocab_forward_plan(d->T, d->V, d->n).bytes;
+  return poetx::vocab_forward_plan(d->T, d->V, d->n, d->dtype == POETX_BF16).bytes;
 }
 
 poetx_status poetx_linear_cross_entropy(const poetx_cross_entropy_desc* d, const void* X, const void* W,

@@ -33,26 +33,27 @@ using namespace vocab;
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThr = 256;
-constexpr int kKB = 128;   // bytes of the summed axis a stage
 
-// An operand: R rows (of the result's axis) by 128 bytes of the summed axis a stage
-template <typename Ty, int R, bool ACROSS>
+// An operand: R rows (of the result's axis) by KB bytes of the summed axis a stage
+template <typename Ty, int R, int KB, bool ACROSS>
 struct Operand;
 
 // rows along the summed axis
-template <typename Ty, int R>
-struct Operand<Ty, R, false> {
-  static constexpr int ES = Ty::kSize, L = R / 32, BYTES = R * kKB;
+template <typename Ty, int R, int KB>
+struct Operand<Ty, R, KB, false> {
+  static constexpr int CPR = KB / 16, RPL = kThr / CPR;   // chunks of a row, rows a load
+  static constexpr int ES = Ty::kSize, L = R / RPL, BYTES = R * KB;
+  static_assert(L * RPL == R, "whole loads");
   const char* p[L];
   __device__ __forceinline__ void init(const void* base, long long ld, int r0, int rows, int) {
 #pragma unroll
     for (int i = 0; i < L; ++i)
-      p[i] = static_cast<const char*>(base) + (long long)min(r0 + i * 32 + (int)threadIdx.x / 8, rows - 1) * ld * ES;
+      p[i] = static_cast<const char*>(base) + (long long)min(r0 + i * RPL + (int)threadIdx.x / CPR, rows - 1) * ld * ES;
   }
   // of the stage from element k0 on; zero from kend on
   __device__ __forceinline__ void fetch(i32x4 (&r)[L], int k0, int kend) const {
-    const long long k = (long long)k0 * ES + (threadIdx.x % 8) * 16, kb = (long long)kend * ES;
-    if (k0 + kKB / ES <= kend) {
+    const long long k = (long long)k0 * ES + (threadIdx.x % CPR) * 16, kb = (long long)kend * ES;
+    if (k0 + KB / ES <= kend) {
 #pragma unroll
       for (int i = 0; i < L; ++i) __builtin_memcpy(&r[i], p[i] + k, 16);
     } else {
@@ -60,11 +61,11 @@ struct Operand<Ty, R, false> {
       for (int i = 0; i < L; ++i) r[i] = load16<ES>(p[i], k, kb);
     }
   }
-  static __device__ __forceinline__ int slot(int r, int c) { return r * 8 + (c ^ ((r / 2) & 7)); }
+  static __device__ __forceinline__ int slot(int r, int c) { return r * CPR + (c ^ (CPR == 8 ? (r / 2) & 7 : r & (CPR - 1))); }
   static __device__ __forceinline__ void keep(char* st, const i32x4 (&r)[L]) {
 #pragma unroll
     for (int i = 0; i < L; ++i)
-      reinterpret_cast<i32x4*>(st)[slot(i * 32 + (int)threadIdx.x / 8, (int)threadIdx.x % 8)] = r[i];
+      reinterpret_cast<i32x4*>(st)[slot(i * RPL + (int)threadIdx.x / CPR, (int)threadIdx.x % CPR)] = r[i];
   }
   // 16 bytes along the summed axis of row r + (lane & 15), chunk 4 q + (lane >> 4)
   static __device__ __forceinline__ i32x4 frag(const char* st, int r, int q, int lane) {
@@ -73,10 +74,10 @@ struct Operand<Ty, R, false> {
 };
 
 // rows across it
-template <typename Ty, int R>
-struct Operand<Ty, R, true> {
-  static constexpr int ES = Ty::kSize, L = R / 32, K = kKB / ES;
-  static constexpr int CPR = R * ES / 16, RPL = kThr / CPR;   // chunks of a summed row, summed rows a load
+template <typename Ty, int R, int KB>
+struct Operand<Ty, R, KB, true> {
+  static constexpr int ES = Ty::kSize, K = KB / ES;
+  static constexpr int CPR = R * ES / 16, RPL = kThr / CPR, L = K / RPL;   // chunks of a summed row, summed rows a load
   static constexpr int PITCH = R * ES + (ES == 2 ? 32 : 16), BYTES = K * PITCH + (ES == 2 ? K / 8 * 128 : 0);
   static_assert(RPL * L == K, "whole loads");
   const char* p;   // the first summed row's first chunk of this thread
@@ -131,10 +132,15 @@ struct Operand<Ty, R, true> {
 
 enum Mode { STATS, GRAD, DX, DW };
 
+// Bytes of the summed axis a stage: twice as many for the smallest tiles, which leave the
+// memory too few loads otherwise (16 tokens, 32000 x 2048 36.4 -> 35.6 us, 3000 x 512 15.6 ->
+// 13.1)
+constexpr int stage_bytes(int bm) { return bm == 32 ? 256 : 128; }
 template <typename Ty, int BM, int BN, Mode M>
 struct Tile {
-  using A = Operand<Ty, BM, M == DW>;
-  using B = Operand<Ty, BN, M == DX || M == DW>;
+  static constexpr int KB = stage_bytes(BM);
+  using A = Operand<Ty, BM, KB, M == DW>;
+  using B = Operand<Ty, BN, KB, M == DX || M == DW>;
   static constexpr int STAGE = A::BYTES + B::BYTES;
   static_assert(STAGE % 16 == 0 && A::BYTES % 16 == 0, "16-byte pieces");
 };
@@ -172,7 +178,8 @@ void vocab_tile_kernel(VocabArgs a) {
   using OA = typename Cfg::A;
   using OB = typename Cfg::B;
   constexpr bool F32 = Ty::kSize == 4;
-  constexpr int KE = kKB / Ty::kSize;          // elements of the summed axis a stage
+  constexpr int KE = Cfg::KB / Ty::kSize;      // elements of the summed axis a stage
+  constexpr int Q = Cfg::KB / 64;              // 64-byte slabs of it
   constexpr int TM = BM / 32, TN = BN / 32;    // 16 x 16 tiles of a wave
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -213,15 +220,15 @@ void vocab_tile_kernel(VocabArgs a) {
   auto read = [&](int buf, int q) __attribute__((always_inline)) {
     const char* const st = lds + buf * Cfg::STAGE;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) af[q][i] = OA::frag(st, wm + i * 16, q, lane);
+    for (int i = 0; i < TM; ++i) af[q & 1][i] = OA::frag(st, wm + i * 16, q, lane);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) bf[q][j] = OB::frag(st + OA::BYTES, wn + j * 16, q, lane);
+    for (int j = 0; j < TN; ++j) bf[q & 1][j] = OB::frag(st + OA::BYTES, wn + j * 16, q, lane);
   };
   auto multiply = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < TN; ++j) Ty::mma(bf[q][j], af[q][i], acc[i][j]);
+      for (int j = 0; j < TN; ++j) Ty::mma(bf[q & 1][j], af[q & 1][i], acc[i][j]);
   };
   const int stages = (kend - k0 + KE - 1) / KE;
   if (stages > 0) {
@@ -235,11 +242,16 @@ void vocab_tile_kernel(VocabArgs a) {
       // nobody reads the other buffer since the barrier of the stage before
       if (s + 1 < stages) keep(buf ^ 1, buf ^ 1);
       if (s + 3 < stages) fetch(k0 + (s + 3) * KE, buf ^ 1);
-      read(buf, 1);
-      multiply(0);
-      lds_sync();
-      if (s + 1 < stages) read(buf ^ 1, 0);
-      multiply(1);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        if (q + 1 < Q) {
+          read(buf, q + 1);
+        } else {
+          lds_sync();
+          if (s + 1 < stages) read(buf ^ 1, 0);
+        }
+        multiply(q);
+      }
     };
     for (int s = 0; s < stages; s += 2) {
       stage(s, 0);
@@ -324,6 +336,95 @@ void vocab_tile_kernel(VocabArgs a) {
       }
     }
   }
+}
+
+// Forward for the fewest tokens, TT of them: every wave multiplies kFewRows rows of W by all
+// of X on the vector units, 32 rows to a workgroup and its part. Bound by W's bytes: one
+// token, 32000 rows of 2048 bf16 that no cache holds 29 us with the join (5.3 TB/s in this
+// kernel). The whole 32 KB of a wave's rows are asked for at once: half of them 33 us, four
+// rows 30.5 us, four rows by halves 35 us. (Four tokens 41 us, in tiles 36.)
+constexpr int kFew = 2, kFewRows = 8, kFewGroup = kThr / 64 * kFewRows;
+template <typename Ty, int TT>
+__global__ __launch_bounds__(kThr) void vocab_few_kernel(VocabArgs a) {
+  constexpr bool F32 = Ty::kSize == 4;
+  constexpr int R = kFewRows, U = 4;
+  __shared__ float2 red[kThr / 64][TT];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int v0 = (int)blockIdx.x * kFewGroup + wave * R;
+  const long long kb = (long long)a.n * Ty::kSize, k = lane * 16;
+  const char *w[R], *x[TT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    w[r] = static_cast<const char*>(a.W) + (long long)min(v0 + r, a.V - 1) * a.ldw * Ty::kSize;
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+    x[t] = static_cast<const char*>(a.X) + min((long long)t, a.T - 1) * a.ldx * Ty::kSize;
+  float z[R][TT] = {};
+  long long p = 0;
+  for (; p + 1024 * U <= kb; p += 1024 * U) {
+    i32x4 wv[U][R], xv[U][TT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) __builtin_memcpy(&wv[u][r], w[r] + p + k + u * 1024, 16);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) __builtin_memcpy(&xv[u][t], x[t] + p + k + u * 1024, 16);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) Ty::dot(wv[u][r], xv[u][t], z[r][t]);
+  }
+  for (; p < kb; p += 1024) {
+    i32x4 wv[R], xv[TT];
+#pragma unroll
+    for (int r = 0; r < R; ++r) wv[r] = load16<Ty::kSize>(w[r], p + k, kb);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) xv[t] = load16<Ty::kSize>(x[t], p + k, kb);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) Ty::dot(wv[r], xv[t], z[r][t]);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) z[r][t] += __shfl_xor(z[r][t], o);
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    float m = -__builtin_inff(), s = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (v0 + r < a.V) m = fmaxf(m, z[r][t]);
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (v0 + r < a.V) s += exp_of<F32>(z[r][t] - base);
+    if (lane == 0) {
+      red[wave][t] = float2{m, s};
+      if (t < a.T) {
+        const long long target = a.target[t];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (v0 + r == target && target < a.V) a.zt[t] = z[r][t];
+      }
+    }
+  }
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t >= TT || t >= a.T) return;
+  float m = red[0][t].x, s = 0.0f;
+#pragma unroll
+  for (int i = 1; i < kThr / 64; ++i) m = fmaxf(m, red[i][t].x);
+  const float base = m == -__builtin_inff() ? 0.0f : m;
+  // an empty or all -inf part has s = 0 and adds 0 exp(-inf); one with a NaN keeps it
+#pragma unroll
+  for (int i = 0; i < kThr / 64; ++i) s += red[i][t].y * exp_of<F32>(red[i][t].x - base);
+  a.part[t * (long long)gridDim.x + blockIdx.x] = float2{m, s};
 }
 
 // A row's lse and loss from the parts of its columns, by G lanes a row
@@ -414,6 +515,16 @@ __global__ __launch_bounds__(kThr) void vocab_finish_kernel(VocabArgs a) {
   }
 }
 
+template <typename Ty, int TT>
+hipError_t few(const VocabArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((vocab_few_kernel<Ty, TT>), dim3((unsigned)((a.V + kFewGroup - 1) / kFewGroup)), dim3(kThr), 0, s, a);
+  return hipGetLastError();
+}
+template <typename Ty>
+hipError_t few(const VocabArgs& a, hipStream_t s) {
+  return a.T == 1 ? few<Ty, 1>(a, s) : few<Ty, 2>(a, s);
+}
+
 // V rows of n elements of zeros (4 or 2 bytes each)
 template <typename E>
 __global__ __launch_bounds__(kThr) void vocab_zero_kernel(E* p, int V, int n, long long ld) {
@@ -486,7 +597,7 @@ VocabTiles cheapest(const TileCost (&costs)[N], long long rows, long long cols, 
 }
 // wide: whether 256 x 256 tiles may be taken
 VocabTiles tiles_of(long long rows, long long cols, long long sum, int bf16, bool wide, bool share = false) {
-  const long long stages = (sum * (bf16 ? 2 : 4) + kKB - 1) / kKB;
+  const long long stages = (sum * (bf16 ? 2 : 4) + 127) / 128;
   return bf16 ? cheapest(kBf16, rows, cols, stages, wide, share) : cheapest(kF32, rows, cols, stages, false, share);
 }
 int group_cols(int tile, int bf16) { return tile == VOCAB_TILE_BIG && bf16 ? 64 : 32; }
@@ -508,7 +619,7 @@ VocabPlan vocab_forward_plan(long long T, int V, int n, int bf16) {
   // as the operands' alignment may lead: 256 x 256 tiles (parts of 64 columns, whole tiles of them) or not
   p.lay[0] = tiles_of(T, V, n, bf16, false);
   p.lay[1] = tiles_of(T, V, n, bf16, bf16 && T >= 256 && V >= 256);
-  const int cols = group_cols(p.lay[0].tile, bf16);
+  const int cols = T <= kFew ? kFewGroup : group_cols(p.lay[0].tile, bf16);
   p.groups = std::max((V + cols - 1) / cols, p.lay[1].tile == VOCAB_TILE_256 ? (V + 255) / 256 * 4 : 0);
   // tokens of a launch: as many as their parts leave room for, and their tiles can be counted
   const long long most = std::min(kRoom / (8LL * p.groups), (1LL << 33) / V);
@@ -533,7 +644,10 @@ hipError_t launch_vocab_forward(const VocabArgs& in, int bf16, void* ws, hipStre
     a.vp = a.V;
     int groups;
     hipError_t e;
-    if (p.lay[1].tile == VOCAB_TILE_256 && vocab_pipe_logits(a)) {
+    if (in.T <= kFew) {
+      groups = p.groups;
+      e = bf16 ? few<TypeBf16>(a, s) : few<TypeF32>(a, s);
+    } else if (p.lay[1].tile == VOCAB_TILE_256 && vocab_pipe_logits(a)) {
       groups = (a.V + 255) / 256 * 4;
       e = launch_vocab_pipe_stats(a, s);
     } else {
@@ -568,7 +682,7 @@ VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, 
   p.dx[1] = tiles_of(T, n, vp, bf16, bf16 && vocab_pipe_dx(T, n), true);
   // shares none of which is empty in the first piece (the others only add to theirs)
   for (VocabTiles& d : p.dx) {
-    const long long stages = ((long long)vp * es + kKB - 1) / kKB, per = (stages + d.splits - 1) / d.splits;
+    const long long stages = ((long long)vp * es + 127) / 128, per = (stages + d.splits - 1) / d.splits;
     d.splits = (int)((stages + per - 1) / per);
   }
   const int splits = std::max(p.dx[0].splits, p.dx[1].splits);

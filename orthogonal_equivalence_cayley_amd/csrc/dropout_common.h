@@ -45,16 +45,27 @@ __device__ __forceinline__ Bits bits(Key k, uint32_t block, uint32_t row, uint32
   return Bits{{c0, c1, c2, c3}};
 }
 
-// The factor 0 or scale of N (8, or 4: one half of the 8) elements from column c0 of a
-// row on, by selection: a dropped infinity or NaN is 0.
+// Which of N (8, or 4: one half of the 8) elements from column c0 of a row on are kept, as bits
 template <int N>
-__device__ __forceinline__ void apply(const DropArgs& d, Key k, uint32_t row, int c0, float (&x)[N]) {
+__device__ __forceinline__ uint32_t kept(const DropArgs& d, Key k, uint32_t row, int c0) {
   static_assert(N == 8 || N == 4, "whole counters or halves");
   const Bits b = bits(k, (uint32_t)c0 >> 3, row, d.site);
   const bool upper = N == 4 && (c0 & 4);
   const Bits m = upper ? Bits{{b.w[2], b.w[3], 0, 0}} : b;
+  uint32_t keep = 0;
 #pragma unroll
-  for (int e = 0; e < N; ++e) x[e] = m.of(e) >= d.threshold ? x[e] * d.scale : 0.0f;
+  for (int e = 0; e < N; ++e) keep |= m.of(e) >= d.threshold ? 1u << e : 0u;
+  return keep;
+}
+// The factor 0 or scale, by selection: a dropped infinity or NaN is 0
+template <int N>
+__device__ __forceinline__ void apply(const DropArgs& d, uint32_t keep, float (&x)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) x[e] = keep >> e & 1 ? x[e] * d.scale : 0.0f;
+}
+template <int N>
+__device__ __forceinline__ void apply(const DropArgs& d, Key k, uint32_t row, int c0, float (&x)[N]) {
+  apply(d, kept<N>(d, k, row, c0), x);
 }
 
 }  // namespace drop

@@ -9,9 +9,8 @@
 //
 // Bound by memory: 8 bytes a bf16 element forward (x, r, h, y), 8 backward (g, gh, h,
 // dx) and 10 with dropout, whose dx is not dr. A row is read once and stays in
-// registers, the mean and then the squares around it summed from there; one wave, four
-// or sixteen to a row, every load of a row (and, backward, of the next row) out before
-// the first is used.
+// registers; one wave, four or sixteen to a row, every load of a row (and, backward, of
+// the next row) out before the first is used.
 #include <algorithm>
 #include <type_traits>
 
@@ -27,105 +26,155 @@ using namespace row;
 constexpr int kThr = 256;
 constexpr int threads(int wpr) { return wpr > 4 ? wpr * 64 : kThr; }
 
+template <typename V>
+struct Two {
+  V a, b;
+};
+// the sums of both over the WPR waves of a row, as row_reduce
+template <int WPR, typename V>
+__device__ __forceinline__ Two<V> row_sums(Two<V> v, Two<V>* red) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    v.a += __shfl_xor(v.a, o);
+    v.b += __shfl_xor(v.b, o);
+  }
+  if constexpr (WPR > 1) {
+    __syncthreads();   // the last use of `red` is over
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) {
+      v.a += red[i].a;
+      v.b += red[i].b;
+    }
+  }
+  return v;
+}
+
+// Mean and variance come from one pass, sums of h - c and its square in 64 bits: their
+// order then does not show in the fp32 results, so the INT8 decisions are the same for
+// every split of a row over lanes. c is a value of the row's own size (its first x + r; any
+// finite number would do), so that a row far from zero keeps its variance.
+__device__ __forceinline__ double center(float x, float r) {
+  const float c = x + r;
+  return fabsf(c) < __builtin_inff() ? (double)c : 0.0;
+}
+struct Stats {
+  float m0, m1;   // the mean as two floats: a row far from zero keeps the digits of h - m
+  float s;
+};
+__device__ __forceinline__ Stats stats_of(Two<double> sums, double c, const LayerNormArgs& a) {
+  const double d = sums.a / (double)a.dim, m = c + d, var = sums.b / (double)a.dim - d * d;
+  Stats r;
+  r.m0 = (float)m;
+  r.m1 = (float)(m - (double)r.m0);
+  // rounding may leave a constant row's variance a little below zero; a NaN stays
+  r.s = (float)(1.0 / sqrt((var < 0.0 ? 0.0 : var) + a.eps));
+  return r;
+}
+
+// A workgroup takes rows a stride apart, w and b of its columns in registers (read for every
+// row from the caches they are as many bytes as x and r: 16384 x 2048 bf16, one wave a row,
+// 56 -> 45 us); the next row's loads are in flight while a row is worked on.
 template <typename E, int NV, int WPR, bool WHOLE, bool DROP>
 __global__ __launch_bounds__(threads(WPR)) void add_layer_norm_kernel(LayerNormArgs a) {
   constexpr int N = 16 / sizeof(E);
   constexpr int RPW = threads(WPR) / 64 / WPR;   // rows per workgroup
   constexpr int STEP = 64 * WPR * N;             // columns between a lane's vectors
-  __shared__ double red[WPR];
+  __shared__ Two<double> red[WPR];
   __shared__ uint32_t redu[WPR];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const long long t = (long long)blockIdx.x * RPW + wave / WPR;
-  if (t >= a.T) return;   // whole rows: with more waves to a row the workgroup has one
   const int c0 = ((wave % WPR) * 64 + lane) * N;
   const bool full = a.dim >= N;
-  const E* x = static_cast<const E*>(a.X) + t * a.ldx + c0;
-  E xr[NV][N], rr[NV][N];
+  float w[NV][N], b[NV][N];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) xr[i][e] = rr[i][e] = E(0);
-    if (c0 + i * STEP < a.dim) load_raw<WHOLE>(x + i * STEP, a.dim - c0 - i * STEP, full, xr[i]);
+    for (int e = 0; e < N; ++e) w[i][e] = b[i][e] = 0.0f;
+    if (c0 + i * STEP < a.dim) {
+      load_raw<WHOLE>(a.w + c0 + i * STEP, a.dim - c0 - i * STEP, full, w[i]);
+      if (a.b) load_raw<WHOLE>(a.b + c0 + i * STEP, a.dim - c0 - i * STEP, full, b[i]);
+    }
   }
-  if (a.R) {
-    const E* r = static_cast<const E*>(a.R) + t * a.ldr + c0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (c0 + i * STEP < a.dim) load_raw<WHOLE>(r + i * STEP, a.dim - c0 - i * STEP, full, rr[i]);
-  }
-  float h[NV][N];
-  double sum = 0.0;
   [[maybe_unused]] drop::Key key{};
   if constexpr (DROP) key = drop::key_of(a.drop);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) h[i][e] = to_f(xr[i][e]);
-    if constexpr (DROP) drop::apply(a.drop, key, a.row0 + (uint32_t)t, c0 + i * STEP, h[i]);
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      // rounded to the type before the norm: the kept h is what the norm sees
-      if (a.R || DROP) h[i][e] = to_f(from_f<E>(a.R ? h[i][e] + to_f(rr[i][e]) : h[i][e]));
-      sum += (double)h[i][e];
-    }
-  }
-  if (a.H) {
-    E* ho = static_cast<E*>(a.H) + t * a.ldh + c0;
+  E xr[NV][N] = {}, rr[NV][N] = {}, x0 = E(0), r0 = E(0);
+  auto fetch = [&](long long t) {
+    const E* x = static_cast<const E*>(a.X) + t * a.ldx;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (c0 + i * STEP < a.dim) store_n<WHOLE>(ho + i * STEP, a.dim - c0 - i * STEP, h[i]);
-  }
-  // statistics in 64 bits: their order does not show in m and s, so the INT8 decisions
-  // are the same for every split of a row over lanes
-  const double m = row_reduce<WPR>(sum, red, Add{}) / (double)a.dim;
-  // the mean as two floats: a row far from zero keeps the digits of h - m
-  const float m0 = (float)m, m1 = (float)(m - (double)m0);
-  double ss = 0.0;
+      if (c0 + i * STEP < a.dim) load_raw<WHOLE>(x + c0 + i * STEP, a.dim - c0 - i * STEP, full, xr[i]);
+    x0 = *x;
+    if (a.R) {
+      const E* r = static_cast<const E*>(a.R) + t * a.ldr;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int left = a.dim - c0 - i * STEP;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const double d = (double)h[i][e] - m;
-      if (WHOLE ? left > 0 : e < left) ss += d * d;
-      h[i][e] = (h[i][e] - m0) - m1;
+      for (int i = 0; i < NV; ++i)
+        if (c0 + i * STEP < a.dim) load_raw<WHOLE>(r + c0 + i * STEP, a.dim - c0 - i * STEP, full, rr[i]);
+      r0 = *r;
     }
-  }
-  ss = row_reduce<WPR>(ss, red, Add{});
-  const float s = (float)(1.0 / sqrt(ss / (double)a.dim + a.eps));
-  if (lane == 0 && wave % WPR == 0) {
-    if (a.mean) a.mean[t] = m0;
-    if (a.rstd) a.rstd[t] = s;
-  }
-  uint32_t amax = 0;
+  };
+  const long long stride = (long long)gridDim.x * RPW;
+  long long t = (long long)blockIdx.x * RPW + wave / WPR;
+  if (t < a.T) fetch(t);
+  for (; t < a.T; t += stride) {   // whole rows: with more waves to a row the workgroup has one
+    float h[NV][N];
+    Two<double> sum{0.0, 0.0};
+    const double c = center(to_f(x0), to_f(r0));
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int left = a.dim - c0 - i * STEP;
-    if (left <= 0) continue;
-    float w[N], b[N] = {};
-    load_raw<WHOLE>(a.w + c0 + i * STEP, left, full, w);
-    if (a.b) load_raw<WHOLE>(a.b + c0 + i * STEP, left, full, b);
+    for (int i = 0; i < NV; ++i) {
+      const int left = a.dim - c0 - i * STEP;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      h[i][e] = (h[i][e] * s) * w[e] + b[e];
-      // behind the row's end stands -m s
-      if (WHOLE || e < left) amax = max(amax, __float_as_uint(h[i][e]) & 0x7fffffffu);
+      for (int e = 0; e < N; ++e) h[i][e] = to_f(xr[i][e]);
+      if constexpr (DROP) drop::apply(a.drop, key, a.row0 + (uint32_t)t, c0 + i * STEP, h[i]);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        // rounded to the type before the norm: the kept h is what the norm sees
+        if (a.R || DROP) h[i][e] = to_f(from_f<E>(a.R ? h[i][e] + to_f(rr[i][e]) : h[i][e]));
+        const double d = (WHOLE ? left > 0 : e < left) ? (double)h[i][e] - c : 0.0;
+        sum.a += d;
+        sum.b += d * d;
+      }
     }
-    if (!a.quant) store_n<WHOLE>(static_cast<E*>(a.Y) + t * a.ldy + c0 + i * STEP, left, h[i]);
-  }
-  if (!a.quant) return;
-  amax = row_reduce<WPR>(amax, redu, Max{});
-  float inv, scale;
-  int8_rule(amax, inv, scale);
-  if (lane == 0 && wave % WPR == 0) a.scale[t] = scale;
+    if (t + stride < a.T) fetch(t + stride);
+    const Stats st = stats_of(row_sums<WPR>(sum, red), c, a);
+    // behind the sums' barrier: H may lie over the first x or r, which every wave reads
+    if (a.H) {
+      E* ho = static_cast<E*>(a.H) + t * a.ldh + c0;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int left = a.dim - c0 - i * STEP;
-    if (left <= 0) continue;
-    int8_t q[N];
+      for (int i = 0; i < NV; ++i)
+        if (c0 + i * STEP < a.dim) store_n<WHOLE>(ho + i * STEP, a.dim - c0 - i * STEP, h[i]);
+    }
+    if (lane == 0 && wave % WPR == 0) {
+      if (a.mean) a.mean[t] = st.m0;
+      if (a.rstd) a.rstd[t] = st.s;
+    }
+    uint32_t amax = 0;
 #pragma unroll
-    for (int e = 0; e < N; ++e) q[e] = to_q(h[i][e], inv);
-    store_raw<WHOLE>(static_cast<int8_t*>(a.Y) + t * a.ldy + c0 + i * STEP, left, q);
+    for (int i = 0; i < NV; ++i) {
+      const int left = a.dim - c0 - i * STEP;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        h[i][e] = (((h[i][e] - st.m0) - st.m1) * st.s) * w[i][e] + b[i][e];
+        // behind the row's end stands -m s times 0
+        if (WHOLE ? left > 0 : e < left) amax = max(amax, __float_as_uint(h[i][e]) & 0x7fffffffu);
+      }
+      if (!a.quant && left > 0) store_n<WHOLE>(static_cast<E*>(a.Y) + t * a.ldy + c0 + i * STEP, left, h[i]);
+    }
+    if (!a.quant) continue;
+    amax = row_reduce<WPR>(amax, redu, Max{});
+    float inv, scale;
+    int8_rule(amax, inv, scale);
+    if (lane == 0 && wave % WPR == 0) a.scale[t] = scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int left = a.dim - c0 - i * STEP;
+      if (left <= 0) continue;
+      int8_t q[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e) q[e] = to_q(h[i][e], inv);
+      store_raw<WHOLE>(static_cast<int8_t*>(a.Y) + t * a.ldy + c0 + i * STEP, left, q);
+    }
   }
 }
 
@@ -136,7 +185,7 @@ constexpr int kLongWaves = 16;
 template <typename E, bool DROP>
 __global__ __launch_bounds__(kLongWaves * 64) void add_layer_norm_long_kernel(LayerNormArgs a) {
   constexpr int N = 16 / sizeof(E), STEP = kLongWaves * 64 * N;
-  __shared__ double red[kLongWaves];
+  __shared__ Two<double> red[kLongWaves];
   __shared__ uint32_t redu[kLongWaves];
   const long long t = blockIdx.x;
   const E* x = static_cast<const E*>(a.X) + t * a.ldx;
@@ -160,13 +209,19 @@ __global__ __launch_bounds__(kLongWaves * 64) void add_layer_norm_long_kernel(La
 #pragma unroll
     for (int e = 0; e < N; ++e) h[e] = to_f(from_f<E>(h[e]));
   };
-  double sum = 0.0;
+  Two<double> sum{0.0, 0.0};
+  const double mid = center(to_f(x[0]), r ? to_f(r[0]) : 0.0f);
+  __syncthreads();   // H may lie over the first x or r
   for (int c = first; c < a.dim; c += STEP) {
     float h[N];
     make(c, h);
     if (ho) store_n<false>(ho + c, a.dim - c, h);
 #pragma unroll
-    for (int e = 0; e < N; ++e) sum += e < a.dim - c ? (double)h[e] : 0.0;
+    for (int e = 0; e < N; ++e) {
+      const double d = e < a.dim - c ? (double)h[e] - mid : 0.0;
+      sum.a += d;
+      sum.b += d * d;
+    }
   }
   // A thread reads back only what it wrote itself: a row's cut vector is not read from
   // the vector in front of it, which another thread may not have written yet.
@@ -183,23 +238,10 @@ __global__ __launch_bounds__(kLongWaves * 64) void add_layer_norm_long_kernel(La
       for (int e = 0; e < N; ++e) h[e] = e < a.dim - c ? to_f(ho[c + e]) : 0.0f;
     }
   };
-  const double m = row_reduce<kLongWaves>(sum, red, Add{}) / (double)a.dim;
-  const float m0 = (float)m, m1 = (float)(m - (double)m0);
-  double ss = 0.0;
-  for (int c = first; c < a.dim; c += STEP) {
-    float h[N];
-    value(c, h);
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const double d = (double)h[e] - m;
-      ss += e < a.dim - c ? d * d : 0.0;
-    }
-  }
-  ss = row_reduce<kLongWaves>(ss, red, Add{});
-  const float s = (float)(1.0 / sqrt(ss / (double)a.dim + a.eps));
+  const Stats st = stats_of(row_sums<kLongWaves>(sum, red), mid, a);
   if (threadIdx.x == 0) {
-    if (a.mean) a.mean[t] = m0;
-    if (a.rstd) a.rstd[t] = s;
+    if (a.mean) a.mean[t] = st.m0;
+    if (a.rstd) a.rstd[t] = st.s;
   }
   auto normed = [&](int c, float (&y)[N]) {
     float w[N], b[N] = {};
@@ -207,7 +249,7 @@ __global__ __launch_bounds__(kLongWaves * 64) void add_layer_norm_long_kernel(La
     load_raw<false>(a.w + c, a.dim - c, true, w);
     if (a.b) load_raw<false>(a.b + c, a.dim - c, true, b);
 #pragma unroll
-    for (int e = 0; e < N; ++e) y[e] = (((y[e] - m0) - m1) * s) * w[e] + b[e];
+    for (int e = 0; e < N; ++e) y[e] = (((y[e] - st.m0) - st.m1) * st.s) * w[e] + b[e];
   };
   uint32_t amax = 0;
   for (int c = first; c < a.dim; c += STEP) {
@@ -233,31 +275,6 @@ __global__ __launch_bounds__(kLongWaves * 64) void add_layer_norm_long_kernel(La
   }
 }
 
-struct Two {
-  float a, b;
-};
-// the sums of both over the WPR waves of a row, as row_reduce
-template <int WPR>
-__device__ __forceinline__ Two row_sums(Two v, Two* red) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    v.a += __shfl_xor(v.a, o);
-    v.b += __shfl_xor(v.b, o);
-  }
-  if constexpr (WPR > 1) {
-    __syncthreads();   // the last use of `red` is over
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int i = 1; i < WPR; ++i) {
-      v.a += red[i].a;
-      v.b += red[i].b;
-    }
-  }
-  return v;
-}
-
 // Where the partial sums of a workgroup go: one row of 2 dim values each, or, for a
 // single workgroup, the sums themselves
 __device__ __forceinline__ void part_rows(const LayerNormBackArgs& a, int block, float*& pw, float*& pb) {
@@ -265,16 +282,16 @@ __device__ __forceinline__ void part_rows(const LayerNormBackArgs& a, int block,
   pb = a.part ? pw + a.dim : a.db;
 }
 
-// Backward: each wave (WPR = 1) or workgroup (WPR = 4) takes rows a stride apart and
+// Backward: each wave (WPR = 1) or workgroup (WPR = 4, 8) takes rows a stride apart and
 // keeps its columns' parts of dw and db in registers, in 64 bits (sums over any number
 // of rows: fp32 would lose small terms behind large ones); the parts of a workgroup's
 // waves are joined in LDS. The next row's loads are in flight while a row is worked on.
 template <typename E, int NV, int WPR, bool WHOLE, bool DROP>
-__global__ __launch_bounds__(kThr) void layer_norm_backward_kernel(LayerNormBackArgs a) {
+__global__ __launch_bounds__(threads(WPR)) void layer_norm_backward_kernel(LayerNormBackArgs a) {
   constexpr int N = 16 / sizeof(E);
-  constexpr int RPW = kThr / 64 / WPR;
+  constexpr int RPW = threads(WPR) / 64 / WPR;
   constexpr int STEP = 64 * WPR * N;
-  __shared__ Two red[4];
+  __shared__ Two<float> red[WPR];
   extern __shared__ double lds[];   // WPR = 1: 2 dim values
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int c0 = ((wave % WPR) * 64 + lane) * N;
@@ -312,7 +329,7 @@ __global__ __launch_bounds__(kThr) void layer_norm_backward_kernel(LayerNormBack
   for (; t < a.T; t += stride) {
     const float m = mn, s = sn;
     float gv[NV][N], u[NV][N], q[NV][N];
-    Two dot{0.0f, 0.0f};
+    Two<float> dot{0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       // behind the row's end g is zero and u a finite number or NaN: not summed
@@ -331,6 +348,13 @@ __global__ __launch_bounds__(kThr) void layer_norm_backward_kernel(LayerNormBack
       }
     }
     if (t + stride < a.T) fetch(t + stride);
+    // the generator runs while waves wait for each other (a wave of its own waits for none:
+    // 8000 x 768 bf16 30 us with it here, 23 behind the sums)
+    [[maybe_unused]] uint32_t keep[NV];
+    if constexpr (DROP && WPR > 1) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) keep[i] = drop::kept<N>(a.drop, key, (uint32_t)t, c0 + i * STEP);
+    }
     dot = row_sums<WPR>(dot, red);
     const float ca = dot.a / (float)a.dim, cb = dot.b / (float)a.dim;
     E* o = static_cast<E*>(a.GX) + t * a.ldgx + c0;
@@ -341,7 +365,8 @@ __global__ __launch_bounds__(kThr) void layer_norm_backward_kernel(LayerNormBack
       for (int e = 0; e < N; ++e) gv[i][e] = s * (gv[i][e] - ca - u[i][e] * cb) + q[i][e];
       if constexpr (DROP) {
         if (ro && c0 + i * STEP < a.dim) store_n<WHOLE>(ro + i * STEP, a.dim - c0 - i * STEP, gv[i]);
-        drop::apply(a.drop, key, (uint32_t)t, c0 + i * STEP, gv[i]);
+        if constexpr (WPR > 1) drop::apply(a.drop, keep[i], gv[i]);
+        else drop::apply(a.drop, key, (uint32_t)t, c0 + i * STEP, gv[i]);
       }
       if (c0 + i * STEP < a.dim) store_n<WHOLE>(o + i * STEP, a.dim - c0 - i * STEP, gv[i]);
     }
@@ -392,12 +417,12 @@ __global__ __launch_bounds__(kThr) void layer_norm_backward_kernel(LayerNormBack
 template <typename E>
 __global__ __launch_bounds__(kLongWaves * 64) void layer_norm_means_kernel(LayerNormBackArgs a) {
   constexpr int N = 16 / sizeof(E);
-  __shared__ Two red[kLongWaves];
+  __shared__ Two<float> red[kLongWaves];
   for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
     const E* g = static_cast<const E*>(a.G) + t * a.ldg;
     const E* h = static_cast<const E*>(a.H) + t * a.ldh;
     const float m = a.mean[t], s = a.rstd[t];
-    Two dot{0.0f, 0.0f};
+    Two<float> dot{0.0f, 0.0f};
     for (int c = (int)threadIdx.x * N; c < a.dim; c += kLongWaves * 64 * N) {
       E gv[N], hv[N];
       float w[N];
@@ -471,10 +496,17 @@ __global__ __launch_bounds__(kThr) void layer_norm_cols_kernel(LayerNormBackArgs
   store_raw<false>(pb + c, left, ob);
 }
 
+// Waves of a CU that share the rows, forward: 16384 x 2048 bf16 45 us with 16, 48 with 24 or 12.
+// fp32 rows go one to a group: 94 us, 102 with 16.
+template <typename E>
+constexpr long long kFwdWaves = sizeof(E) == 2 ? 16 : 1LL << 40;
+
 template <typename E, int NV, int WPR>
 void fwd(const LayerNormArgs& a, hipStream_t s) {
-  const long long rpw = threads(WPR) / 64 / WPR;
-  const dim3 grid((unsigned)((a.T + rpw - 1) / rpw)), block(threads(WPR));
+  const long long rpw = threads(WPR) / 64 / WPR, groups = (a.T + rpw - 1) / rpw;
+  // a few workgroups to a CU, each with as many rows as the others
+  const long long most = kFwdWaves<E> * 256 / (threads(WPR) / 64), each = (groups + most - 1) / most;
+  const dim3 grid((unsigned)((groups + each - 1) / each)), block(threads(WPR));
   const bool whole = a.dim % (16 / (int)sizeof(E)) == 0, drop = a.drop.threshold != 0;
   if (whole && !drop) hipLaunchKernelGGL((add_layer_norm_kernel<E, NV, WPR, true, false>), grid, block, 0, s, a);
   else if (whole) hipLaunchKernelGGL((add_layer_norm_kernel<E, NV, WPR, true, true>), grid, block, 0, s, a);
@@ -484,7 +516,7 @@ void fwd(const LayerNormArgs& a, hipStream_t s) {
 template <typename E, int NV, int WPR>
 void bwd(const LayerNormBackArgs& a, int parts, hipStream_t s) {
   const size_t lds = WPR == 1 ? (size_t)a.dim * 16 : 0;
-  const dim3 grid((unsigned)parts), block(kThr);
+  const dim3 grid((unsigned)parts), block(threads(WPR));
   const bool whole = a.dim % (16 / (int)sizeof(E)) == 0, drop = a.drop.threshold != 0;
   if (whole && !drop) hipLaunchKernelGGL((layer_norm_backward_kernel<E, NV, WPR, true, false>), grid, block, lds, s, a);
   else if (whole) hipLaunchKernelGGL((layer_norm_backward_kernel<E, NV, WPR, true, true>), grid, block, lds, s, a);
@@ -492,11 +524,12 @@ void bwd(const LayerNormBackArgs& a, int parts, hipStream_t s) {
   else hipLaunchKernelGGL((layer_norm_backward_kernel<E, NV, WPR, false, true>), grid, block, lds, s, a);
 }
 
-// f(NV) for the least NV in 1, 2, 4 up to MAX whose NV * per covers dim; false if none
+// f(NV) for the least NV in 1, 2, 3, 4 up to MAX whose NV * per covers dim; false if none
 template <int MAX, typename F>
 bool with_nv(int dim, int per, F f) {
   if (dim <= per) f(std::integral_constant<int, 1>{});
   else if (dim <= 2 * per) f(std::integral_constant<int, 2>{});
+  else if (dim <= 3 * per && MAX >= 3) f(std::integral_constant<int, (MAX >= 3 ? 3 : 1)>{});
   else if (dim <= 4 * per && MAX >= 4) f(std::integral_constant<int, (MAX >= 4 ? 4 : 1)>{});
   else return false;
   return true;
@@ -504,12 +537,11 @@ bool with_nv(int dim, int per, F f) {
 
 // Rows from which one wave takes a row
 constexpr long long kManyRows = 1024;
-constexpr int kBackVecs = 4;   // vectors of a row a lane of four waves keeps in the backward
 
 template <typename E>
 void fwd_any(const LayerNormArgs& a, hipStream_t s) {
   constexpr int N = 16 / sizeof(E);
-  if (a.T >= kManyRows && with_nv<2>(a.dim, 64 * N, [&](auto nv) { fwd<E, nv.value, 1>(a, s); })) return;
+  if (a.T >= kManyRows && with_nv<(sizeof(E) == 2 ? 4 : 2)>(a.dim, 64 * N, [&](auto nv) { fwd<E, nv.value, 1>(a, s); })) return;
   if (with_nv<4>(a.dim, 256 * N, [&](auto nv) { fwd<E, nv.value, 4>(a, s); })) return;
   if (with_nv<2>(a.dim, 1024 * N, [&](auto nv) { fwd<E, nv.value, 16>(a, s); })) return;
   const dim3 grid((unsigned)a.T), block(kLongWaves * 64);
@@ -520,7 +552,9 @@ template <typename E>
 void bwd_any(const LayerNormBackArgs& a, int parts, hipStream_t s) {
   constexpr int N = 16 / sizeof(E);
   if (a.T >= kManyRows && with_nv<2>(a.dim, 64 * N, [&](auto nv) { bwd<E, nv.value, 1>(a, parts, s); })) return;
-  if (with_nv<kBackVecs>(a.dim, 256 * N, [&](auto nv) { bwd<E, nv.value, 4>(a, parts, s); })) return;
+  if (with_nv<3>(a.dim, 256 * N, [&](auto nv) { bwd<E, nv.value, 4>(a, parts, s); })) return;
+  // four vectors a lane leave a SIMD one wave: eight waves a row instead (4096 x 8192 bf16 65 -> 60 us)
+  if (a.dim <= 2 * 512 * N) return bwd<E, 2, 8>(a, parts, s);
   hipLaunchKernelGGL((layer_norm_means_kernel<E>), dim3((unsigned)std::min<long long>(a.T, 4096)), dim3(kLongWaves * 64), 0,
                      s, a);
   const dim3 grid((unsigned)((a.dim + kThr * N - 1) / (kThr * N)), (unsigned)parts);
@@ -540,7 +574,7 @@ P at(P p, long long bytes) {
 
 // Two workgroups to a CU, as in the norm without a mean (k_norm.hip)
 int layer_norm_backward_parts(long long T) { return (int)std::min<long long>((T + 1) / 2, 512); }
-int layer_norm_back_reg_dim(int bf16) { return 256 * kBackVecs * (bf16 ? 8 : 4); }
+int layer_norm_back_reg_dim(int bf16) { return 2 * 512 * (bf16 ? 8 : 4); }
 
 hipError_t launch_add_layer_norm(const LayerNormArgs& a, int bf16, hipStream_t s) {
   if (a.dim <= 0 || a.dim > kNormMaxDim) return hipErrorInvalidValue;

@@ -45,7 +45,7 @@ struct Operand<Ty, R, KB, false> {
   static constexpr int ES = Ty::kSize, L = R / RPL, BYTES = R * KB;
   static_assert(L * RPL == R, "whole loads");
   const char* p[L];
-  __device__ __forceinline__ void init(const void* base, long long ld, int r0, int rows, int) {
+  __device__ __forceinline__ void init(const void* base, long long ld, int r0, int rows) {
 #pragma unroll
     for (int i = 0; i < L; ++i)
       p[i] = static_cast<const char*>(base) + (long long)min(r0 + i * RPL + (int)threadIdx.x / CPR, rows - 1) * ld * ES;
@@ -83,7 +83,7 @@ struct Operand<Ty, R, KB, true> {
   const char* p;   // the first summed row's first chunk of this thread
   long long ld, c, cb;
   bool whole;
-  __device__ __forceinline__ void init(const void* base, long long ld_, int r0, int rows, int) {
+  __device__ __forceinline__ void init(const void* base, long long ld_, int r0, int rows) {
     p = static_cast<const char*>(base);
     ld = ld_ * ES;
     c = (long long)r0 * ES + (threadIdx.x % CPR) * 16;
@@ -130,8 +130,6 @@ struct Operand<Ty, R, KB, true> {
   }
 };
 
-enum Mode { STATS, GRAD, DX, DW };
-
 // Bytes of the summed axis a stage: twice as many for the smallest tiles, which leave the
 // memory too few loads otherwise (16 tokens, 32000 x 2048 36.4 -> 35.6 us, 3000 x 512 15.6 ->
 // 13.1)
@@ -139,37 +137,11 @@ constexpr int stage_bytes(int bm) { return bm == 32 ? 256 : 128; }
 template <typename Ty, int BM, int BN, Mode M>
 struct Tile {
   static constexpr int KB = stage_bytes(BM);
-  using A = Operand<Ty, BM, KB, M == DW>;
-  using B = Operand<Ty, BN, KB, M == DX || M == DW>;
+  using A = Operand<Ty, BM, KB, false>;
+  using B = Operand<Ty, BN, KB, M == DX>;
   static constexpr int STAGE = A::BYTES + B::BYTES;
   static_assert(STAGE % 16 == 0 && A::BYTES % 16 == 0, "16-byte pieces");
 };
-
-template <bool F32>
-__device__ __forceinline__ void put(const void* base, long long at, const float (&v)[4], int cols) {
-  if constexpr (F32) {
-    float* const p = static_cast<float*>(const_cast<void*>(base)) + at;
-    if (cols >= 4) {
-      *reinterpret_cast<Pack<float, 4>*>(p) = Pack<float, 4>{{v[0], v[1], v[2], v[3]}};
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < cols) p[i] = v[i];
-    }
-  } else {
-    uint16_t* const p = static_cast<uint16_t*>(const_cast<void*>(base)) + at;
-    Pack<uint16_t, 4> o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o.v[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v[i]));
-    if (cols >= 4) {
-      *reinterpret_cast<Pack<uint16_t, 4>*>(p) = o;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < cols) p[i] = o.v[i];
-    }
-  }
-}
 
 template <typename Ty, int BM, int BN, Mode MODE>
 __global__ __launch_bounds__(kThr) __attribute__((amdgpu_waves_per_eu(2, 2)))
@@ -177,17 +149,16 @@ void vocab_tile_kernel(VocabArgs a) {
   using Cfg = Tile<Ty, BM, BN, MODE>;
   using OA = typename Cfg::A;
   using OB = typename Cfg::B;
-  constexpr bool F32 = Ty::kSize == 4;
   constexpr int KE = Cfg::KB / Ty::kSize;      // elements of the summed axis a stage
   constexpr int Q = Cfg::KB / 64;              // 64-byte slabs of it
   constexpr int TM = BM / 32, TN = BN / 32;    // 16 x 16 tiles of a wave
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
-  const int rows = MODE == DW ? a.vp : (int)a.T, cols = MODE == STATS || MODE == GRAD ? a.vp : a.n;
+  const int rows = (int)a.T, cols = MODE == DX ? a.n : a.vp;
   int m0, n0;
   if (!tile_origin(rows, cols, BM, BN, m0, n0)) return;
-  int k0 = 0, kend = MODE == DX ? a.vp : MODE == DW ? (int)a.T : a.n;
+  int k0 = 0, kend = MODE == DX ? a.vp : a.n;
   if (MODE == DX && a.splits > 1) {
     const int per = ((kend + a.splits - 1) / a.splits + KE - 1) / KE * KE;
     k0 = min(kend, (int)blockIdx.y * per);
@@ -196,16 +167,9 @@ void vocab_tile_kernel(VocabArgs a) {
   const char* const w = static_cast<const char*>(a.W) + (long long)a.v0 * a.ldw * Ty::kSize;
   OA oa;
   OB ob;
-  if constexpr (MODE == STATS || MODE == GRAD) {
-    oa.init(a.X, a.ldx, m0, rows, 0);
-    ob.init(w, a.ldw, n0, cols, 0);
-  } else if constexpr (MODE == DX) {
-    oa.init(a.dS, a.ldp, m0, rows, 0);
-    ob.init(w, a.ldw, n0, cols, 0);
-  } else {
-    oa.init(a.dS, a.ldp, m0, rows, 0);
-    ob.init(a.Xm, a.ldm, n0, cols, 0);
-  }
+  if constexpr (MODE == DX) oa.init(a.dS, a.ldp, m0, rows);
+  else oa.init(a.X, a.ldx, m0, rows);
+  ob.init(w, a.ldw, n0, cols);
   i32x4 ar[2][OA::L], br[2][OB::L];   // two stages under way
   auto fetch = [&](int k, int set) __attribute__((always_inline)) {
     oa.fetch(ar[set], k, kend);
@@ -259,83 +223,7 @@ void vocab_tile_kernel(VocabArgs a) {
     }
   }
 
-  // lane l holds row l & 15 of each tile and 4 of its columns, from 4 (l >> 4) on
-  const int r0 = m0 + wm + (lane & 15), c0 = n0 + wn + 4 * (lane >> 4);
-  if constexpr (MODE == STATS) {
-    const int groups = (a.V + BN / 2 - 1) / (BN / 2), group = (n0 + wn) / (BN / 2);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int t = r0 + i * 16;
-      float m = -__builtin_inff(), s = 0.0f;
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          if (c0 + j * 16 + v < a.V) m = fmaxf(m, acc[i][j][v]);
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      // all -inf: each term is exp(-inf), not exp(-inf + inf); a NaN stays one
-      const float base = m == -__builtin_inff() ? 0.0f : m;
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          if (c0 + j * 16 + v < a.V) s += exp_of<F32>(acc[i][j][v] - base);
-      s += __shfl_xor(s, 16);
-      s += __shfl_xor(s, 32);
-      if (t >= rows || group >= groups) continue;
-      if (lane < 16) a.part[(long long)t * groups + group] = float2{m, s};
-      const long long target = a.target[t];
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          if (c0 + j * 16 + v == target && target < a.V) a.zt[t] = acc[i][j][v];
-    }
-  } else if constexpr (MODE == GRAD) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int t = r0 + i * 16;
-      if (t >= rows) continue;
-      const Row r = token_of(a, t);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int c = c0 + j * 16;
-        if (c >= cols) continue;
-        float d[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) d[v] = grad_of<F32>(r, acc[i][j][v], (long long)a.v0 + c + v);
-        put<F32>(a.dS, t * a.ldp + c, d, cols - c);
-      }
-    }
-  } else {
-    const float scale = a.g_each ? 1.0f : *a.g;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int t = r0 + i * 16;
-      if (t >= rows) continue;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int c = c0 + j * 16;
-        if (c >= cols) continue;
-        float o[4];
-        if (MODE == DX && a.acc) {
-          float4* const to = reinterpret_cast<float4*>(a.acc + ((long long)blockIdx.y * a.T + t) * a.lda + c);
-          float4 v = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-          if (a.v0 > 0) {
-            const float4 b = *to;
-            v = float4{v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w};
-          }
-          *to = v;
-          continue;
-        }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) o[v] = acc[i][j][v] * scale;
-        if constexpr (MODE == DX) put<F32>(a.GX, t * a.ldgx + c, o, cols - c);
-        else put<F32>(a.GW, (long long)(a.v0 + t) * a.ldgw + c, o, cols - c);
-      }
-    }
-  }
+  epilogue<Ty, BN, TM, TN, MODE>(a, acc, rows, cols, m0, n0, wm, wn, MODE == DX ? (int)blockIdx.y : 0);
 }
 
 // Forward for the fewest tokens, TT of them: every wave multiplies kFewRows rows of W by all
@@ -496,6 +384,16 @@ __global__ __launch_bounds__(kThr) void vocab_mask_kernel(VocabArgs a) {
   }
 }
 
+// Zeros in d's columns from vp to a multiple of 64
+template <typename E>
+__global__ __launch_bounds__(kThr) void vocab_pad_kernel(VocabArgs a) {
+  const int vz = (a.vp + 63) / 64 * 64;
+  for (long long i = (long long)blockIdx.x * kThr + threadIdx.x; i < a.T * 64; i += (long long)gridDim.x * kThr) {
+    const int c = a.vp + (int)(i & 63);
+    if (c < vz) static_cast<E*>(a.dS)[(i >> 6) * a.ldp + c] = E(0);
+  }
+}
+
 // dX = round(factor * the sum of the splits' parts)
 template <bool F32>
 __global__ __launch_bounds__(kThr) void vocab_finish_kernel(VocabArgs a) {
@@ -525,6 +423,13 @@ hipError_t few(const VocabArgs& a, hipStream_t s) {
   return a.T == 1 ? few<Ty, 1>(a, s) : few<Ty, 2>(a, s);
 }
 
+hipError_t launch_pad(const VocabArgs& a, int bf16, hipStream_t s) {
+  const dim3 grid((unsigned)std::min<long long>((a.T + 3) / 4, 4096));
+  if (bf16) hipLaunchKernelGGL((vocab_pad_kernel<uint16_t>), grid, dim3(kThr), 0, s, a);
+  else hipLaunchKernelGGL((vocab_pad_kernel<float>), grid, dim3(kThr), 0, s, a);
+  return hipGetLastError();
+}
+
 // V rows of n elements of zeros (4 or 2 bytes each)
 template <typename E>
 __global__ __launch_bounds__(kThr) void vocab_zero_kernel(E* p, int V, int n, long long ld) {
@@ -532,23 +437,24 @@ __global__ __launch_bounds__(kThr) void vocab_zero_kernel(E* p, int V, int n, lo
     for (int c = threadIdx.x; c < n; c += kThr) p[v * ld + c] = E(0);
 }
 
-// 128 rows by 128 columns, fp32 by 64: two workgroups to a CU, for one wave to a SIMD
-// leaves its matrix unit idle (512 x 512 x 8000 53 -> 45 us)
-constexpr int big_cols(bool bf16) { return bf16 ? 128 : 64; }
-
 template <typename Ty, int BM, int BN, Mode M>
 hipError_t tiles(const VocabArgs& a, hipStream_t s) {
-  const long long rows = M == DW ? a.vp : a.T;
-  const int cols = M == STATS || M == GRAD ? a.vp : a.n;
+  const int cols = M == DX ? a.n : a.vp;
   hipLaunchKernelGGL((vocab_tile_kernel<Ty, BM, BN, M>),
-                     dim3((unsigned)tile_grid(rows, cols, BM, BN), M == DX ? (unsigned)a.splits : 1u), dim3(kThr),
+                     dim3((unsigned)tile_grid(a.T, cols, BM, BN), M == DX ? (unsigned)a.splits : 1u), dim3(kThr),
                      (2 * Tile<Ty, BM, BN, M>::STAGE), s, a);
   return hipGetLastError();
 }
 template <typename Ty, Mode M>
 hipError_t tiles(const VocabArgs& a, int tile, hipStream_t s) {
   switch (tile) {
-    case VOCAB_TILE_BIG: return tiles<Ty, 128, big_cols(Ty::kSize == 2), M>(a, s);
+    case VOCAB_TILE_128:
+      if constexpr (Ty::kSize == 2) return tiles<Ty, 128, 128, M>(a, s);
+      break;
+    case VOCAB_TILE_128x64:
+      // fp32: two workgroups to a CU, for one wave to a SIMD leaves its matrix unit idle
+      if constexpr (Ty::kSize == 4) return tiles<Ty, 128, 64, M>(a, s);
+      break;
     case VOCAB_TILE_64: return tiles<Ty, 64, 64, M>(a, s);
     case VOCAB_TILE_32x64: return tiles<Ty, 32, 64, M>(a, s);
   }
@@ -560,47 +466,51 @@ hipError_t tiles(const VocabArgs& a, int bf16, int tile, hipStream_t s) {
 }
 
 // How a product is laid out: its tile, and how many workgroups share the sum of one.
-// `cost` in us, of measured parts: a stage of 128 bytes of the sum takes a tile `alone` on
-// its CU or two beside each other there `pair` (256 x 256 tiles have a CU to themselves), a
-// tile's start and epilogue `ends`.
+// What a tile takes in us for 32 stages of 128 bytes of the sum: `first` for a grid of up to
+// 256 tiles, one to a CU, `round` for every 256 tiles of a grid where the CUs are full, and
+// `ends` once for its start and epilogue. kRing, kRingF32: filled by direct-to-LDS loads
+// (k_vocab_loss_ring.hip, k_vocab_loss_pipe.hip), the others through registers.
 struct TileCost {
   int tile, bm, bn;
-  double alone, pair, ends;
+  double first, round, ends;
 };
-constexpr TileCost kBf16[] = {{VOCAB_TILE_256, 256, 256, 0.88, 1.76, 9},
-                              {VOCAB_TILE_BIG, 128, 128, 0.85, 1.4, 5},
-                              {VOCAB_TILE_64, 64, 64, 0.75, 1.2, 4},
-                              {VOCAB_TILE_32x64, 32, 64, 0.65, 0.95, 4}};
-constexpr TileCost kF32[] = {{VOCAB_TILE_BIG, 128, 64, 1.6, 2.6, 5},
-                             {VOCAB_TILE_64, 64, 64, 1.0, 1.5, 4},
-                             {VOCAB_TILE_32x64, 32, 64, 0.8, 1.1, 4}};
+constexpr TileCost kRing[] = {{VOCAB_TILE_256, 256, 256, 28, 50, 9}, {VOCAB_TILE_128, 128, 128, 24, 17, 5},
+                              {VOCAB_TILE_128x64, 128, 64, 11, 9.5, 4}, {VOCAB_TILE_64, 64, 64, 6.5, 5.8, 3},
+                              {VOCAB_TILE_32x64, 32, 64, 4.6, 4.3, 3}};
+constexpr TileCost kRingF32[] = {{VOCAB_TILE_128x64, 128, 64, 33, 30, 5}, {VOCAB_TILE_64, 64, 64, 18, 16.5, 4},
+                                 {VOCAB_TILE_32x64, 32, 64, 10, 9, 3}};
+constexpr TileCost kTiles[] = {{VOCAB_TILE_128, 128, 128, 27, 22, 5}, {VOCAB_TILE_64, 64, 64, 24, 19, 4},
+                               {VOCAB_TILE_32x64, 32, 64, 20, 15, 4}};
+constexpr TileCost kTilesF32[] = {{VOCAB_TILE_128x64, 128, 64, 51, 42, 5}, {VOCAB_TILE_64, 64, 64, 32, 24, 4},
+                                  {VOCAB_TILE_32x64, 32, 64, 25, 18, 4}};
 
 template <size_t N>
 VocabTiles cheapest(const TileCost (&costs)[N], long long rows, long long cols, long long stages, bool wide, bool share) {
   VocabTiles best{-1, 1, 0.0};
   for (const TileCost& c : costs) {
     if (c.tile == VOCAB_TILE_256 && !wide) continue;
-    if (c.bm > 32 && rows <= c.bm / 2 && c.tile != VOCAB_TILE_256) continue;
     const long long n = ((rows + c.bm - 1) / c.bm) * ((cols + c.bn - 1) / c.bn);
-    const long long slots = c.tile == VOCAB_TILE_256 ? 256 : 512;
     for (int splits = 1; splits <= (share ? 64 : 1); splits *= 2) {
       const long long per = (stages + splits - 1) / splits, items = n * splits;
-      if (splits > 1 && (per < 4 || items > slots)) break;
+      if (splits > 1 && (per < 4 || items > 512)) break;
       // shares are written and read once more, by another launch
-      const double extra = splits > 1 ? 4 + 8e-6 * (double)splits * (double)(rows * cols) / 4.0 : 0.0;
-      const double round = items <= 256 ? per * c.alone : per * c.pair;
-      const double cost = (round + c.ends) * (double)((items + slots - 1) / slots) + extra;
+      const double extra = splits > 1 ? 4 + 2e-6 * (double)splits * (double)(rows * cols) : 0.0;
+      const double time = std::max(c.first, c.round * (double)((items + 255) / 256)) * (double)per / 32;
+      const double cost = time + c.ends + extra;
       if (best.tile < 0 || cost < best.cost) best = VocabTiles{c.tile, splits, cost};
     }
   }
   return best;
 }
-// wide: whether 256 x 256 tiles may be taken
-VocabTiles tiles_of(long long rows, long long cols, long long sum, int bf16, bool wide, bool share = false) {
+// fast: whether the operands' rows are whole 16 bytes; wide: whether 256 x 256 tiles may be taken
+VocabTiles tiles_of(long long rows, long long cols, long long sum, int bf16, bool fast, bool wide, bool share = false) {
   const long long stages = (sum * (bf16 ? 2 : 4) + 127) / 128;
-  return bf16 ? cheapest(kBf16, rows, cols, stages, wide, share) : cheapest(kF32, rows, cols, stages, false, share);
+  if (fast) {
+    return bf16 ? cheapest(kRing, rows, cols, stages, wide, share) : cheapest(kRingF32, rows, cols, stages, false, share);
+  }
+  return bf16 ? cheapest(kTiles, rows, cols, stages, false, share) : cheapest(kTilesF32, rows, cols, stages, false, share);
 }
-int group_cols(int tile, int bf16) { return tile == VOCAB_TILE_BIG && bf16 ? 64 : 32; }
+int group_cols(int tile) { return tile == VOCAB_TILE_128 || tile == VOCAB_TILE_256 ? 64 : 32; }
 
 constexpr long long kRoom = 256LL << 20;   // bytes that a part of the work may take as workspace
 size_t padded(size_t b) { return (b + 255) / 256 * 256; }
@@ -616,11 +526,13 @@ hipError_t launch_vocab_zero(void* p, int V, int n, long long ld, int es, hipStr
 
 VocabPlan vocab_forward_plan(long long T, int V, int n, int bf16) {
   VocabPlan p{};
-  // as the operands' alignment may lead: 256 x 256 tiles (parts of 64 columns, whole tiles of them) or not
-  p.lay[0] = tiles_of(T, V, n, bf16, false);
-  p.lay[1] = tiles_of(T, V, n, bf16, bf16 && T >= 256 && V >= 256);
-  const int cols = T <= kFew ? kFewGroup : group_cols(p.lay[0].tile, bf16);
-  p.groups = std::max((V + cols - 1) / cols, p.lay[1].tile == VOCAB_TILE_256 ? (V + 255) / 256 * 4 : 0);
+  // as the operands' alignment may lead: rows of whole 16 bytes or not
+  p.lay[0] = tiles_of(T, V, n, bf16, false, false);
+  p.lay[1] = tiles_of(T, V, n, bf16, true, false);
+  p.lay[2] = tiles_of(T, V, n, bf16, true, bf16 && T >= 256 && V >= 256);
+  p.groups = T <= kFew ? (V + kFewGroup - 1) / kFewGroup : 0;
+  for (const VocabTiles& l : p.lay)   // 256-column tiles leave parts of whole tiles
+    p.groups = std::max(p.groups, l.tile == VOCAB_TILE_256 ? (V + 255) / 256 * 4 : (V + group_cols(l.tile) - 1) / group_cols(l.tile));
   // tokens of a launch: as many as their parts leave room for, and their tiles can be counted
   const long long most = std::min(kRoom / (8LL * p.groups), (1LL << 33) / V);
   p.rows = std::min(T, std::max(256LL, most / 256 * 256));
@@ -642,17 +554,17 @@ hipError_t launch_vocab_forward(const VocabArgs& in, int bf16, void* ws, hipStre
     a.zt = reinterpret_cast<float*>(static_cast<char*>(ws) + padded((size_t)p.rows * p.groups * 8));
     a.v0 = 0;
     a.vp = a.V;
-    int groups;
+    const VocabTiles& lay = p.lay[!vocab_ring_logits(a, bf16) ? 0 : bf16 && vocab_pipe_logits(a) ? 2 : 1];
+    int groups = (a.V + group_cols(lay.tile) - 1) / group_cols(lay.tile);
     hipError_t e;
     if (in.T <= kFew) {
-      groups = p.groups;
+      groups = (a.V + kFewGroup - 1) / kFewGroup;
       e = bf16 ? few<TypeBf16>(a, s) : few<TypeF32>(a, s);
-    } else if (p.lay[1].tile == VOCAB_TILE_256 && vocab_pipe_logits(a)) {
+    } else if (lay.tile == VOCAB_TILE_256) {
       groups = (a.V + 255) / 256 * 4;
       e = launch_vocab_pipe_stats(a, s);
     } else {
-      groups = (a.V + group_cols(p.lay[0].tile, bf16) - 1) / group_cols(p.lay[0].tile, bf16);
-      e = tiles<STATS>(a, bf16, p.lay[0].tile, s);
+      e = &lay == &p.lay[0] ? tiles<STATS>(a, bf16, lay.tile, s) : launch_vocab_ring_stats(a, bf16, lay.tile, s);
     }
     if (e != hipSuccess) return e;
     if (a.T >= 1024)
@@ -672,17 +584,17 @@ VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, 
   p.ldm = (n + 7) / 8 * 8;
   p.lda = (n + 3) / 4 * 4;
   // columns of a piece: those whose d leaves room, in whole tiles, the pieces alike
-  const long long most = std::max(256LL, std::min(kRoom / (p.Tm * es), (1LL << 36) / n) / 256 * 256);
+  const long long most = std::max(256LL, std::min({kRoom / (p.Tm * es), (1LL << 36) / n, 1LL << 19}) / 256 * 256);
   const long long pieces = (V + most - 1) / most;
   p.vp = (int)std::min<long long>(most, ((V + pieces - 1) / pieces + 255) / 256 * 256);
   const int vp = std::min(p.vp, V);
   const bool one = V <= p.vp;
-  // as the operands' alignment may lead: 256 x 256 tiles or not
-  p.dx[0] = tiles_of(T, n, vp, bf16, false, true);
-  p.dx[1] = tiles_of(T, n, vp, bf16, bf16 && vocab_pipe_dx(T, n), true);
+  // as the operands' alignment may lead: rows of whole 16 bytes or not
+  p.dx[0] = tiles_of(T, n, vp, bf16, false, false, true);
+  p.dx[1] = tiles_of(T, n, vp, bf16, true, bf16 && vocab_pipe_dx(T, n), true);
   // shares none of which is empty in the first piece (the others only add to theirs)
   for (VocabTiles& d : p.dx) {
-    const long long stages = ((long long)vp * es + 127) / 128, per = (stages + d.splits - 1) / d.splits;
+    const long long stages = (long long)((vp + 63) / 64 * 64) * es / 128, per = (stages + d.splits - 1) / d.splits;
     d.splits = (int)((stages + per - 1) / per);
   }
   const int splits = std::max(p.dx[0].splits, p.dx[1].splits);
@@ -702,7 +614,8 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
   a.ldm = p.ldm;
   a.Tm = p.Tm;
   a.lda = p.lda;
-  const VocabTiles dx = p.dx[bf16 && vocab_pipe_weight(a) ? 1 : 0];
+  const bool fast = vocab_ring_weight(a, bf16);
+  const VocabTiles dx = p.dx[fast ? 1 : 0];
   const bool wide_dx = dx.tile == VOCAB_TILE_256;
   a.splits = dx.splits;
   a.acc = a.splits > 1 || a.V > p.vp ? reinterpret_cast<float*>(static_cast<char*>(ws) + p.at_acc) : nullptr;
@@ -718,20 +631,26 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
   for (long long v = 0; v < a.V; v += p.vp) {
     a.v0 = (int)v;
     a.vp = (int)std::min<long long>(p.vp, a.V - v);
-    const VocabTiles grad = tiles_of(a.T, a.vp, a.n, bf16, bf16 && vocab_pipe_logits(a));
-    e = grad.tile == VOCAB_TILE_256 ? launch_vocab_pipe_grad(a, s) : tiles<GRAD>(a, bf16, grad.tile, s);
+    const bool fast_logits = vocab_ring_logits(a, bf16);
+    const VocabTiles grad = tiles_of(a.T, a.vp, a.n, bf16, fast_logits, bf16 && vocab_pipe_logits(a));
+    e = grad.tile == VOCAB_TILE_256 ? launch_vocab_pipe_grad(a, s)
+        : fast_logits               ? launch_vocab_ring_grad(a, bf16, grad.tile, s)
+                                    : tiles<GRAD>(a, bf16, grad.tile, s);
     if (e != hipSuccess) return e;
     if (a.GX) {
-      if (wide_dx && a.vp % 64 && (!a.GW || a.v0 > 0)) {
-        e = launch_vocab_pad(a, s);
+      if (fast && a.vp % 64 && (!a.GW || a.v0 > 0)) {
+        e = launch_pad(a, bf16, s);
         if (e != hipSuccess) return e;
       }
-      e = wide_dx ? launch_vocab_pipe_dx(a, s) : tiles<DX>(a, bf16, dx.tile, s);
+      e = wide_dx ? launch_vocab_pipe_dx(a, s)
+          : fast  ? launch_vocab_ring_dx(a, bf16, dx.tile, s)
+                  : tiles<DX>(a, bf16, dx.tile, s);
       if (e != hipSuccess) return e;
     }
     if (a.GW) {
-      const VocabTiles dw = tiles_of(a.vp, a.n, a.T, bf16, bf16 && vocab_pipe_dw(a));
-      e = dw.tile == VOCAB_TILE_256 ? launch_vocab_pipe_dw(a, s) : tiles<DW>(a, bf16, dw.tile, s);
+      // both operands are this call's own: their rows are whole 16 bytes
+      const VocabTiles dw = tiles_of(a.vp, a.n, a.T, bf16, true, bf16 && vocab_pipe_dw(a));
+      e = dw.tile == VOCAB_TILE_256 ? launch_vocab_pipe_dw(a, s) : launch_vocab_ring_dw(a, bf16, dw.tile, s);
       if (e != hipSuccess) return e;
     }
   }

@@ -44,8 +44,6 @@ constexpr int kSteps = kKB / 32;
 constexpr int kLoads = kTile / 32;         // loads of a lane per operand tile, 4 KB of it each
 constexpr int kGroupRows = 4;              // tile-rows per group of the XCD-aware order
 
-enum Mode { STATS, GRAD, DX, DW };
-
 constexpr float kLog2E = 1.44269504088896340736f;
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -58,32 +56,6 @@ __device__ __forceinline__ void swap_halves(float& a, float& b) {
   const uint32_t r0 = r[0], r1 = r[1];
   a = __uint_as_float(r0);
   b = __uint_as_float(r1);
-}
-
-// 16 bytes per lane from the buffer's byte `off` + `soff` to lane * 16 behind the LDS address
-// `to`. WRITTEN out for kernels that read by the transposing LDS read: beside the builtin the
-// compiler lets every such read of the wave wait for all its loads (16384 tokens, 8192 rows
-// of 2048: d W 553 -> 421, d^T X 591 -> 422 us). It has no result in registers; vm_wait waits
-// for it. M0, which the compiler keeps to itself, is left as it was; the s_nop is for scalar
-// operands that a vector instruction wrote.
-typedef uint32_t Buffer __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ Buffer buffer_at(const char* p, uint32_t bytes) {
-  const uint64_t a = (uint64_t)(uintptr_t)p;
-  return Buffer{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, 0x00020000u};
-}
-template <bool WRITTEN>
-__device__ __forceinline__ void load_lds(const char* p, uint32_t bytes, uint32_t to, uint32_t off, uint32_t soff) {
-  if constexpr (WRITTEN) {
-    uint32_t m0;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\ts_mov_b32 m0, %0"
-        : "=&s"(m0)
-        : "s"(to), "v"(off), "s"(buffer_at(p, bytes)), "s"(soff));
-  } else {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, (int)bytes, 0x00020000),
-        (__attribute__((address_space(3))) void*)(uintptr_t)to, 16, off, soff, 0, 0);
-  }
 }
 
 // How the lanes load and read an operand tile whose rows run along the summed axis, or
@@ -511,16 +483,6 @@ hipError_t launch(const VocabArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Zeros in columns [vp, vz) of d's rows
-__global__ __launch_bounds__(256) void vocab_pad_kernel(VocabArgs a) {
-  const int vz = (a.vp + 63) / 64 * 64;
-  uint16_t* const d = static_cast<uint16_t*>(a.dS);
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < a.T * 64; i += (long long)gridDim.x * 256) {
-    const int c = a.vp + (int)(i & 63);
-    if (c < vz) d[(i >> 6) * a.ldp + c] = 0;
-  }
-}
-
 bool aligned16(const void* p, long long ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
 
 }  // namespace
@@ -530,16 +492,11 @@ bool vocab_pipe_logits(const VocabArgs& a) {
          a.ldx < (1 << 21) && a.ldw < (1 << 21);
 }
 bool vocab_pipe_dx(long long T, int n) { return T >= kTile && n >= kTile && n % 8 == 0; }
-bool vocab_pipe_weight(const VocabArgs& a) { return aligned16(a.W, a.ldw) && a.ldw < (1 << 21) && a.ldp < (1 << 21); }
 bool vocab_pipe_dw(const VocabArgs& a) { return a.vp > kTile - 64 && a.ldm >= kTile && a.ldp < (1 << 21); }
 
 hipError_t launch_vocab_pipe_stats(const VocabArgs& a, hipStream_t s) { return launch<STATS>(a, s); }
 hipError_t launch_vocab_pipe_grad(const VocabArgs& a, hipStream_t s) { return launch<GRAD>(a, s); }
 hipError_t launch_vocab_pipe_dx(const VocabArgs& a, hipStream_t s) { return launch<DX>(a, s); }
 hipError_t launch_vocab_pipe_dw(const VocabArgs& a, hipStream_t s) { return launch<DW>(a, s); }
-hipError_t launch_vocab_pad(const VocabArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(vocab_pad_kernel, dim3((unsigned)std::min<long long>((a.T + 3) / 4, 4096)), dim3(256), 0, s, a);
-  return hipGetLastError();
-}
 
 }  // namespace poetx

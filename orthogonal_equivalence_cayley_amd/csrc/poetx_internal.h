@@ -379,15 +379,14 @@ struct VocabArgs {
 };
 enum VocabTile {
   VOCAB_TILE_256,    // k_vocab_loss_pipe.hip
-  VOCAB_TILE_BIG,    // 128 x 128, fp32 128 x 64
-  VOCAB_TILE_64, VOCAB_TILE_32x64
+  VOCAB_TILE_128, VOCAB_TILE_128x64, VOCAB_TILE_64, VOCAB_TILE_32x64
 };
 struct VocabTiles {
   int tile, splits;
   double cost;
 };
 struct VocabPlan {
-  VocabTiles lay[2];   // without and with 256 x 256 tiles
+  VocabTiles lay[3];   // rows of no whole 16 bytes, of whole ones, and with 256 x 256 tiles
   int groups;
   long long rows;   // tokens of a launch
   size_t bytes;
@@ -395,7 +394,7 @@ struct VocabPlan {
 struct VocabBackPlan {
   long long Tm, ldm, lda;
   int vp;
-  VocabTiles dx[2];   // without and with 256 x 256 tiles
+  VocabTiles dx[2];   // rows of no whole 16 bytes, and of whole ones
   bool acc;
   size_t at_x, at_acc, bytes;
 };
@@ -410,13 +409,18 @@ hipError_t launch_vocab_backward(const VocabArgs& a, int bf16, void* ws, hipStre
 // sizes and alignment allow them, and the launches
 bool vocab_pipe_logits(const VocabArgs& a);
 bool vocab_pipe_dx(long long T, int n);
-bool vocab_pipe_weight(const VocabArgs& a);
 bool vocab_pipe_dw(const VocabArgs& a);
 hipError_t launch_vocab_pipe_stats(const VocabArgs& a, hipStream_t s);
 hipError_t launch_vocab_pipe_grad(const VocabArgs& a, hipStream_t s);
 hipError_t launch_vocab_pipe_dx(const VocabArgs& a, hipStream_t s);
 hipError_t launch_vocab_pipe_dw(const VocabArgs& a, hipStream_t s);
-hipError_t launch_vocab_pad(const VocabArgs& a, hipStream_t s);   // zeros in d's columns up to a multiple of 64
+// smaller tiles with a ring of LDS stages (k_vocab_loss_ring.hip), rows of whole 16 bytes
+bool vocab_ring_logits(const VocabArgs& a, int bf16);   // X's and W's
+bool vocab_ring_weight(const VocabArgs& a, int bf16);   // W's
+hipError_t launch_vocab_ring_stats(const VocabArgs& a, int bf16, int tile, hipStream_t s);
+hipError_t launch_vocab_ring_grad(const VocabArgs& a, int bf16, int tile, hipStream_t s);
+hipError_t launch_vocab_ring_dx(const VocabArgs& a, int bf16, int tile, hipStream_t s);
+hipError_t launch_vocab_ring_dw(const VocabArgs& a, int bf16, int tile, hipStream_t s);
 hipError_t launch_vocab_zero(void* p, int V, int n, long long ld, int es, hipStream_t s);
 
 }  // namespace poetx

@@ -466,23 +466,28 @@ hipError_t tiles(const VocabArgs& a, int bf16, int tile, hipStream_t s) {
 }
 
 // How a product is laid out: its tile, and how many workgroups share the sum of one.
-// What a tile takes in us for 32 stages of 128 bytes of the sum: `first` for a grid of up to
-// 256 tiles, one to a CU, `round` for every 256 tiles of a grid where the CUs are full, and
-// `ends` once for its start and epilogue. kRing, kRingF32: filled by direct-to-LDS loads
-// (k_vocab_loss_ring.hip, k_vocab_loss_pipe.hip), the others through registers.
+// What tiles take in us: for 32 stages of 128 bytes of the sum `first` in a grid of up to 256
+// of them, one to a CU, and `round` for every 256 of a grid where the CUs are full; for the
+// start and the epilogue `ends` for every 256. kRing, kRingF32: filled by direct-to-LDS loads
+// (k_vocab_loss_ring.hip, k_vocab_loss_pipe.hip), the others through registers. Measured at
+// 16 to 16384 tokens; e.g. logits of 1003 x 1000 x 10007 bf16 31 us in 256 x 256 tiles (said
+// 35), 46 in 128 x 64 (said 43), of 256 x 2048 x 32000 60 in 256 x 256 (58), 50 in 128 x 128 (49).
 struct TileCost {
   int tile, bm, bn;
   double first, round, ends;
 };
-constexpr TileCost kRing[] = {{VOCAB_TILE_256, 256, 256, 28, 50, 9}, {VOCAB_TILE_128, 128, 128, 24, 17, 5},
-                              {VOCAB_TILE_128x64, 128, 64, 11, 9.5, 4}, {VOCAB_TILE_64, 64, 64, 6.5, 5.8, 3},
-                              {VOCAB_TILE_32x64, 32, 64, 4.6, 4.3, 3}};
-constexpr TileCost kRingF32[] = {{VOCAB_TILE_128x64, 128, 64, 33, 30, 5}, {VOCAB_TILE_64, 64, 64, 18, 16.5, 4},
-                                 {VOCAB_TILE_32x64, 32, 64, 10, 9, 3}};
-constexpr TileCost kTiles[] = {{VOCAB_TILE_128, 128, 128, 27, 22, 5}, {VOCAB_TILE_64, 64, 64, 24, 19, 4},
-                               {VOCAB_TILE_32x64, 32, 64, 20, 15, 4}};
-constexpr TileCost kTilesF32[] = {{VOCAB_TILE_128x64, 128, 64, 51, 42, 5}, {VOCAB_TILE_64, 64, 64, 32, 24, 4},
-                                  {VOCAB_TILE_32x64, 32, 64, 25, 18, 4}};
+constexpr TileCost kRing[] = {{VOCAB_TILE_256, 256, 256, 46, 46, 9}, {VOCAB_TILE_128, 128, 128, 24, 17, 6},
+                              {VOCAB_TILE_128x64, 128, 64, 11, 9.5, 3.3}, {VOCAB_TILE_64, 64, 64, 6.5, 5.8, 1.7},
+                              {VOCAB_TILE_32x64, 32, 64, 4.6, 4.3, 1.1}};
+constexpr TileCost kRingF32[] = {{VOCAB_TILE_128x64, 128, 64, 33, 30, 4}, {VOCAB_TILE_64, 64, 64, 18, 16.5, 2.2},
+                                 {VOCAB_TILE_32x64, 32, 64, 10, 9, 1.3}};
+constexpr TileCost kTiles[] = {{VOCAB_TILE_128, 128, 128, 27, 22, 6}, {VOCAB_TILE_64, 64, 64, 24, 19, 2},
+                               {VOCAB_TILE_32x64, 32, 64, 20, 15, 1.5}};
+constexpr TileCost kTilesF32[] = {{VOCAB_TILE_128x64, 128, 64, 51, 42, 5}, {VOCAB_TILE_64, 64, 64, 32, 24, 2.5},
+                                  {VOCAB_TILE_32x64, 32, 64, 25, 18, 2}};
+// d W in the ring's tiles, whose reads across the sum keep fewer loads in flight: 4000 x 256
+// x 13568 bf16 66 us in 64 x 64 against 50 in shared 256 x 256 tiles
+constexpr double kAcross = 1.5;
 
 template <size_t N>
 VocabTiles cheapest(const TileCost (&costs)[N], long long rows, long long cols, long long stages, bool wide, bool share) {
@@ -495,8 +500,9 @@ VocabTiles cheapest(const TileCost (&costs)[N], long long rows, long long cols, 
       if (splits > 1 && (per < 4 || items > 512)) break;
       // shares are written and read once more, by another launch
       const double extra = splits > 1 ? 4 + 2e-6 * (double)splits * (double)(rows * cols) : 0.0;
-      const double time = std::max(c.first, c.round * (double)((items + 255) / 256)) * (double)per / 32;
-      const double cost = time + c.ends + extra;
+      const double rounds = (double)((items + 255) / 256);
+      const double time = std::max(c.first, c.round * rounds) * (double)per / 32;
+      const double cost = time * (share && c.tile != VOCAB_TILE_256 ? kAcross : 1.0) + c.ends * rounds + 3 + extra;
       if (best.tile < 0 || cost < best.cost) best = VocabTiles{c.tile, splits, cost};
     }
   }

@@ -542,8 +542,8 @@ poetx_status poetx_linear(const poetx_linear_desc* desc, const void* X, const vo
  *     0 .. V - 1 has loss NaN.
  *   ws poetx_linear_cross_entropy_workspace(desc) bytes
  * Logits are sums in fp32. T = 0 is a no-op. No row is touched behind the T-th. T, V <=
- * 2^24, n <= 2^16 (POETX_ERR_SHAPE), also in the backward. ld_gx, ld_gw and g_count are
- * the backward's. */
+ * 2^24, n <= 2^16, T n, V n <= 2^36 (POETX_ERR_SHAPE), also in the backward. ld_gx, ld_gw
+ * and g_count are the backward's. */
 typedef struct {
   int64_t T;
   int32_t V, n;

@@ -400,6 +400,7 @@ struct VocabBackPlan {
 };
 constexpr int kVocabMax = 1 << 24;        // tokens of a call, rows of W
 constexpr int kVocabMaxDim = 1 << 16;
+constexpr long long kVocabMaxElems = 1LL << 36;   // of X, of W: their tiles stay countable
 // by the sizes alone
 VocabPlan vocab_forward_plan(long long T, int V, int n, int bf16);
 VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, bool gw);

@@ -29,6 +29,7 @@ poetx_status vocab_desc(const poetx_cross_entropy_desc* d) {
   if (!d || d->T < 0) return POETX_ERR_INVALID_ARG;
   if (d->V < 1 || d->V > poetx::kVocabMax || d->n < 1 || d->n > poetx::kVocabMaxDim || d->T > poetx::kVocabMax)
     return POETX_ERR_SHAPE;
+  if (d->T * d->n > poetx::kVocabMaxElems || (int64_t)d->V * d->n > poetx::kVocabMaxElems) return POETX_ERR_SHAPE;
   if (!real_type(d->dtype)) return POETX_ERR_DTYPE;
   return POETX_OK;
 }

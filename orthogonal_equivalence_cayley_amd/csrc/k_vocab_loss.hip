@@ -155,7 +155,7 @@ void vocab_tile_kernel(VocabArgs a) {
   extern __shared__ __align__(16) char lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
-  const int rows = (int)a.T, cols = MODE == DX ? a.n : a.vp;
+  const int rows = (int)(MODE == DX ? a.Td : a.T), cols = MODE == DX ? a.n : a.vp;
   int m0, n0;
   if (!tile_origin(rows, cols, BM, BN, m0, n0)) return;
   int k0 = 0, kend = MODE == DX ? a.vp : a.n;
@@ -357,27 +357,28 @@ __global__ __launch_bounds__(kThr) void vocab_join_kernel(VocabArgs a, int group
 }
 
 // Xm = X with zeros in ignored rows (a padded token's activations may be anything, and
-// 0 times infinity would reach dW), columns up to ldm and rows up to a.Tm zero too; d's rows
-// behind the last token as well, and its columns from vp to a multiple of 64
+// 0 times infinity would reach dW), once more below itself where d has two halves, columns
+// up to ldm and rows up to a.Tm zero too; d's rows behind the last as well, and its columns from vp to a multiple of 64
 template <typename E>
 __global__ __launch_bounds__(kThr) void vocab_mask_kernel(VocabArgs a) {
   constexpr int N = 16 / sizeof(E);
   const int nv = (int)(a.ldm / N);
   for (long long t = blockIdx.x; t < a.Tm; t += gridDim.x) {
-    const bool none = t >= a.T || a.target[t] == a.ignore;
-    const char* const from = static_cast<const char*>(a.X) + t * a.ldx * (long long)sizeof(E);
+    const long long r = t < a.T ? t : t - a.T;
+    const bool none = t >= a.Td || a.target[r] == a.ignore;
+    const char* const from = static_cast<const char*>(a.X) + r * a.ldx * (long long)sizeof(E);
     E* const to = static_cast<E*>(a.Xm) + t * a.ldm;
     for (int c = threadIdx.x; c < nv; c += kThr) {
       i32x4 v = {0, 0, 0, 0};
       if (!none) v = load16<sizeof(E)>(from, (long long)c * 16, (long long)a.n * sizeof(E));
       reinterpret_cast<i32x4*>(to)[c] = v;
     }
-    if (a.vp % 64 && t < a.T && threadIdx.x < 64) {
+    if (a.vp % 64 && t < a.Td && threadIdx.x < 64) {
       // behind a single piece's last column
       const int c = a.vp + (int)threadIdx.x;
       if (c < (a.vp + 63) / 64 * 64) static_cast<E*>(a.dS)[t * a.ldp + c] = E(0);
     }
-    if (t >= a.T) {
+    if (t >= a.Td) {
       i32x4* const d = reinterpret_cast<i32x4*>(static_cast<E*>(a.dS) + t * a.ldp);
       for (int c = threadIdx.x; c < (int)(a.ldp / N); c += kThr) d[c] = i32x4{0, 0, 0, 0};
     }
@@ -388,13 +389,13 @@ __global__ __launch_bounds__(kThr) void vocab_mask_kernel(VocabArgs a) {
 template <typename E>
 __global__ __launch_bounds__(kThr) void vocab_pad_kernel(VocabArgs a) {
   const int vz = (a.vp + 63) / 64 * 64;
-  for (long long i = (long long)blockIdx.x * kThr + threadIdx.x; i < a.T * 64; i += (long long)gridDim.x * kThr) {
+  for (long long i = (long long)blockIdx.x * kThr + threadIdx.x; i < a.Td * 64; i += (long long)gridDim.x * kThr) {
     const int c = a.vp + (int)(i & 63);
     if (c < vz) static_cast<E*>(a.dS)[(i >> 6) * a.ldp + c] = E(0);
   }
 }
 
-// dX = round(factor * the sum of the splits' parts)
+// dX = round(factor * the sum of the splits' parts, and of both halves of d)
 template <bool F32>
 __global__ __launch_bounds__(kThr) void vocab_finish_kernel(VocabArgs a) {
   const int quads = (a.n + 3) / 4;
@@ -404,10 +405,11 @@ __global__ __launch_bounds__(kThr) void vocab_finish_kernel(VocabArgs a) {
     const long long t = i / quads;
     const int c = (int)(i - t * quads) * 4;
     float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int z = 0; z < a.splits; ++z) {
-      const float4 b = *reinterpret_cast<const float4*>(a.acc + (z * a.T + t) * a.lda + c);
-      v = float4{v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w};
-    }
+    for (int z = 0; z < a.splits; ++z)
+      for (long long r = t; r < a.Td; r += a.T) {
+        const float4 b = *reinterpret_cast<const float4*>(a.acc + (z * a.Td + r) * a.lda + c);
+        v = float4{v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w};
+      }
     const float o[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
     put<F32>(a.GX, t * a.ldgx + c, o, a.n - c);
   }
@@ -424,7 +426,7 @@ hipError_t few(const VocabArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_pad(const VocabArgs& a, int bf16, hipStream_t s) {
-  const dim3 grid((unsigned)std::min<long long>((a.T + 3) / 4, 4096));
+  const dim3 grid((unsigned)std::min<long long>((a.Td + 3) / 4, 4096));
   if (bf16) hipLaunchKernelGGL((vocab_pad_kernel<uint16_t>), grid, dim3(kThr), 0, s, a);
   else hipLaunchKernelGGL((vocab_pad_kernel<float>), grid, dim3(kThr), 0, s, a);
   return hipGetLastError();
@@ -441,7 +443,7 @@ template <typename Ty, int BM, int BN, Mode M>
 hipError_t tiles(const VocabArgs& a, hipStream_t s) {
   const int cols = M == DX ? a.n : a.vp;
   hipLaunchKernelGGL((vocab_tile_kernel<Ty, BM, BN, M>),
-                     dim3((unsigned)tile_grid(a.T, cols, BM, BN), M == DX ? (unsigned)a.splits : 1u), dim3(kThr),
+                     dim3((unsigned)tile_grid(M == DX ? a.Td : a.T, cols, BM, BN), M == DX ? (unsigned)a.splits : 1u), dim3(kThr),
                      (2 * Tile<Ty, BM, BN, M>::STAGE), s, a);
   return hipGetLastError();
 }
@@ -518,6 +520,13 @@ VocabTiles tiles_of(long long rows, long long cols, long long sum, int bf16, boo
 }
 int group_cols(int tile) { return tile == VOCAB_TILE_128 || tile == VOCAB_TILE_256 ? 64 : 32; }
 
+// Up to this many tokens in bf16 the products take what d loses in rounding too, as rows of
+// their own: few d of a size share a result there, so that the rounding of one (a target's,
+// up to 2^-9 of it) shows as an error of whole rows of dX and dW, two and a half times what
+// rounding them does; more tokens, and the errors are as many as the results'. The memory
+// traffic, which bounds these sizes, hardly grows (64 x 2048 x 32000 backward XX us).
+constexpr long long kHalves = 64;
+
 constexpr long long kRoom = 256LL << 20;   // bytes that a part of the work may take as workspace
 size_t padded(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -586,7 +595,8 @@ hipError_t launch_vocab_forward(const VocabArgs& in, int bf16, void* ws, hipStre
 VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, bool gw) {
   VocabBackPlan p{};
   const int es = bf16 ? 2 : 4;
-  p.Tm = (T + 63) / 64 * 64;
+  p.Td = bf16 && T <= kHalves ? 2 * T : T;
+  p.Tm = (p.Td + 63) / 64 * 64;
   p.ldm = (n + 7) / 8 * 8;
   p.lda = (n + 3) / 4 * 4;
   // columns of a piece: those whose d leaves room, in whole tiles, the pieces alike
@@ -596,18 +606,18 @@ VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, 
   const int vp = std::min(p.vp, V);
   const bool one = V <= p.vp;
   // as the operands' alignment may lead: rows of whole 16 bytes or not
-  p.dx[0] = tiles_of(T, n, vp, bf16, false, false, true);
-  p.dx[1] = tiles_of(T, n, vp, bf16, true, bf16 && vocab_pipe_dx(T, n), true);
+  p.dx[0] = tiles_of(p.Td, n, vp, bf16, false, false, true);
+  p.dx[1] = tiles_of(p.Td, n, vp, bf16, true, bf16 && vocab_pipe_dx(p.Td, n), true);
   // shares none of which is empty in the first piece (the others only add to theirs)
   for (VocabTiles& d : p.dx) {
     const long long stages = (long long)((vp + 63) / 64 * 64) * es / 128, per = (stages + d.splits - 1) / d.splits;
     d.splits = (int)((stages + per - 1) / per);
   }
   const int splits = std::max(p.dx[0].splits, p.dx[1].splits);
-  p.acc = gx && (splits > 1 || !one);
+  p.acc = gx && (splits > 1 || !one || p.Td > T);
   p.at_x = padded((size_t)p.Tm * p.vp * es);
   p.at_acc = p.at_x + (gw ? padded((size_t)p.Tm * p.ldm * es) : 0);
-  p.bytes = p.at_acc + (p.acc ? padded((size_t)splits * T * p.lda * 4) : 0);
+  p.bytes = p.at_acc + (p.acc ? padded((size_t)splits * p.Td * p.lda * 4) : 0);
   return p;
 }
 
@@ -618,13 +628,14 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
   a.ldp = p.vp;
   a.Xm = static_cast<char*>(ws) + p.at_x;
   a.ldm = p.ldm;
+  a.Td = p.Td;
   a.Tm = p.Tm;
   a.lda = p.lda;
   const bool fast = vocab_ring_weight(a, bf16);
   const VocabTiles dx = p.dx[fast ? 1 : 0];
   const bool wide_dx = dx.tile == VOCAB_TILE_256;
   a.splits = dx.splits;
-  a.acc = a.splits > 1 || a.V > p.vp ? reinterpret_cast<float*>(static_cast<char*>(ws) + p.at_acc) : nullptr;
+  a.acc = a.splits > 1 || a.V > p.vp || a.Td > a.T ? reinterpret_cast<float*>(static_cast<char*>(ws) + p.at_acc) : nullptr;
   hipError_t e;
   if (a.GW) {
     a.vp = a.V <= p.vp ? a.V : p.vp;
@@ -655,7 +666,7 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
     }
     if (a.GW) {
       // both operands are this call's own: their rows are whole 16 bytes
-      const VocabTiles dw = tiles_of(a.vp, a.n, a.T, bf16, true, bf16 && vocab_pipe_dw(a));
+      const VocabTiles dw = tiles_of(a.vp, a.n, a.Td, bf16, true, bf16 && vocab_pipe_dw(a));
       e = dw.tile == VOCAB_TILE_256 ? launch_vocab_pipe_dw(a, s) : launch_vocab_ring_dw(a, bf16, dw.tile, s);
       if (e != hipSuccess) return e;
     }

@@ -117,7 +117,7 @@ void vocab_pipe_kernel(VocabArgs p) {
   // The operands: rows along the result's rows and columns, and the summed axis. Of d,
   // columns up to a multiple of 64 exist (zeros behind the piece's last).
   const int vz = (p.vp + 63) / 64 * 64;
-  const int rows = MODE == DW ? vz : (int)p.T;
+  const int rows = MODE == DW ? vz : (int)(MODE == DX ? p.Td : p.T);
   const int cols = MODE == STATS || MODE == GRAD ? p.vp : MODE == DX ? p.n : (int)p.ldm;
   const int sum = MODE == DX ? vz : MODE == DW ? (int)p.Tm : p.n;
   const char* const a_base = static_cast<const char*>(MODE == STATS || MODE == GRAD ? p.X : p.dS);
@@ -319,7 +319,7 @@ void vocab_pipe_kernel(VocabArgs p) {
   const float scale = MODE == DX || MODE == DW ? (p.g_each ? 1.0f : *p.g) : 1.0f;
   auto dx = [&](Acc (&acc)[4][2], int m0, int n0, int m1, int n1, int ti) __attribute__((always_inline)) {
     const bool first = p.v0 == 0, last = p.v0 + p.vp == p.V && p.splits == 1;
-    float* const sums = p.acc + share(ti) * p.T * p.lda;
+    float* const sums = p.acc + share(ti) * p.Td * p.lda;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const long long t = (long long)m0 + wm0 + i * 32 + cm;
@@ -470,7 +470,7 @@ void vocab_pipe_kernel(VocabArgs p) {
 
 template <Mode MODE>
 hipError_t launch(const VocabArgs& a, hipStream_t s) {
-  const long long rows = MODE == DW ? (a.vp + 63) / 64 * 64 : a.T;
+  const long long rows = MODE == DW ? (a.vp + 63) / 64 * 64 : MODE == DX ? a.Td : a.T;
   const long long cols = MODE == STATS || MODE == GRAD ? a.vp : MODE == DX ? a.n : a.ldm;
   const long long ntile = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile) * (MODE == DX ? a.splits : 1);
   // a multiple of 8, so that every XCD's range of tiles has its workgroups

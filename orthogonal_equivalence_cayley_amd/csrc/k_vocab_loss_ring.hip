@@ -132,7 +132,7 @@ void vocab_ring_kernel(VocabArgs p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave >> 1) * (BM / 2), wn = (wave & 1) * (BN / 2);
-  const int rows = MODE == DW ? p.vp : (int)p.T, cols = MODE == STATS || MODE == GRAD ? p.vp : p.n;
+  const int rows = MODE == DW ? p.vp : (int)(MODE == DX ? p.Td : p.T), cols = MODE == STATS || MODE == GRAD ? p.vp : p.n;
   int m0, n0;
   if (!tile_origin(rows, cols, BM, BN, m0, n0)) return;
   // d has zeros in its columns up to a multiple of 64 and in its rows up to Tm
@@ -216,7 +216,7 @@ void vocab_ring_kernel(VocabArgs p) {
 
 template <typename Ty, int BM, int BN, int NS, Mode MODE>
 hipError_t launch(const VocabArgs& a, hipStream_t s) {
-  const long long rows = MODE == DW ? a.vp : a.T;
+  const long long rows = MODE == DW ? a.vp : MODE == DX ? a.Td : a.T;
   const int cols = MODE == STATS || MODE == GRAD ? a.vp : a.n;
   const dim3 grid((unsigned)tile_grid(rows, cols, BM, BN), MODE == DX ? (unsigned)a.splits : 1u);
   constexpr int lds = NS * (BM + BN) * kKB;

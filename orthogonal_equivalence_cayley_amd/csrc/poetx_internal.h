@@ -371,9 +371,10 @@ struct VocabArgs {
   int g_each;
   void* GX; void* GW;               // each may be null
   long long ldgx, ldgw;
-  void* dS; long long ldp;          // Tm x ldp: dL/dz of a piece of the vocabulary
+  void* dS; long long ldp;          // Tm x ldp: dL/dz of a piece of the vocabulary,
+  long long Td;                     // T rows of it, or 2 T: what those lost in rounding below them
   void* Xm; long long ldm, Tm;      // Tm x ldm: X with zeros for ignored tokens and behind the last row and column
-  float* acc; long long lda;        // splits x T x lda parts of dX, or null: GX is written at once
+  float* acc; long long lda;        // splits x Td x lda parts of dX, or null: GX is written at once
   int splits;
   int v0, vp;                       // the piece: its first row of W and how many
 };
@@ -392,7 +393,7 @@ struct VocabPlan {
   size_t bytes;
 };
 struct VocabBackPlan {
-  long long Tm, ldm, lda;
+  long long Td, Tm, ldm, lda;
   int vp;
   VocabTiles dx[2];   // rows of no whole 16 bytes, and of whole ones
   bool acc;

@@ -146,6 +146,11 @@ __device__ __forceinline__ void epilogue(const VocabArgs& a, typename Ty::Acc (&
 #pragma unroll
         for (int v = 0; v < 4; ++v) d[v] = grad_of<F32>(r, acc[i][j][v], (long long)a.v0 + c + v);
         put<F32>(a.dS, t * a.ldp + c, d, cols - c);
+        if (!F32 && a.Td > a.T) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) d[v] -= (float)static_cast<__bf16>(d[v]);
+          put<F32>(a.dS, (t + a.T) * a.ldp + c, d, cols - c);
+        }
       }
     }
   } else {
@@ -160,7 +165,7 @@ __device__ __forceinline__ void epilogue(const VocabArgs& a, typename Ty::Acc (&
         if (c >= cols) continue;
         float o[4];
         if (MODE == DX && a.acc) {
-          float4* const to = reinterpret_cast<float4*>(a.acc + ((long long)share * a.T + t) * a.lda + c);
+          float4* const to = reinterpret_cast<float4*>(a.acc + ((long long)share * a.Td + t) * a.lda + c);
           float4 v = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
           if (a.v0 > 0) {
             const float4 b = *to;

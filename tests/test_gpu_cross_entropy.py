@@ -56,7 +56,8 @@ def reference(X, W, target, g, dt):
     d = p.clone()
     d[torch.arange(T, device=d.device), t] -= 1
     d, dp = d * counts[:, None], dp * counts[:, None]
-    half = HALF[dt] if dt == "bf16" else 0.0
+    # up to 64 tokens what d loses in rounding is multiplied as well
+    half = 0.0 if dt != "bf16" else HALF[dt] if T > 64 else 2.0 ** -17
     ed = dp + (half + 3 * U) * (d.abs() + dp)
     gd = g.double().expand(T)[:, None]
     gx, gw = (d * gd) @ w, (d * gd).T @ x
@@ -166,10 +167,11 @@ def test_nothing_is_lost(T, n, V, dt):
     import torch
     log(f"cross entropy exact T={T} n={n} V={V} {dt}")
     q = torch.tensor(1.0 / V, dtype=torch.float64).to(torch.bfloat16).double()
+    few = dt == "bf16" and T <= 64      # what d loses in rounding is multiplied as well
     # exp(-lse) is off by 2^-20 of itself at most: no border of bf16 that near
     for k in (1 - 2.0 ** -19, 1 + 2.0 ** -19):
         assert torch.tensor(k / V, dtype=torch.float64).float().to(torch.bfloat16).double() == q
-    if dt == "f32":
+    if dt == "f32" or few:
         q = torch.tensor(1.0 / V, dtype=torch.float64)
     g = gen(T + n + V)
     whole = torch.randint(1, 5, (max(T, V), n), generator=g).to(T_(dt))
@@ -186,7 +188,12 @@ def test_nothing_is_lost(T, n, V, dt):
     W2[star] = 0
     b = run(X2.cuda(), W2.cuda(), target.cuda(), one)
     want2 = (W2.double().sum(0) * q).expand(T, n)
-    if dt == "bf16":
+    if few:
+        # d to half a step of its second half, 2^-17, and exp as in fp32
+        tol = HALF[dt] + 2.0 ** -17 + (2 * math.log(V) + 100 + 2 * max(T, V)) * U
+        close("G_W", a["G_W"].cpu()[others], want, tol * want)
+        close("G_X", b["G_X"], want2, tol * want2)
+    elif dt == "bf16":
         # 8 bits times at most 4, in sums of less than 2^24 of their last place
         assert V * 4 * 255 < 2 ** 24
         assert torch.equal(b["G_X"].cpu(), want2.float().to(torch.bfloat16))

@@ -22,6 +22,7 @@
 #include <cmath>
 
 #include "linear_common.h"
+#include "row_common.h"
 #include "vocab_loss.h"
 
 namespace poetx {
@@ -395,25 +396,143 @@ __global__ __launch_bounds__(kThr) void vocab_pad_kernel(VocabArgs a) {
   }
 }
 
-// dX = round(factor * the sum of the splits' parts, and of both halves of d)
-template <bool F32>
+// dX = round(factor * the sum of the splits' parts, and of both halves of d), G threads to 4
+// columns of a row, each with every G-th part
+template <bool F32, int G>
 __global__ __launch_bounds__(kThr) void vocab_finish_kernel(VocabArgs a) {
-  const int quads = (a.n + 3) / 4;
+  __shared__ float4 red[G][kThr / G];
+  const int quads = (a.n + 3) / 4, lane = threadIdx.x % (kThr / G), grp = threadIdx.x / (kThr / G);
   const float scale = a.g_each ? 1.0f : *a.g;
   const long long count = a.T * quads;
-  for (long long i = (long long)blockIdx.x * kThr + threadIdx.x; i < count; i += (long long)gridDim.x * kThr) {
-    const long long t = i / quads;
-    const int c = (int)(i - t * quads) * 4;
+  const int halves = a.Td > a.T ? 2 : 1, parts = a.splits * halves;
+  for (long long i0 = (long long)blockIdx.x * (kThr / G); i0 < count; i0 += (long long)gridDim.x * (kThr / G)) {
+    const long long i = i0 + lane;
+    const bool in = i < count;
+    const long long t = in ? i / quads : 0;
+    const int c = in ? (int)(i - t * quads) * 4 : 0;
     float4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int z = 0; z < a.splits; ++z)
-      for (long long r = t; r < a.Td; r += a.T) {
-        const float4 b = *reinterpret_cast<const float4*>(a.acc + (z * a.Td + r) * a.lda + c);
+    if (in) {
+#pragma unroll 4
+      for (int z = grp; z < parts; z += G) {
+        const long long row = (z / halves) * a.Td + t + (z % halves) * a.T;
+        const float4 b = *reinterpret_cast<const float4*>(a.acc + row * a.lda + c);
         v = float4{v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w};
       }
-    const float o[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
-    put<F32>(a.GX, t * a.ldgx + c, o, a.n - c);
+    }
+    if constexpr (G > 1) {
+      red[grp][lane] = v;
+      __syncthreads();
+      if (grp == 0) {
+#pragma unroll
+        for (int k = 1; k < G; ++k) {
+          const float4 b = red[k][lane];
+          v = float4{v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w};
+        }
+      }
+      __syncthreads();
+    }
+    if (grp == 0 && in) {
+      const float o[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+      put<F32>(a.GX, t * a.ldgx + c, o, a.n - c);
+    }
   }
 }
+template <bool F32>
+hipError_t finish(const VocabArgs& a, hipStream_t s) {
+  const long long quads = a.T * ((a.n + 3) / 4);
+  // few results of many parts leave the CUs idle otherwise (20 x 1001, 64 parts 20 -> 5 us)
+  if (quads < 65536 && a.splits * (a.Td > a.T ? 2 : 1) >= 16) {
+    const dim3 grid((unsigned)std::min<long long>((quads + 15) / 16, 1 << 16));
+    hipLaunchKernelGGL((vocab_finish_kernel<F32, 16>), grid, dim3(kThr), 0, s, a);
+  } else {
+    const dim3 grid((unsigned)std::min<long long>((quads + kThr - 1) / kThr, 1 << 16));
+    hipLaunchKernelGGL((vocab_finish_kernel<F32, 1>), grid, dim3(kThr), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+// d W and d^T X of the fewest fp32 tokens, at most TD, in one pass over W: a thread has 4
+// columns of X in registers and goes down `per` rows of W, whose d are the same for all of its
+// workgroup's; each chunk of rows leaves its part of dX. Bound by memory, W read and dW written
+// (8 x 1024 x 32000 52 us, 5.0 TB/s; in tiles 98; rows of no whole 16 bytes 142 against 299).
+// Not for bf16, whose d come in two halves, and for twice as many columns a thread: 4 x 2048 x
+// 32000 134 us against 57 in tiles.
+template <int TD>
+__global__ __launch_bounds__(kThr) void vocab_outer_kernel(VocabArgs a, int per) {
+  constexpr int N = 4, U = 4;   // U rows' loads out at a time
+  constexpr int kRows = 64;     // of d in LDS at a time
+  __shared__ __align__(16) float ds[kRows][TD];
+  const int c = ((int)blockIdx.x * kThr + (int)threadIdx.x) * N, left = a.n - c;
+  const bool in = left > 0;
+  const int first = (int)blockIdx.y * per, end = min(first + per, a.vp);
+  const float scale = a.g_each ? 1.0f : *a.g;
+  float x[TD][N] = {}, acc[TD][N] = {};
+#pragma unroll
+  for (int t = 0; t < TD; ++t)
+    // a padded token's activations may be anything
+    if (t < a.T && in && a.target[t] != a.ignore)
+      row::load_raw<false>(static_cast<const float*>(a.X) + t * a.ldx + c, left, true, x[t]);
+  const float* const w = static_cast<const float*>(a.W) + (long long)a.v0 * a.ldw + c;
+  float* const gw = a.GW ? static_cast<float*>(a.GW) + (long long)a.v0 * a.ldgw + c : nullptr;
+  for (int v0 = first; v0 < end; v0 += kRows) {
+    const int rows = min(kRows, end - v0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * TD; i += kThr) {
+      const int t = i / kRows, v = i % kRows;
+      ds[v][t] = t < a.T && v < rows ? static_cast<const float*>(a.dS)[t * a.ldp + v0 + v] : 0.0f;
+    }
+    __syncthreads();
+    if (!in) continue;
+    for (int v = 0; v < rows; v += U) {
+      float wv[U][N] = {};
+      if (a.GX) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          row::load_raw<false>(w + (long long)(v0 + min(v + u, rows - 1)) * a.ldw, left, true, wv[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (v + u >= rows) break;
+        float o[N] = {};
+#pragma unroll
+        for (int t = 0; t < TD; ++t) {
+          const float d = ds[v + u][t];
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            acc[t][e] = fmaf(d, wv[u][e], acc[t][e]);
+            o[e] = fmaf(d, x[t][e], o[e]);
+          }
+        }
+        if (gw) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) o[e] *= scale;
+          row::store_raw<false>(gw + (long long)(v0 + v + u) * a.ldgw, left, o);
+        }
+      }
+    }
+  }
+  if (!a.GX || !in) return;
+  float* const to = a.acc + (long long)blockIdx.y * a.Td * a.lda + c;
+#pragma unroll
+  for (int t = 0; t < TD; ++t) {
+    if (t >= a.T) break;
+    // whole vectors: lda is a multiple of 4
+    float4* const at = reinterpret_cast<float4*>(to + t * a.lda);
+    float4 v = {acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
+    if (a.v0 > 0) v = float4{v.x + at->x, v.y + at->y, v.z + at->z, v.w + at->w};
+    *at = v;
+  }
+}
+hipError_t outer(const VocabArgs& a, const VocabBackPlan& p, hipStream_t s) {
+  const int per = (std::min<int>(p.vp, a.V) + p.chunks - 1) / p.chunks;
+  const dim3 grid((unsigned)((a.n + kThr * 4 - 1) / (kThr * 4)), (unsigned)p.chunks);
+  if (a.T <= 2) hipLaunchKernelGGL((vocab_outer_kernel<2>), grid, dim3(kThr), 0, s, a, per);
+  else if (a.T <= 4) hipLaunchKernelGGL((vocab_outer_kernel<4>), grid, dim3(kThr), 0, s, a, per);
+  else hipLaunchKernelGGL((vocab_outer_kernel<8>), grid, dim3(kThr), 0, s, a, per);
+  return hipGetLastError();
+}
+// Tokens up to which, and columns from which, it is taken
+constexpr int kOuter = 8, kOuterCols = 4 * kThr;
 
 template <typename Ty, int TT>
 hipError_t few(const VocabArgs& a, hipStream_t s) {
@@ -524,7 +643,7 @@ int group_cols(int tile) { return tile == VOCAB_TILE_128 || tile == VOCAB_TILE_2
 // their own: few d of a size share a result there, so that the rounding of one (a target's,
 // up to 2^-9 of it) shows as an error of whole rows of dX and dW, two and a half times what
 // rounding them does; more tokens, and the errors are as many as the results'. The memory
-// traffic, which bounds these sizes, hardly grows (64 x 2048 x 32000 backward XX us).
+// traffic, which bounds these sizes, hardly grows (64 x 2048 x 32000 backward 124 -> 131 us).
 constexpr long long kHalves = 64;
 
 constexpr long long kRoom = 256LL << 20;   // bytes that a part of the work may take as workspace
@@ -613,10 +732,18 @@ VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, 
     const long long stages = (long long)((vp + 63) / 64 * 64) * es / 128, per = (stages + d.splits - 1) / d.splits;
     d.splits = (int)((stages + per - 1) / per);
   }
-  const int splits = std::max(p.dx[0].splits, p.dx[1].splits);
-  p.acc = gx && (splits > 1 || !one || p.Td > T);
+  int splits = std::max(p.dx[0].splits, p.dx[1].splits);
+  p.outer = !bf16 && T <= kOuter && n >= kOuterCols;
+  if (p.outer) {
+    // enough workgroups, whose parts of dX stay an eighth of W
+    const long long wide = (n + kOuterCols - 1) / kOuterCols;
+    const long long want = std::max(1LL, std::min({2048 / wide, vp / (8 * T), (vp + 63LL) / 64}));
+    const long long per = (vp + want - 1) / want;
+    splits = p.chunks = (int)((vp + per - 1) / per);
+  }
+  p.acc = gx && (p.outer || splits > 1 || !one || p.Td > T);
   p.at_x = padded((size_t)p.Tm * p.vp * es);
-  p.at_acc = p.at_x + (gw ? padded((size_t)p.Tm * p.ldm * es) : 0);
+  p.at_acc = p.at_x + (gw && !p.outer ? padded((size_t)p.Tm * p.ldm * es) : 0);
   p.bytes = p.at_acc + (p.acc ? padded((size_t)splits * p.Td * p.lda * 4) : 0);
   return p;
 }
@@ -634,10 +761,10 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
   const bool fast = vocab_ring_weight(a, bf16);
   const VocabTiles dx = p.dx[fast ? 1 : 0];
   const bool wide_dx = dx.tile == VOCAB_TILE_256;
-  a.splits = dx.splits;
-  a.acc = a.splits > 1 || a.V > p.vp || a.Td > a.T ? reinterpret_cast<float*>(static_cast<char*>(ws) + p.at_acc) : nullptr;
+  a.splits = p.outer ? p.chunks : dx.splits;
+  a.acc = p.outer || a.splits > 1 || a.V > p.vp || a.Td > a.T ? reinterpret_cast<float*>(static_cast<char*>(ws) + p.at_acc) : nullptr;
   hipError_t e;
-  if (a.GW) {
+  if (a.GW && !p.outer) {
     a.vp = a.V <= p.vp ? a.V : p.vp;
     const dim3 grid((unsigned)std::min<long long>(a.Tm, 1 << 16));
     if (bf16) hipLaunchKernelGGL((vocab_mask_kernel<uint16_t>), grid, dim3(kThr), 0, s, a);
@@ -654,6 +781,11 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
         : fast_logits               ? launch_vocab_ring_grad(a, bf16, grad.tile, s)
                                     : tiles<GRAD>(a, bf16, grad.tile, s);
     if (e != hipSuccess) return e;
+    if (p.outer) {
+      e = outer(a, p, s);
+      if (e != hipSuccess) return e;
+      continue;
+    }
     if (a.GX) {
       if (fast && a.vp % 64 && (!a.GW || a.v0 > 0)) {
         e = launch_pad(a, bf16, s);
@@ -672,12 +804,8 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
     }
   }
   // the last piece of an unshared dX in 256 x 256 tiles writes it whole
-  if (!a.GX || !a.acc || (wide_dx && a.splits == 1)) return hipSuccess;
-  const long long quads = a.T * ((a.n + 3) / 4);
-  const dim3 grid((unsigned)std::min<long long>((quads + kThr - 1) / kThr, 1 << 16));
-  if (bf16) hipLaunchKernelGGL((vocab_finish_kernel<false>), grid, dim3(kThr), 0, s, a);
-  else hipLaunchKernelGGL((vocab_finish_kernel<true>), grid, dim3(kThr), 0, s, a);
-  return hipGetLastError();
+  if (!a.GX || !a.acc || (wide_dx && a.splits == 1 && !p.outer)) return hipSuccess;
+  return bf16 ? finish<false>(a, s) : finish<true>(a, s);
 }
 
 }  // namespace poetx

@@ -396,7 +396,8 @@ struct VocabBackPlan {
   long long Td, Tm, ldm, lda;
   int vp;
   VocabTiles dx[2];   // rows of no whole 16 bytes, and of whole ones
-  bool acc;
+  bool outer, acc;    // outer: the fewest fp32 tokens, by chunks of W's rows
+  int chunks;
   size_t at_x, at_acc, bytes;
 };
 constexpr int kVocabMax = 1 << 24;        // tokens of a call, rows of W

@@ -89,7 +89,8 @@ def compare(got, want):
 # tokens, width, vocabulary: single ones, each tile's edges, ragged rows, several pieces
 SIZES = [(1, 1, 1), (1, 7, 2), (3, 5, 63), (1, 64, 1000), (2, 100, 257), (4, 1001, 333), (5, 64, 5003), (33, 40, 130),
          (64, 256, 512), (65, 129, 129), (130, 72, 1000), (200, 1000, 700), (257, 64, 4099), (600, 130, 2049),
-         (1031, 96, 300), (300, 512, 2600)]
+         (1031, 96, 300), (300, 512, 2600), (1, 1030, 900), (2, 1024, 65), (4, 2049, 500), (7, 1100, 1000), (8, 3001, 300),
+         (9, 1024, 200)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])

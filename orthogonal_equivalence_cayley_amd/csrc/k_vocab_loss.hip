@@ -606,9 +606,10 @@ constexpr TileCost kTiles[] = {{VOCAB_TILE_128, 128, 128, 27, 22, 6}, {VOCAB_TIL
                                {VOCAB_TILE_32x64, 32, 64, 20, 15, 1.5}};
 constexpr TileCost kTilesF32[] = {{VOCAB_TILE_128x64, 128, 64, 51, 42, 5}, {VOCAB_TILE_64, 64, 64, 32, 24, 2.5},
                                   {VOCAB_TILE_32x64, 32, 64, 25, 18, 2}};
-// d W in the ring's tiles, whose reads across the sum keep fewer loads in flight: 4000 x 256
-// x 13568 bf16 66 us in 64 x 64 against 50 in shared 256 x 256 tiles
-constexpr double kAcross = 1.5;
+// d W in the ring's tiles, whose loads and reads across the sum do not overlap as well, most
+// of all for a workgroup alone on its CU: 1003 x 1000 x 10007 bf16 49 us in 256 tiles of 64 x
+// 64, 35 + 5 in 512 shares of tiles of 128 x 64
+constexpr double kAcrossFirst = 1.5, kAcrossRound = 1.1;
 
 template <size_t N>
 VocabTiles cheapest(const TileCost (&costs)[N], long long rows, long long cols, long long stages, bool wide, bool share) {
@@ -620,10 +621,11 @@ VocabTiles cheapest(const TileCost (&costs)[N], long long rows, long long cols, 
       const long long per = (stages + splits - 1) / splits, items = n * splits;
       if (splits > 1 && (per < 4 || items > 512)) break;
       // shares are written and read once more, by another launch
-      const double extra = splits > 1 ? 4 + 2e-6 * (double)splits * (double)(rows * cols) : 0.0;
+      const double extra = splits > 1 ? 3 + 1e-6 * (double)splits * (double)(rows * cols) : 0.0;
       const double rounds = (double)((items + 255) / 256);
-      const double time = std::max(c.first, c.round * rounds) * (double)per / 32;
-      const double cost = time * (share && c.tile != VOCAB_TILE_256 ? kAcross : 1.0) + c.ends * rounds + 3 + extra;
+      const bool across = share && c.tile != VOCAB_TILE_256;
+      const double time = std::max(c.first * (across ? kAcrossFirst : 1.0), c.round * rounds * (across ? kAcrossRound : 1.0));
+      const double cost = time * (double)per / 32 + c.ends * rounds + 3 + extra;
       if (best.tile < 0 || cost < best.cost) best = VocabTiles{c.tile, splits, cost};
     }
   }

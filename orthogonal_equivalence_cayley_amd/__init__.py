@@ -16,4 +16,5 @@ from .layer import PoetxLayer, build_many, param_grad_many  # noqa: F401
 
 __all__ = ["poetx", "PoetxLayer", "build_many", "param_grad_many", "add_rms_norm",
            "add_rms_norm_backward", "add_layer_norm", "add_layer_norm_backward", "dropout",
-           "dropout_backward", "linear_cross_entropy", "linear_cross_entropy_backward", "linear", "MergedLinear", "clip_grads"]
+           "dropout_backward", "linear_cross_entropy", "linear_cross_entropy_backward", "linear",
+           "MergedLinear", "clip_grads"]

@@ -1,5 +1,5 @@
 // What the kernels of the vocabulary's cross entropy share (k_vocab_loss.hip,
-// k_vocab_loss_pipe.hip): the parts of their epilogues.
+// k_vocab_loss_pipe.hip, k_vocab_loss_ring.hip): loads to LDS, the parts of their epilogues.
 #pragma once
 
 #include "linear_common.h"

@@ -653,6 +653,30 @@ int group_cols(int tile) { return tile == VOCAB_TILE_128 || tile == VOCAB_TILE_2
 // traffic, which bounds these sizes, hardly grows (64 x 2048 x 32000 backward 124 -> 131 us).
 constexpr long long kHalves = 64;
 
+// Into how many shares the sum of d W goes where it and d^T X are one launch of 256 x 256
+// tiles, one to a CU; 0 where one launch after the other is as fast, or their tiles are more
+// than the CUs. 1003 x 1000 x 10007 bf16 55 us and 6 for joining the shares, one after the
+// other 35 + 30 and 5; 2048 x 1024 x 8192 60 + 8 against 39 + 47 + 12, 300 x 512 x 5000 21 + 4
+// against 9 + 13 + 3.
+int shares_of_both(const VocabBackPlan& p, int vp, int n) {
+  const long long tx = ((p.Td + 255) / 256) * ((n + 255) / 256), tw = ((vp + 255LL) / 256) * ((p.ldm + 255) / 256);
+  const long long sx = (vp + 63) / 64, sw = p.Tm / 64, left = 256 - (tw + 7) / 8 * 8;
+  const TileCost& c = kRing[0];
+  double best = p.dx[1].cost + tiles_of(vp, n, p.Td, 1, true, true).cost;
+  int shares = 0;
+  for (int s = 1; s <= 64 && (tx * s + 7) / 8 * 8 <= left; ++s) {
+    const long long per = (sx + s - 1) / s;
+    if (s > 1 && per < 4) break;
+    const double extra = s > 1 ? 3 + 1e-6 * (double)s * (double)(p.Td * n) : 0.0;
+    const double cost = c.first * (double)std::max(per, sw) / 32 + c.ends + 3 + extra;
+    if (cost < best) {
+      best = cost;
+      shares = (int)((sx + per - 1) / per);
+    }
+  }
+  return shares;
+}
+
 constexpr long long kRoom = 256LL << 20;   // bytes that a part of the work may take as workspace
 size_t padded(size_t b) { return (b + 255) / 256 * 256; }
 
@@ -739,7 +763,8 @@ VocabBackPlan vocab_backward_plan(long long T, int V, int n, int bf16, bool gx, 
     const long long stages = (long long)((vp + 63) / 64 * 64) * es / 128, per = (stages + d.splits - 1) / d.splits;
     d.splits = (int)((stages + per - 1) / per);
   }
-  int splits = std::max(p.dx[0].splits, p.dx[1].splits);
+  if (bf16 && gx && gw && one && vocab_pipe_dx(p.Td, n) && vp >= 256) p.both = shares_of_both(p, vp, n);
+  int splits = std::max({p.dx[0].splits, p.dx[1].splits, p.both});
   p.outer = !bf16 && T <= kOuter && n >= kOuterCols;
   if (p.outer) {
     // enough workgroups, whose parts of dX stay an eighth of W
@@ -767,8 +792,8 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
   a.lda = p.lda;
   const bool fast = vocab_ring_weight(a, bf16);
   const VocabTiles dx = p.dx[fast ? 1 : 0];
-  const bool wide_dx = dx.tile == VOCAB_TILE_256;
-  a.splits = p.outer ? p.chunks : dx.splits;
+  const bool both = fast && p.both > 0, wide_dx = both || dx.tile == VOCAB_TILE_256;
+  a.splits = p.outer ? p.chunks : both ? p.both : dx.splits;
   a.acc = p.outer || a.splits > 1 || a.V > p.vp || a.Td > a.T ? reinterpret_cast<float*>(static_cast<char*>(ws) + p.at_acc) : nullptr;
   hipError_t e;
   if (a.GW && !p.outer) {
@@ -790,6 +815,12 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
     if (e != hipSuccess) return e;
     if (p.outer) {
       e = outer(a, p, s);
+      if (e != hipSuccess) return e;
+      continue;
+    }
+    if (both) {
+      // (one piece: vocab_mask_kernel has written the zeros behind d)
+      e = launch_vocab_pipe_both(a, s);
       if (e != hipSuccess) return e;
       continue;
     }

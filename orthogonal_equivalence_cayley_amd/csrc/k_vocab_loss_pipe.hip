@@ -108,9 +108,9 @@ struct Side<true> {
 // TAIL: the last stage of a sum is cut, for n (STATS, GRAD) or the piece of the vocabulary
 // (DX) is no multiple of 64 (a branch around the loads parts the products from the reads
 // beside them, so it has its own kernel)
+// What workgroup `block` of `blocks` does of a product
 template <Mode MODE, bool TAIL>
-__global__ __launch_bounds__(kThr) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void vocab_pipe_kernel(VocabArgs p) {
+__device__ __forceinline__ void vocab_pipe(const VocabArgs& p, int block, int blocks) {
   constexpr bool AX = MODE == DW, BX = MODE == DX || MODE == DW;   // across the summed axis
   extern __shared__ __align__(16) unsigned char lds[];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -134,12 +134,12 @@ void vocab_pipe_kernel(VocabArgs p) {
   const int per = MODE == DX ? (nk_all + p.splits - 1) / p.splits : nk_all;
   const int shares = MODE == DX ? (nk_all + per - 1) / per : 1;
 
-  // XCD x = blockIdx.x % 8 owns the tiles [ntile x / 8, ntile (x + 1) / 8), walked by its
+  // XCD x = block % 8 owns the tiles [ntile x / 8, ntile (x + 1) / 8), walked by its
   // workgroups with a stride of their count, in groups of kGroupRows tile-rows
   const int tn = (cols + kTile - 1) / kTile, tm = (rows + kTile - 1) / kTile;
   const int ntile = tn * tm * shares;
-  const int x = blockIdx.x % 8, sx = blockIdx.x / 8;
-  const int nx = (int)gridDim.x / 8 + (x < (int)gridDim.x % 8 ? 1 : 0);
+  const int x = block % 8, sx = block / 8;
+  const int nx = blocks / 8 + (x < blocks % 8 ? 1 : 0);
   const int t_first = (int)((long long)ntile * x / 8) + sx, t_end = (int)((long long)ntile * (x + 1) / 8);
   const int t_count = t_first < t_end ? (t_end - t_first + nx - 1) / nx : 0;
   if (t_count == 0) return;
@@ -472,13 +472,31 @@ void vocab_pipe_kernel(VocabArgs p) {
   vm_wait<0>();
 }
 
+template <Mode MODE, bool TAIL>
+__global__ __launch_bounds__(kThr) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void vocab_pipe_kernel(VocabArgs p) {
+  vocab_pipe<MODE, TAIL>(p, (int)blockIdx.x, (int)gridDim.x);
+}
+// d W by the first `first` workgroups and d^T X by the others, where a launch of each would
+// leave CUs idle
+template <bool TAIL>
+__global__ __launch_bounds__(kThr) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void vocab_pipe_both_kernel(VocabArgs p, int first) {
+  if ((int)blockIdx.x < first) vocab_pipe<DX, TAIL>(p, (int)blockIdx.x, first);
+  else vocab_pipe<DW, false>(p, (int)blockIdx.x - first, (int)gridDim.x - first);
+}
+
+// Tiles of a product, and workgroups for them: a multiple of 8, so that every XCD's range of
+// tiles has its own
 template <Mode MODE>
-hipError_t launch(const VocabArgs& a, hipStream_t s) {
+long long tiles_for(const VocabArgs& a) {
   const long long rows = MODE == DW ? (a.vp + 63) / 64 * 64 : MODE == DX ? a.Td : a.T;
   const long long cols = MODE == STATS || MODE == GRAD ? a.vp : MODE == DX ? a.n : a.ldm;
-  const long long ntile = ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile) * (MODE == DX ? a.splits : 1);
-  // a multiple of 8, so that every XCD's range of tiles has its workgroups
-  const long long grid = std::min<long long>((ntile + 7) / 8 * 8, 256);
+  return ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile) * (MODE == DX ? a.splits : 1);
+}
+template <Mode MODE>
+hipError_t launch(const VocabArgs& a, hipStream_t s) {
+  const long long grid = std::min<long long>((tiles_for<MODE>(a) + 7) / 8 * 8, 256);
   const bool tail = MODE == DX ? a.vp % kKE != 0 : MODE != DW && a.n % kKE != 0;
   if (tail)
     hipLaunchKernelGGL((vocab_pipe_kernel<MODE, MODE != DW>), dim3((unsigned)grid), dim3(kThr), kLds, s, a);
@@ -502,5 +520,11 @@ hipError_t launch_vocab_pipe_stats(const VocabArgs& a, hipStream_t s) { return l
 hipError_t launch_vocab_pipe_grad(const VocabArgs& a, hipStream_t s) { return launch<GRAD>(a, s); }
 hipError_t launch_vocab_pipe_dx(const VocabArgs& a, hipStream_t s) { return launch<DX>(a, s); }
 hipError_t launch_vocab_pipe_dw(const VocabArgs& a, hipStream_t s) { return launch<DW>(a, s); }
+hipError_t launch_vocab_pipe_both(const VocabArgs& a, hipStream_t s) {
+  const unsigned first = (unsigned)((tiles_for<DX>(a) + 7) / 8 * 8), rest = (unsigned)((tiles_for<DW>(a) + 7) / 8 * 8);
+  if (a.vp % kKE) hipLaunchKernelGGL((vocab_pipe_both_kernel<true>), dim3(first + rest), dim3(kThr), kLds, s, a, (int)first);
+  else hipLaunchKernelGGL((vocab_pipe_both_kernel<false>), dim3(first + rest), dim3(kThr), kLds, s, a, (int)first);
+  return hipGetLastError();
+}
 
 }  // namespace poetx

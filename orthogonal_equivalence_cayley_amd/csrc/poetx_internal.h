@@ -396,6 +396,7 @@ struct VocabBackPlan {
   long long Td, Tm, ldm, lda;
   int vp;
   VocabTiles dx[2];   // rows of no whole 16 bytes, and of whole ones
+  int both;           // shares of d W's tiles in one launch with d^T X; 0: one after the other
   bool outer, acc;    // outer: the fewest fp32 tokens, by chunks of W's rows
   int chunks;
   size_t at_x, at_acc, bytes;
@@ -417,6 +418,7 @@ hipError_t launch_vocab_pipe_stats(const VocabArgs& a, hipStream_t s);
 hipError_t launch_vocab_pipe_grad(const VocabArgs& a, hipStream_t s);
 hipError_t launch_vocab_pipe_dx(const VocabArgs& a, hipStream_t s);
 hipError_t launch_vocab_pipe_dw(const VocabArgs& a, hipStream_t s);
+hipError_t launch_vocab_pipe_both(const VocabArgs& a, hipStream_t s);   // d W and d^T X in one launch
 // smaller tiles with a ring of LDS stages (k_vocab_loss_ring.hip), rows of whole 16 bytes
 bool vocab_ring_logits(const VocabArgs& a, int bf16);   // X's and W's
 bool vocab_ring_weight(const VocabArgs& a, int bf16);   // W's

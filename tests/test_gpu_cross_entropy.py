@@ -151,6 +151,31 @@ def test_many_tokens(T, n, V):
     compare(b, {k: (v.cpu(), e.cpu()) for k, (v, e) in reference(Xc, Wc, tc, one.cuda(), "bf16").items()})
 
 
+# few tiles of 256 x 256, whose two gradients are one launch: each axis's edges, sums shared by few and by many
+@pytest.mark.parametrize("T, n, V", [(256, 256, 256), (257, 264, 300), (512, 1024, 2000), (300, 512, 5000),
+                                     (1003, 1000, 1009), (1031, 520, 4160)])
+def test_both_gradients_of_few_tiles(T, n, V):
+    import torch
+    log(f"cross entropy, both gradients of few tiles T={T} n={n} V={V}")
+    X, W, target, g = inputs(T, n, V, "bf16", seed=3)
+    each = torch.rand(T, generator=g) + 0.1
+    # what a padded token holds is nobody's business
+    pad = target == IGNORE
+    junk = X.clone()
+    junk[pad] = float("nan")
+    Xc, Wc, tc, gc = X.cuda(), strided(W, 8), target.cuda(), each.cuda()
+    a = run(Xc, Wc, tc, gc)
+    compare(a, reference(X, W, target, each, "bf16"))
+    b = run(junk.cuda(), Wc, tc, gc)
+    for k in ("G_X", "G_W"):
+        assert torch.equal(a[k], b[k])
+    # into places with rows a stride apart, whose gaps stay as they were
+    gx, gw = torch.full((T, n + 8), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((V, n + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+    run(Xc, Wc, tc, gc, G_X=gx[:, :n], G_W=gw[:, :n])
+    assert torch.equal(gx[:, :n], a["G_X"]) and torch.equal(gw[:, :n], a["G_W"])
+    assert (gx[:, n:] == 7).all() and (gw[:, n:] == 7).all()
+
+
 def run_back(X, W, target, lse, g, **kw):
     import orthogonal_equivalence_cayley_amd as oec
     return oec.linear_cross_entropy_backward(g.cuda(), X, W, target, lse, ignore_index=IGNORE, **kw)

@@ -644,7 +644,28 @@ VocabTiles tiles_of(long long rows, long long cols, long long sum, int bf16, boo
   }
   return bf16 ? cheapest(kTiles, rows, cols, stages, false, share) : cheapest(kTilesF32, rows, cols, stages, false, share);
 }
+// Of a product's columns in 256 x 256 tiles those that make whole rounds of the CUs, where the
+// others in smaller tiles (`rest`), a launch of their own, take less than one more round: 2048 x
+// 4096 x 50021, 1568 tiles, 641 us, in one launch 681. All of them where not.
+int whole_rounds(long long rows, int cols, int n, int& rest) {
+  const long long tm = (rows + 255) / 256, tn = (cols + 255LL) / 256, full = tm * tn / 256 * 256 / tm;
+  if (full < 1 || full >= tn) return cols;
+  const int main = (int)full * 256;
+  const long long stages = (2LL * n + 127) / 128;
+  const TileCost& c = kRing[0];
+  const double round = c.round * (double)stages / 32 + c.ends;
+  const VocabTiles r = cheapest(kRing, rows, cols - main, stages, false, false);
+  if ((double)((tm * full + 255) / 256) * round + 3 + r.cost >= (double)((tm * tn + 255) / 256) * round) return cols;
+  rest = r.tile;
+  return main;
+}
 int group_cols(int tile) { return tile == VOCAB_TILE_128 || tile == VOCAB_TILE_256 ? 64 : 32; }
+
+// Parts of a row: 256-column tiles leave those of whole tiles
+int groups_of(const VocabPlan& p, int tile, int V) {
+  if (tile != VOCAB_TILE_256) return (V + group_cols(tile) - 1) / group_cols(tile);
+  return (p.main + 255) / 256 * 4 + (p.main < V ? (V - p.main + group_cols(p.rest) - 1) / group_cols(p.rest) : 0);
+}
 
 // Up to this many tokens in bf16 the products take what d loses in rounding too, as rows of
 // their own: few d of a size share a result there, so that the rounding of one (a target's,
@@ -696,8 +717,8 @@ VocabPlan vocab_forward_plan(long long T, int V, int n, int bf16) {
   p.lay[1] = tiles_of(T, V, n, bf16, true, false);
   p.lay[2] = tiles_of(T, V, n, bf16, true, bf16 && T >= 256 && V >= 256);
   p.groups = T <= kFew ? (V + kFewGroup - 1) / kFewGroup : 0;
-  for (const VocabTiles& l : p.lay)   // 256-column tiles leave parts of whole tiles
-    p.groups = std::max(p.groups, l.tile == VOCAB_TILE_256 ? (V + 255) / 256 * 4 : (V + group_cols(l.tile) - 1) / group_cols(l.tile));
+  p.main = p.lay[2].tile == VOCAB_TILE_256 ? whole_rounds(T, V, n, p.rest) : V;
+  for (const VocabTiles& l : p.lay) p.groups = std::max(p.groups, groups_of(p, l.tile, V));
   // tokens of a launch: as many as their parts leave room for, and their tiles can be counted
   const long long most = std::min(kRoom / (8LL * p.groups), (1LL << 33) / V);
   p.rows = std::min(T, std::max(256LL, most / 256 * 256));
@@ -720,14 +741,22 @@ hipError_t launch_vocab_forward(const VocabArgs& in, int bf16, void* ws, hipStre
     a.v0 = 0;
     a.vp = a.V;
     const VocabTiles& lay = p.lay[!vocab_ring_logits(a, bf16) ? 0 : bf16 && vocab_pipe_logits(a) ? 2 : 1];
-    int groups = (a.V + group_cols(lay.tile) - 1) / group_cols(lay.tile);
+    int groups = groups_of(p, lay.tile, a.V);
+    a.groups = groups;
     hipError_t e;
     if (in.T <= kFew) {
       groups = (a.V + kFewGroup - 1) / kFewGroup;
       e = bf16 ? few<TypeBf16>(a, s) : few<TypeF32>(a, s);
     } else if (lay.tile == VOCAB_TILE_256) {
-      groups = (a.V + 255) / 256 * 4;
+      a.vp = p.main;
       e = launch_vocab_pipe_stats(a, s);
+      if (e == hipSuccess && p.main < a.V) {
+        VocabArgs b = a;
+        b.v0 = p.main;
+        b.vp = a.V - p.main;
+        b.group0 = p.main / 64;
+        e = launch_vocab_ring_stats(b, bf16, p.rest, s);
+      }
     } else {
       e = &lay == &p.lay[0] ? tiles<STATS>(a, bf16, lay.tile, s) : launch_vocab_ring_stats(a, bf16, lay.tile, s);
     }
@@ -809,9 +838,20 @@ hipError_t launch_vocab_backward(const VocabArgs& in, int bf16, void* ws, hipStr
     a.vp = (int)std::min<long long>(p.vp, a.V - v);
     const bool fast_logits = vocab_ring_logits(a, bf16);
     const VocabTiles grad = tiles_of(a.T, a.vp, a.n, bf16, fast_logits, bf16 && vocab_pipe_logits(a));
-    e = grad.tile == VOCAB_TILE_256 ? launch_vocab_pipe_grad(a, s)
-        : fast_logits               ? launch_vocab_ring_grad(a, bf16, grad.tile, s)
-                                    : tiles<GRAD>(a, bf16, grad.tile, s);
+    if (grad.tile == VOCAB_TILE_256) {
+      VocabArgs b = a;
+      int rest = 0;
+      b.vp = whole_rounds(a.T, a.vp, a.n, rest);
+      e = launch_vocab_pipe_grad(b, s);
+      if (e == hipSuccess && b.vp < a.vp) {
+        b.v0 = a.v0 + b.vp;
+        b.dS = static_cast<uint16_t*>(a.dS) + b.vp;
+        b.vp = a.vp - b.vp;
+        e = launch_vocab_ring_grad(b, bf16, rest, s);
+      }
+    } else {
+      e = fast_logits ? launch_vocab_ring_grad(a, bf16, grad.tile, s) : tiles<GRAD>(a, bf16, grad.tile, s);
+    }
     if (e != hipSuccess) return e;
     if (p.outer) {
       e = outer(a, p, s);

@@ -223,7 +223,7 @@ __device__ __forceinline__ void vocab_pipe(const VocabArgs& p, int block, int bl
   typedef f32x16 Acc;
   // m0, n0: where the tile lies; m1, n1: the first row and column that are its own
   auto stats = [&](Acc (&acc)[4][2], int m0, int n0, int m1, int n1) __attribute__((always_inline)) {
-    const int groups = tn * 4, group = n1 / 64 + (wave & 3);
+    const int group = n1 / 64 + (wave & 3);
     const bool whole = n0 == n1;
     float2 out[4];
 #pragma unroll
@@ -255,7 +255,7 @@ __device__ __forceinline__ void vocab_pipe(const VocabArgs& p, int block, int bl
       sum_ += __shfl_xor(sum_, 32);
       out[i] = float2{m, sum_};
       const long long at = target - (n0 + wn0) - 4 * half;
-      const bool mine = t >= m1 && target >= n1 && target < p.V && at >= 0 && at < 64 && (at & 4) == 0;
+      const bool mine = t >= m1 && target >= n1 && target < p.vp && at >= 0 && at < 64 && (at & 4) == 0;
       if (__any(mine)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -267,7 +267,7 @@ __device__ __forceinline__ void vocab_pipe(const VocabArgs& p, int block, int bl
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = m0 + wm0 + i * 32 + cm;
-      if (t >= m1 && half == 0) p.part[(long long)t * groups + group] = out[i];
+      if (t >= m1 && half == 0) p.part[(long long)t * p.groups + group] = out[i];
     }
   };
 

@@ -365,6 +365,7 @@ struct VocabArgs {
   // forward
   float* loss; float* lse_out;
   float2* part;                     // maximum and sum of exponentials, T x groups of columns
+  int groups, group0;               // (of all columns, and the first of this launch)
   float* zt;                        // T logits of the targets
   // backward
   const float* lse; const float* g; // T of each, or one g (g_each 0) that the results are multiplied by
@@ -388,6 +389,7 @@ struct VocabTiles {
 };
 struct VocabPlan {
   VocabTiles lay[3];   // rows of no whole 16 bytes, of whole ones, and with 256 x 256 tiles
+  int main, rest;      // columns of those tiles (all, or whole rounds of the CUs), and the others' tile
   int groups;
   long long rows;   // tokens of a launch
   size_t bytes;

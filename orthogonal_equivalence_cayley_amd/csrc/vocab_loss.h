@@ -102,7 +102,7 @@ __device__ __forceinline__ void epilogue(const VocabArgs& a, typename Ty::Acc (&
   // lane l holds row l & 15 of each tile and 4 of its columns, from 4 (l >> 4) on
   const int r0 = m0 + wm + (lane & 15), c0 = n0 + wn + 4 * (lane >> 4);
   if constexpr (MODE == STATS) {
-    const int groups = (a.V + BN / 2 - 1) / (BN / 2), group = (n0 + wn) / (BN / 2);
+    const int groups = (cols + BN / 2 - 1) / (BN / 2), group = (n0 + wn) / (BN / 2);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int t = r0 + i * 16;
@@ -111,7 +111,7 @@ __device__ __forceinline__ void epilogue(const VocabArgs& a, typename Ty::Acc (&
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          if (c0 + j * 16 + v < a.V) m = fmaxf(m, acc[i][j][v]);
+          if (c0 + j * 16 + v < cols) m = fmaxf(m, acc[i][j][v]);
       m = fmaxf(m, __shfl_xor(m, 16));
       m = fmaxf(m, __shfl_xor(m, 32));
       // all -inf: each term is exp(-inf), not exp(-inf + inf); a NaN stays one
@@ -120,17 +120,17 @@ __device__ __forceinline__ void epilogue(const VocabArgs& a, typename Ty::Acc (&
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          if (c0 + j * 16 + v < a.V) s += exp_of<F32>(acc[i][j][v] - base);
+          if (c0 + j * 16 + v < cols) s += exp_of<F32>(acc[i][j][v] - base);
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
       if (t >= rows || group >= groups) continue;
-      if (lane < 16) a.part[(long long)t * groups + group] = float2{m, s};
+      if (lane < 16) a.part[(long long)t * a.groups + a.group0 + group] = float2{m, s};
       const long long target = a.target[t];
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          if (c0 + j * 16 + v == target && target < a.V) a.zt[t] = acc[i][j][v];
+          if ((long long)a.v0 + c0 + j * 16 + v == target && c0 + j * 16 + v < cols) a.zt[t] = acc[i][j][v];
     }
   } else if constexpr (MODE == GRAD) {
 #pragma unroll

@@ -176,6 +176,25 @@ def test_both_gradients_of_few_tiles(T, n, V):
     assert (gx[:, n:] == 7).all() and (gw[:, n:] == 7).all()
 
 
+# a little more than whole rounds of 256 tiles: the last columns are a launch of their own, with targets at the seam
+@pytest.mark.parametrize("T, n, V, seam", [(2048, 64, 8448, 8192), (2500, 72, 6700, 6400), (4099, 128, 4400, 3840),
+                                           (2048, 256, 8300, 8192)])
+def test_columns_behind_whole_rounds(T, n, V, seam):
+    import torch
+    log(f"cross entropy, columns behind whole rounds T={T} n={n} V={V}")
+    X, W, target, g = inputs(T, n, V, "bf16", seed=5)
+    target[:8] = torch.tensor([0, seam - 1, seam, seam + 1, V - 1, IGNORE, seam - 257, seam + 63])
+    each = (torch.rand(T, generator=g) + 0.1).cuda()
+    Xc, Wc, tc = X.cuda(), W.cuda(), target.cuda()
+    a = run(Xc, Wc, tc, each)
+    compare(a, {k: (v.cpu(), e.cpu()) for k, (v, e) in reference(Xc, Wc, tc, each, "bf16").items()})
+    tc[3], tc[4] = V, -1   # outside: a loss of their own, and the gradients that they reach
+    b = run(Xc, Wc, tc, each)
+    assert b["loss"][3:5].isnan().all() and not b["loss"][5:].isnan().any()
+    assert torch.equal(b["lse"], a["lse"]) and torch.equal(b["loss"][5:], a["loss"][5:])
+    assert b["G_X"][3:5].isnan().all() and b["G_W"].isnan().all() and torch.equal(b["G_X"][5:], a["G_X"][5:])
+
+
 def run_back(X, W, target, lse, g, **kw):
     import orthogonal_equivalence_cayley_amd as oec
     return oec.linear_cross_entropy_backward(g.cuda(), X, W, target, lse, ignore_index=IGNORE, **kw)

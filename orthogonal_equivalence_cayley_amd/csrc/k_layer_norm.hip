@@ -55,11 +55,22 @@ __device__ __forceinline__ Two<V> row_sums(Two<V> v, Two<V>* red) {
 
 // Mean and variance come from one pass, sums of h - c and its square in 64 bits: their
 // order then does not show in the fp32 results, so the INT8 decisions are the same for
-// every split of a row over lanes. c is a value of the row's own size (its first x + r; any
-// finite number would do), so that a row far from zero keeps its variance.
-__device__ __forceinline__ double center(float x, float r) {
-  const float c = x + r;
-  return fabsf(c) < __builtin_inff() ? (double)c : 0.0;
+// every split of a row over lanes. c is the row's own h_0, behind dropout and the residual:
+// what the squares cancel by is then (h_0 - mean)^2 over the variance, the row's length at
+// most, and a row far from zero keeps its variance. (A value that is not of the row would
+// not do: at 1e7 deviations off it costs 1 % of the result, at 1e9 all of it.)
+__device__ __forceinline__ double center(float h0) { return fabsf(h0) < __builtin_inff() ? (double)h0 : 0.0; }
+// h_0 of row `row` from its parts, where several waves share the row (its only wave takes it
+// from its first lane: 16384 x 300 bf16 with dropout 21.7 us, 23.0 from the parts). The row is
+// the wave's, so the generator runs on the scalar unit.
+template <typename E, bool DROP>
+__device__ __forceinline__ float first_h(const DropArgs& d, drop::Key k, uint32_t row, E x0, bool res, E r0) {
+  float h[1] = {to_f(x0)};
+  if constexpr (DROP) {
+    const drop::Bits b = drop::bits(k, 0, __builtin_amdgcn_readfirstlane(row), d.site);
+    drop::apply(d, b.of(0) >= d.threshold ? 1u : 0u, h);
+  }
+  return to_f(from_f<E>(res ? h[0] + to_f(r0) : h[0]));
 }
 struct Stats {
   float m0, m1;   // the mean as two floats: a row far from zero keeps the digits of h - m
@@ -100,19 +111,20 @@ __global__ __launch_bounds__(threads(WPR)) void add_layer_norm_kernel(LayerNormA
   }
   [[maybe_unused]] drop::Key key{};
   if constexpr (DROP) key = drop::key_of(a.drop);
-  E xr[NV][N] = {}, rr[NV][N] = {}, x0 = E(0), r0 = E(0);
+  E xr[NV][N] = {}, rr[NV][N] = {};
+  [[maybe_unused]] E x0 = E(0), r0 = E(0);   // the row's first, for every wave of it
   auto fetch = [&](long long t) {
     const E* x = static_cast<const E*>(a.X) + t * a.ldx;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (c0 + i * STEP < a.dim) load_raw<WHOLE>(x + c0 + i * STEP, a.dim - c0 - i * STEP, full, xr[i]);
-    x0 = *x;
+    if constexpr (WPR > 1) x0 = *x;
     if (a.R) {
       const E* r = static_cast<const E*>(a.R) + t * a.ldr;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (c0 + i * STEP < a.dim) load_raw<WHOLE>(r + c0 + i * STEP, a.dim - c0 - i * STEP, full, rr[i]);
-      r0 = *r;
+      if constexpr (WPR > 1) r0 = *r;
     }
   };
   const long long stride = (long long)gridDim.x * RPW;
@@ -121,7 +133,8 @@ __global__ __launch_bounds__(threads(WPR)) void add_layer_norm_kernel(LayerNormA
   for (; t < a.T; t += stride) {   // whole rows: with more waves to a row the workgroup has one
     float h[NV][N];
     Two<double> sum{0.0, 0.0};
-    const double c = center(to_f(x0), to_f(r0));
+    double c = 0.0;
+    if constexpr (WPR > 1) c = center(first_h<E, DROP>(a.drop, key, a.row0 + (uint32_t)t, x0, a.R != nullptr, r0));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int left = a.dim - c0 - i * STEP;
@@ -132,6 +145,9 @@ __global__ __launch_bounds__(threads(WPR)) void add_layer_norm_kernel(LayerNormA
       for (int e = 0; e < N; ++e) {
         // rounded to the type before the norm: the kept h is what the norm sees
         if (a.R || DROP) h[i][e] = to_f(from_f<E>(a.R ? h[i][e] + to_f(rr[i][e]) : h[i][e]));
+        if constexpr (WPR == 1) {
+          if (i == 0 && e == 0) c = center(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(h[0][0]))));
+        }
         const double d = (WHOLE ? left > 0 : e < left) ? (double)h[i][e] - c : 0.0;
         sum.a += d;
         sum.b += d * d;
@@ -211,7 +227,7 @@ __global__ __launch_bounds__(kLongWaves * 64) void add_layer_norm_long_kernel(La
     for (int e = 0; e < N; ++e) h[e] = to_f(from_f<E>(h[e]));
   };
   Two<double> sum{0.0, 0.0};
-  const double mid = center(to_f(x[0]), r ? to_f(r[0]) : 0.0f);
+  const double mid = center(first_h<E, DROP>(a.drop, key, a.row0 + (uint32_t)t, x[0], r != nullptr, r ? r[0] : E(0)));
   __syncthreads();   // H may lie over the first x or r
   for (int c = first; c < a.dim; c += STEP) {
     float h[N];

@@ -429,8 +429,11 @@ __global__ __launch_bounds__(threads(WPR)) void layer_norm_backward_kernel(Layer
   }
 }
 
-// Rows too long for registers: first both means of every row, then tiles of 256 vectors
-// of columns by a range of rows.
+// Rows too long for registers: first both means of every row, then tiles of 256 vectors of
+// columns by a range of rows. A row has up to 2^24 terms, 2^14 to a thread, and in one fp32
+// number what their additions round alike would add up: a thread sums in fp32 within a vector
+// and in 64 bits from there. The 1024 threads' sums are joined in fp32 (in 64 bits the kernel
+// takes more registers than two workgroups on a CU have: 4096 x 8192 fp32 178 us, so 161).
 template <typename E>
 __global__ __launch_bounds__(kLongWaves * 64) void layer_norm_means_kernel(LayerNormBackArgs a) {
   constexpr int N = 16 / sizeof(E);
@@ -439,21 +442,24 @@ __global__ __launch_bounds__(kLongWaves * 64) void layer_norm_means_kernel(Layer
     const E* g = static_cast<const E*>(a.G) + t * a.ldg;
     const E* h = static_cast<const E*>(a.H) + t * a.ldh;
     const float m = a.mean[t], s = a.rstd[t];
-    Two<float> dot{0.0f, 0.0f};
+    Two<double> sum{0.0, 0.0};
     for (int c = (int)threadIdx.x * N; c < a.dim; c += kLongWaves * 64 * N) {
       E gv[N], hv[N];
       float w[N];
       load_raw<false>(g + c, a.dim - c, true, gv);
       load_raw<false>(h + c, a.dim - c, true, hv);
       load_raw<false>(a.w + c, a.dim - c, true, w);
+      float da = 0.0f, db = 0.0f;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const float gw = to_f(gv[e]) * w[e];
-        dot.a += gw;
-        dot.b += e < a.dim - c ? gw * ((to_f(hv[e]) - m) * s) : 0.0f;
+        da += gw;
+        db += e < a.dim - c ? gw * ((to_f(hv[e]) - m) * s) : 0.0f;
       }
+      sum.a += (double)da;
+      sum.b += (double)db;
     }
-    dot = row_sums<kLongWaves>(dot, red);
+    const Two<float> dot = row_sums<kLongWaves>(Two<float>{(float)sum.a, (float)sum.b}, red);
     if (threadIdx.x == 0) {
       a.rowc[2 * t] = dot.a / (float)a.dim;
       a.rowc[2 * t + 1] = dot.b / (float)a.dim;

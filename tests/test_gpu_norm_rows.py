@@ -7,7 +7,7 @@ import pytest
 
 from gpu_util import device_ready, log
 from test_gpu_block_ops import HALF, T_, U, close, gen, rand
-from test_gpu_train_ops import SEED, factor, norm_ref
+from test_gpu_train_ops import SEED, back_ref, factor, norm_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +72,29 @@ def test_a_first_value_that_the_residual_cancels(T, dim, dt):
     close("rstd", o.rstd, s, 2 * U * s)
     close("mean", o.mean, m, U * m.abs() + 1e-15)
     close("Y", o.Y, y, HALF[dt] * y.abs() + U * y.abs() + 6 * U * mag + 2.0 ** -46 * (m.abs() * s)[:, None] * w.cpu().abs())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_backward_of_the_longest_sums(dt):
+    """A row of 2^22 columns whose g w is the same everywhere: a sum in one fp32 number would lose what
+    its every addition rounds alike."""
+    import torch
+    import orthogonal_equivalence_cayley_amd as oec
+    log(f"layer norm backward of 2^22 columns {dt}")
+    T, dim = 2, 2 ** 22
+    g = gen(5)
+    x = rand(g, T, dim, dtype=dt)
+    gy = torch.full((T, dim), 0.3, dtype=T_(dt))
+    w = torch.ones(dim)
+    f = oec.add_layer_norm(x.cuda(), w.cuda(), eps=1e-5, save=True)
+    m, s, _, _ = norm_ref(x, w, None, 1e-5)
+    # the gradient of a sum: zero but for the roundings of g w - mean(g w) - u mean(g w u), the two means one each
+    dh, mag, sums, gw, gwm, gb, gbm = back_ref(gy, None, x, w, m, s)
+    o = oec.add_layer_norm_backward(gy.cuda(), x.cuda(), w.cuda(), f.mean, f.rstd)
+    u = ((x.double() - m[:, None]) * s[:, None]).abs()
+    eu = (U * m.abs() * s)[:, None]
+    cb = gy.double().abs() * (6 * U * u + eu)              # a term's, and so the mean's, error
+    tol = HALF[dt] * dh.abs() + 9 * U * mag + s[:, None] * (eu * gy.double().abs().mean() + u * cb.mean(1, keepdim=True))
+    close("G_X", o.G_X, dh, tol)
+    close("g_w", o.g_weight, gw, 9 * U * gwm + (gy.double().abs() * eu).sum(0))
+    close("g_b", o.g_bias, gb, 2 * U * gbm)

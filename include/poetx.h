@@ -477,7 +477,9 @@ poetx_status poetx_add_layer_norm(const poetx_layer_norm_desc* desc, const void*
                                   void* stream);
 
 /* Backward of poetx_add_layer_norm (y_dtype = dtype, the same rule) from G = dL/dY and
- * G_H, the gradient that reaches h through the residual stream: u = (h - m) s,
+ * G_H, the gradient that reaches h through the residual stream: u = (h - m) s, m and s
+ * those of h (where |m| s > 16, the mean of h - m is taken off once more, for what m lost
+ * as one float),
  *   dr = round(dh),  dh = gh + s (g w - mean_j(g w) - u mean_j(g w u)),
  *   dx = round(drop(dh)),  g_w[j] = sum_t g_tj u_tj,  g_b[j] = sum_t g_tj (overwritten)
  *   G [T, dim]    G_H [T, dim] or NULL    H [T, dim]: h (X where it is x itself)

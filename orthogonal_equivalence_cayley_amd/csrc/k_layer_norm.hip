@@ -299,6 +299,12 @@ __device__ __forceinline__ void part_rows(const LayerNormBackArgs& a, int block,
   pb = a.part ? pw + a.dim : a.db;
 }
 
+// The backward is handed the mean as one float. Its rounding puts u = (h - m) s off by up to
+// 2^-24 |m| s in a whole row, which shows in rows far from zero; there, from 16 deviations on
+// (2^-20 of u), h - m is exact and its own mean is what the rounding lost: taken once more, by
+// the few rows that need it.
+__device__ __forceinline__ bool far_mean(float m, float s) { return fabsf(m) * s > 16.0f; }
+
 // Backward: each wave (WPR = 1) or workgroup (WPR = 4, 8) takes rows a stride apart and
 // keeps its columns' parts of dw and db in registers, in 64 bits (sums over any number
 // of rows: fp32 would lose small terms behind large ones); the parts of a workgroup's
@@ -309,6 +315,7 @@ __global__ __launch_bounds__(threads(WPR)) void layer_norm_backward_kernel(Layer
   constexpr int RPW = threads(WPR) / 64 / WPR;
   constexpr int STEP = 64 * WPR * N;
   __shared__ Two<float> red[WPR];
+  __shared__ double redm[WPR];
   extern __shared__ double lds[];   // WPR = 1: 2 dim values
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int c0 = ((wave % WPR) * 64 + lane) * N;
@@ -354,16 +361,36 @@ __global__ __launch_bounds__(threads(WPR)) void layer_norm_backward_kernel(Layer
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const bool in = WHOLE ? left > 0 : e < left;
-        gv[i][e] = to_f(gr[i][e]);
+        gv[i][e] = to_f(gr[i][e]) * w[i][e];
         u[i][e] = in ? (to_f(hr[i][e]) - m) * s : 0.0f;
         q[i][e] = to_f(qr[i][e]);
-        dw[i][e] += (double)(gv[i][e] * u[i][e]);
-        db[i][e] += (double)gv[i][e];
-        gv[i][e] *= w[i][e];
         dot.a += gv[i][e];
         dot.b += gv[i][e] * u[i][e];
       }
     }
+    if (far_mean(m, s)) {   // the same for every wave of the row
+      double rest = 0.0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) rest += c0 + i * STEP + e < a.dim ? (double)(to_f(hr[i][e]) - m) : 0.0;
+      const float m1 = (float)(row_reduce<WPR>(rest, redm, Add{}) / (double)a.dim);
+      dot.b = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          u[i][e] = c0 + i * STEP + e < a.dim ? ((to_f(hr[i][e]) - m) - m1) * s : 0.0f;
+          dot.b += gv[i][e] * u[i][e];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        dw[i][e] += (double)(to_f(gr[i][e]) * u[i][e]);
+        db[i][e] += (double)to_f(gr[i][e]);
+      }
     if (t + stride < a.T) fetch(t + stride);
     // the generator runs while waves wait for each other (a wave of its own waits for none:
     // 8000 x 768 bf16 30 us with it here, 23 behind the sums)
@@ -438,6 +465,7 @@ template <typename E>
 __global__ __launch_bounds__(kLongWaves * 64) void layer_norm_means_kernel(LayerNormBackArgs a) {
   constexpr int N = 16 / sizeof(E);
   __shared__ Two<float> red[kLongWaves];
+  __shared__ double redm[kLongWaves];
   for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
     const E* g = static_cast<const E*>(a.G) + t * a.ldg;
     const E* h = static_cast<const E*>(a.H) + t * a.ldh;
@@ -459,10 +487,18 @@ __global__ __launch_bounds__(kLongWaves * 64) void layer_norm_means_kernel(Layer
       sum.a += (double)da;
       sum.b += (double)db;
     }
+    float m1 = 0.0f;
+    if (far_mean(m, s)) {
+      double rest = 0.0;
+      for (int c = threadIdx.x; c < a.dim; c += kLongWaves * 64) rest += (double)(to_f(h[c]) - m);
+      m1 = (float)(row_reduce<kLongWaves>(rest, redm, Add{}) / (double)a.dim);
+      sum.b -= (double)m1 * (double)s * sum.a;   // with u of the cols kernel
+    }
     const Two<float> dot = row_sums<kLongWaves>(Two<float>{(float)sum.a, (float)sum.b}, red);
     if (threadIdx.x == 0) {
-      a.rowc[2 * t] = dot.a / (float)a.dim;
-      a.rowc[2 * t + 1] = dot.b / (float)a.dim;
+      a.rowc[3 * t] = dot.a / (float)a.dim;
+      a.rowc[3 * t + 1] = dot.b / (float)a.dim;
+      a.rowc[3 * t + 2] = m1;
     }
   }
 }
@@ -493,11 +529,12 @@ __global__ __launch_bounds__(kThr) void layer_norm_cols_kernel(LayerNormBackArgs
     get(a.G, a.ldg, g);
     get(a.H, a.ldh, h);
     if (a.GH) get(a.GH, a.ldgh, q);
-    const float m = a.mean[t], s = a.rstd[t], ca = a.rowc[2 * t], cb = a.rowc[2 * t + 1];
+    const float m = a.mean[t], s = a.rstd[t];
+    const float ca = a.rowc[3 * t], cb = a.rowc[3 * t + 1], m1 = a.rowc[3 * t + 2];
     float o[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      const float gv = to_f(g[e]), u = (to_f(h[e]) - m) * s;
+      const float gv = to_f(g[e]), u = ((to_f(h[e]) - m) - m1) * s;
       dw[e] += (double)(gv * u);
       db[e] += (double)gv;
       o[e] = s * (gv * w[e] - ca - u * cb) + to_f(q[e]);

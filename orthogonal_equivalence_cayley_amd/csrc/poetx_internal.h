@@ -296,7 +296,7 @@ struct LayerNormBackArgs {
   void* GX; void* GR;      // GR (with dropout) may be null
   float* dw; float* db;
   float* part;             // layer_norm_backward_parts x 2 dim partial sums
-  float* rowc;             // 2 T values, for rows past layer_norm_back_reg_dim only
+  float* rowc;             // 3 T values, for rows past layer_norm_back_reg_dim only
   long long T; int dim;
   long long ldg, ldgh, ldh, ldgx, ldgr;
   DropArgs drop;

@@ -92,8 +92,8 @@ poetx_status poetx_add_layer_norm(const poetx_layer_norm_desc* d, const void* X,
 
 size_t poetx_layer_norm_backward_workspace(int64_t T, int32_t dim) {
   if (T < 0 || T > kMaxRows || dim < 1 || dim > poetx::kNormMaxDim) return 0;
-  // partial sums of g_w and g_b, then two values per row for rows that no workgroup holds
-  const size_t rows = dim > poetx::layer_norm_back_reg_dim(0) ? (size_t)T * 8 : 0;
+  // partial sums of g_w and g_b, then three values per row for rows that no workgroup holds
+  const size_t rows = dim > poetx::layer_norm_back_reg_dim(0) ? (size_t)T * 12 : 0;
   return ((size_t)poetx::layer_norm_backward_parts(T) * dim * 8 + rows + 255) / 256 * 256 + 256;
 }
 

@@ -48,7 +48,21 @@ constexpr int kSteps = kKB / 32;
 constexpr int kLoads = kTile / 32;         // loads of a lane per operand tile, 4 KB of it each
 constexpr int kGroupRows = 4;              // tile-rows per group of the XCD-aware order
 
-constexpr float kLog2E = 1.44269504088896340736f;
+// exp(z - m) = 2^(z k - base) corr over the z of a row, one rounding of the exponent: k =
+// log2 e, base = m k rounded, and corr = 2^(base - m k) gives back what that lost (2^-12 of the
+// exponent, 2e-4 of every term, at m = 4000). Past 2^120, where m k would overflow, two z that
+// differ differ by 2^96 and more, so any k will do, and m / 2 is exact.
+struct Base {
+  float k, base, lost;   // lost: m k - base
+};
+__device__ __forceinline__ Base base_of(float m) {
+  Base b;
+  const bool far = fabsf(m) > 0x1p120f;   // infinities too
+  b.k = far ? 0.5f : 1.44269504088896340736f;
+  b.base = m * b.k;
+  b.lost = far ? 0.0f : fmaf(m, b.k, -b.base);
+  return b;
+}
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __bf16 a = static_cast<__bf16>(lo), b = static_cast<__bf16>(hi);
@@ -245,13 +259,13 @@ __device__ __forceinline__ void vocab_pipe(const VocabArgs& p, int block, int bl
         for (int v = 0; v < 16; ++v) m = fmaxf(m, acc[i][j][v]);
       m = fmaxf(m, __shfl_xor(m, 32));
       // all -inf: each term is exp(-inf), not exp(-inf + inf); a NaN stays one
-      const float base = m == -__builtin_inff() ? 0.0f : m * kLog2E;
+      const Base b = base_of(m == -__builtin_inff() ? 0.0f : m);
       float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) s[v & 3] += __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2E, -base));
-      float sum_ = (s[0] + s[1]) + (s[2] + s[3]);
+        for (int v = 0; v < 16; ++v) s[v & 3] += __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], b.k, -b.base));
+      float sum_ = ((s[0] + s[1]) + (s[2] + s[3])) * __builtin_amdgcn_exp2f(-b.lost);
       sum_ += __shfl_xor(sum_, 32);
       out[i] = float2{m, sum_};
       const long long at = target - (n0 + wn0) - 4 * half;
@@ -296,7 +310,9 @@ __device__ __forceinline__ void vocab_pipe(const VocabArgs& p, int block, int bl
     for (int i = 0; i < 4; ++i) {
       const int t = m0 + wm0 + i * 32 + cm;
       const Row r = token_of(p, t);
-      const float base = r.lse * kLog2E;
+      // (p - 1) g = (2^(z k - base) - 1 / corr) (corr g)
+      const Base b = base_of(r.lse);
+      const float one = __builtin_amdgcn_exp2f(b.lost), factor = __builtin_amdgcn_exp2f(-b.lost) * r.factor;
       const uint32_t keep = r.target < 0 && r.factor == 0.0f ? 0u : ~0u;   // an ignored row is zero whatever its logits are
       const long long at = r.target - p.v0 - (n0 + wn0) - 8 * half;
       const bool any = __any(at >= 0 && at < 64);
@@ -305,15 +321,15 @@ __device__ __forceinline__ void vocab_pipe(const VocabArgs& p, int block, int bl
         float v[8];
         eight(acc, i, q, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_exp2f(fmaf(v[e], kLog2E, -base));
+        for (int e = 0; e < 8; ++e) v[e] = __builtin_amdgcn_exp2f(fmaf(v[e], b.k, -b.base));
         if (any) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (at == q * 16 + e) v[e] -= 1.0f;
+            if (at == q * 16 + e) v[e] -= one;
         }
         u32x4 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = pack2(v[2 * e] * r.factor, v[2 * e + 1] * r.factor) & keep;
+        for (int e = 0; e < 4; ++e) o[e] = pack2(v[2 * e] * factor, v[2 * e + 1] * factor) & keep;
         const int c = column(n0, q);
         if (t >= m1 && c + 8 > n1) store8(static_cast<uint16_t*>(p.dS) + t * p.ldp + c, o, n1 - c, 8);
         __builtin_amdgcn_sched_barrier(0);   // one group at a time: registers

@@ -566,7 +566,7 @@ poetx_status poetx_linear_cross_entropy(const poetx_cross_entropy_desc* desc, co
  *   G_X [T, n], G_W [V, n] (dtype); either may be NULL
  *   ws poetx_linear_cross_entropy_backward_workspace(desc, need_x, need_w) bytes
  * POETX_BF16: d is rounded to bf16 before the products that take it, without the factor
- * g where it is one for all; up to 64 tokens they take what it lost, too. Products are
+ * g where it is one finite number for all; up to 64 tokens they take what it lost, too. Products are
  * summed in fp32. A token whose target is neither in the vocabulary nor ignored makes its
  * row of G_X and all of G_W NaN. What an ignored token's x holds reaches no gradient. Deterministic. T = 0 writes zero G_W. */
 size_t poetx_linear_cross_entropy_backward_workspace(const poetx_cross_entropy_desc* desc, int32_t need_x,

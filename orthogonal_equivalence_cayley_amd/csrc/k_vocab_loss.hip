@@ -407,7 +407,7 @@ template <bool F32, int G>
 __global__ __launch_bounds__(kThr) void vocab_finish_kernel(VocabArgs a) {
   __shared__ float4 red[G][kThr / G];
   const int quads = (a.n + 3) / 4, lane = threadIdx.x % (kThr / G), grp = threadIdx.x / (kThr / G);
-  const float scale = a.g_each ? 1.0f : *a.g;
+  const float scale = scale_of(a);
   const long long count = a.T * quads;
   const int halves = a.Td > a.T ? 2 : 1, parts = a.splits * halves;
   for (long long i0 = (long long)blockIdx.x * (kThr / G); i0 < count; i0 += (long long)gridDim.x * (kThr / G)) {
@@ -470,7 +470,7 @@ __global__ __launch_bounds__(kThr) void vocab_outer_kernel(VocabArgs a, int per)
   const int c = ((int)blockIdx.x * kThr + (int)threadIdx.x) * N, left = a.n - c;
   const bool in = left > 0;
   const int first = (int)blockIdx.y * per, end = min(first + per, a.vp);
-  const float scale = a.g_each ? 1.0f : *a.g;
+  const float scale = scale_of(a);
   float x[TD][N] = {}, acc[TD][N] = {};
 #pragma unroll
   for (int t = 0; t < TD; ++t)

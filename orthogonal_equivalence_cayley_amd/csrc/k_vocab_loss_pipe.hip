@@ -336,7 +336,7 @@ __device__ __forceinline__ void vocab_pipe(const VocabArgs& p, int block, int bl
       }
     }
   };
-  const float scale = MODE == DX || MODE == DW ? (p.g_each ? 1.0f : *p.g) : 1.0f;
+  const float scale = MODE == DX || MODE == DW ? scale_of(p) : 1.0f;
   auto dx = [&](Acc (&acc)[4][2], int m0, int n0, int m1, int n1, int ti) __attribute__((always_inline)) {
     const bool first = p.v0 == 0, last = p.v0 + p.vp == p.V && p.splits == 1;
     float* const sums = p.acc + share(ti) * p.Td * p.lda;

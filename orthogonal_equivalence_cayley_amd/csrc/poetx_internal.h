@@ -368,7 +368,7 @@ struct VocabArgs {
   int groups, group0;               // (of all columns, and the first of this launch)
   float* zt;                        // T logits of the targets
   // backward
-  const float* lse; const float* g; // T of each, or one g (g_each 0) that the results are multiplied by
+  const float* lse; const float* g; // T of each, or one g (g_each 0)
   int g_each;
   void* GX; void* GW;               // each may be null
   long long ldgx, ldgw;

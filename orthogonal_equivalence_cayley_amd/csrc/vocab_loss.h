@@ -45,6 +45,12 @@ __device__ __forceinline__ float exp_of(float x) {
 
 enum Mode { STATS, GRAD, DX, DW };   // logits with their statistics or as dL/dz, d W, d^T X
 
+// One factor for all tokens is left out of d and multiplied into the results. Not so if it is no
+// finite number (the mean's 1 / count where no token counts): 0 times it would not be the 0 of
+// ignored tokens, so it goes into the d of the others.
+__device__ __forceinline__ bool behind_sums(const VocabArgs& a) { return !a.g_each && fabsf(*a.g) < __builtin_inff(); }
+__device__ __forceinline__ float scale_of(const VocabArgs& a) { return behind_sums(a) ? *a.g : 1.0f; }
+
 // What the backward needs of a row
 struct Row {
   float lse, factor;
@@ -55,9 +61,9 @@ __device__ __forceinline__ Row token_of(const VocabArgs& a, long long t) {
   if (target == a.ignore) return Row{0.0f, 0.0f, -1};
   // a target outside the vocabulary has no loss: its gradients are NaN
   const bool bad = target < 0 || target >= a.V;
-  return Row{a.lse[t], bad ? __builtin_nanf("") : a.g_each ? a.g[t] : 1.0f, target};
+  return Row{a.lse[t], bad ? __builtin_nanf("") : a.g_each ? a.g[t] : behind_sums(a) ? 1.0f : *a.g, target};
 }
-// dL/dz of column v, but for a factor that all rows share (a.g without g_each)
+// dL/dz of column v, but for a factor behind the sums
 template <bool F32>
 __device__ __forceinline__ float grad_of(const Row& r, float z, long long v) {
   // an ignored row is zero whatever its logits are
@@ -154,7 +160,7 @@ __device__ __forceinline__ void epilogue(const VocabArgs& a, typename Ty::Acc (&
       }
     }
   } else {
-    const float scale = a.g_each ? 1.0f : *a.g;
+    const float scale = scale_of(a);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int t = r0 + i * 16;

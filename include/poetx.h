@@ -542,7 +542,8 @@ poetx_status poetx_linear(const poetx_linear_desc* desc, const void* X, const vo
  *   X [T, n], W [V, n] (dtype)    target device int64 [T]
  *   loss, lse fp32 [T]: a target equal to ignore_index has loss 0; another one outside
  *     0 .. V - 1 has loss NaN.
- *   ws poetx_linear_cross_entropy_workspace(desc) bytes
+ *   ws poetx_linear_cross_entropy_workspace(desc) bytes: 8 for every 32 or 64 columns of
+ *     a token, up to 256 MB or, where that is more, those of 256 tokens (64 V); and 4 T
  * Logits are sums in fp32. T = 0 is a no-op. No row is touched behind the T-th. T, V <=
  * 2^24, n <= 2^16, T n, V n <= 2^36 (POETX_ERR_SHAPE), also in the backward. ld_gx, ld_gw
  * and g_count are the backward's. */
@@ -564,11 +565,17 @@ poetx_status poetx_linear_cross_entropy(const poetx_cross_entropy_desc* desc, co
  *   G_X = round(d W),  G_W = round(d^T X) (overwritten).
  *   g fp32 [g_count]: one for each token, or one for all    lse of the forward
  *   G_X [T, n], G_W [V, n] (dtype); either may be NULL
- *   ws poetx_linear_cross_entropy_backward_workspace(desc, need_x, need_w) bytes
+ *   ws poetx_linear_cross_entropy_backward_workspace(desc, need_x, need_w) bytes: dL/dz of
+ *     a piece, up to 256 MB or, where that is more, of 256 columns; with need_w a copy of
+ *     X; with need_x sums of G_X in fp32, 4 T n or, in shares of few tokens, up to 64 MB
  * POETX_BF16: d is rounded to bf16 before the products that take it, without the factor
- * g where it is one finite number for all; up to 64 tokens they take what it lost, too. Products are
- * summed in fp32. A token whose target is neither in the vocabulary nor ignored makes its
- * row of G_X and all of G_W NaN. What an ignored token's x holds reaches no gradient. Deterministic. T = 0 writes zero G_W. */
+ * g where it is one finite number for all; up to 64 tokens they take what it lost, too.
+ * (G_X and G_W are off by about 0.0017 of their 2-norm, what rounding them costs; past 64
+ * tokens with a g for each by 0.0024.) Products are summed in fp32; exp(z - lse) is off by
+ * lse's rounding, 2^-24 |lse|. A token whose target is neither in the vocabulary nor
+ * ignored makes its row of G_X and all of G_W NaN. What an ignored token's x holds reaches
+ * no gradient, and neither does a g that is not finite by way of it. Deterministic. T = 0
+ * writes zero G_W. */
 size_t poetx_linear_cross_entropy_backward_workspace(const poetx_cross_entropy_desc* desc, int32_t need_x,
                                                      int32_t need_w);
 poetx_status poetx_linear_cross_entropy_backward(const poetx_cross_entropy_desc* desc, const float* g, const void* X,

@@ -10,8 +10,9 @@
 // Bound by memory: 8 bytes a bf16 element forward (x, r, h, y), 8 backward (g, gh, h,
 // dx) and 10 with dropout, whose dx is not dr. A row is read once and stays in
 // registers; one wave, four or sixteen to a row, every load of a row and of the next one
-// out before the first is used. 16384 x 2048 bf16: forward 45 us, with dropout 47 (6.0 and
-// 5.8 TB/s), backward 50, with dropout 67 (5.4 and 5.0 TB/s).
+// out before the first is used. 16384 x 2048 bf16, call after call: forward 45 us, with dropout
+// 48 (5.9 and 5.5 TB/s; with the statistics kept and under the profiler 57 to 61), backward 51,
+// with dropout 65 (5.2 and 5.1 TB/s; 73).
 #include <algorithm>
 #include <type_traits>
 

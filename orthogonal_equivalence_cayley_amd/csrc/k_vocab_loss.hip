@@ -459,7 +459,7 @@ hipError_t finish(const VocabArgs& a, hipStream_t s) {
 // d W and d^T X of the fewest fp32 tokens, at most TD, in one pass over W: a thread has 4
 // columns of X in registers and goes down `per` rows of W, whose d are the same for all of its
 // workgroup's; each chunk of rows leaves its part of dX. Bound by memory, W read and dW written
-// (8 x 1024 x 32000 52 us, 5.0 TB/s; in tiles 98; rows of no whole 16 bytes 142 against 299).
+// (8 x 1024 x 32000 52 us by the profiler, 5.0 TB/s, 45 call after call; in tiles 98; rows of no whole 16 bytes 142 against 299).
 // Not for bf16, whose d come in two halves, and for twice as many columns a thread: 4 x 2048 x
 // 32000 134 us against 57 in tiles.
 template <int TD>
@@ -668,10 +668,14 @@ int groups_of(const VocabPlan& p, int tile, int V) {
 }
 
 // Up to this many tokens in bf16 the products take what d loses in rounding too, as rows of
-// their own: few d of a size share a result there, so that the rounding of one (a target's,
-// up to 2^-9 of it) shows as an error of whole rows of dX and dW, two and a half times what
-// rounding them does; more tokens, and the errors are as many as the results'. The memory
-// traffic, which bounds these sizes, hardly grows (64 x 2048 x 32000 backward 124 -> 131 us).
+// their own. It shows where tokens have factors of their own: a target's d, about -g, rounds by
+// up to half a step, and a row of dX and one of dW with it. Both are off by 0.0024 of their
+// 2-norm then, and by 0.0017 with the second rows, as rounding the results alone costs. (One
+// factor is left out of d, whose targets are -1 or near it: 0.0017 at any size.) Why not past
+// 64: to there memory bounds the products, and its traffic hardly grows (64 x 2048 x 32000
+// backward 124 -> 131 us); from some hundred tokens on the matrix units do, and two of the
+// three products would double. Nor can g go behind the sums of dX: dW takes the same d and
+// would have to round g x instead, a third rounding of its terms.
 constexpr long long kHalves = 64;
 
 // Into how many shares the sum of d W goes where it and d^T X are one launch of 256 x 256

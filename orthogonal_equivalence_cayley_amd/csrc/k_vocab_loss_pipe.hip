@@ -17,7 +17,7 @@
 // Requirements (vocab_pipe_logits and the like): at least one tile of each axis, n a multiple
 // of 8, 16-byte rows of X and W.
 //
-// Bound by the matrix units at the clock that they leave (1.7 to 1.9 GHz), busy for 0.65 to
+// Bound by the matrix units at the clock that they leave (1.65 to 1.9 GHz), busy for 0.65 to
 // 0.79 of the time: 16384 x 2048 x 32000 STATS 1552 us (1380 TFLOP/s), and of 8192 columns GRAD
 // 438 (1255), DX 427 (1287), DW 412 (1334).
 #include <algorithm>

@@ -459,7 +459,7 @@ hipError_t finish(const VocabArgs& a, hipStream_t s) {
 // d W and d^T X of the fewest fp32 tokens, at most TD, in one pass over W: a thread has 4
 // columns of X in registers and goes down `per` rows of W, whose d are the same for all of its
 // workgroup's; each chunk of rows leaves its part of dX. Bound by memory, W read and dW written
-// (8 x 1024 x 32000 52 us by the profiler, 5.0 TB/s, 45 call after call; in tiles 98; rows of no whole 16 bytes 142 against 299).
+// (8 x 1024 x 32000 48 to 52 us, 5.0 TB/s; in tiles 98; rows of no whole 16 bytes 142 against 299).
 // Not for bf16, whose d come in two halves, and for twice as many columns a thread: 4 x 2048 x
 // 32000 134 us against 57 in tiles.
 template <int TD>
